@@ -10,10 +10,12 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
 
-ABI_VERSION = 7
+ABI_VERSION = 8
 CHUNK = 64
 FWD_STAGES = 3
 BWD_STAGES = 4
+TREE_MAX = 64    # GDR_TREE_MAX: nodes of a tree
+COPY_MAX = 4096  # GDR_COPY_MAX: entries of one gdr_copy_states
 
 OK, EINVAL, ENOTSUP, EWORKSPACE, ELAUNCH, ESCRATCH = 0, -1, -2, -3, -4, -5
 SCRATCH_BYTES = 256 << 20  # GDR_SCRATCH_BYTES: gdr_fwd_noalloc's per-device scratch
@@ -54,6 +56,29 @@ class BwdArgs(ctypes.Structure):
     ]
 
 
+class PoolArgs(ctypes.Structure):
+    """Mirror of gdr_pool_args."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("H_q", _i64), ("H_v", _i64), ("K", _i64), ("V", _i64),
+        ("n_seq", _i64), ("n_slots", _i64), ("slot_stride", _i64),
+        ("q_row", _i64), ("k_row", _i64), ("v_row", _i64),
+        ("q_batch", _i64), ("k_batch", _i64), ("v_batch", _i64),
+        ("dtype", _i32), ("out_dtype", _i32), ("scale", ctypes.c_float),
+        ("q", _p), ("k", _p), ("v", _p), ("g", _p), ("beta", _p), ("cu_seqlens", _p), ("slots", _p),
+        ("parents", _p), ("accepted", _p), ("states", _p), ("o", _p),
+    ]
+
+
+class CopyArgs(ctypes.Structure):
+    """Mirror of gdr_copy_args."""
+    _fields_ = [
+        ("n", _i64), ("n_dst", _i64), ("n_src", _i64), ("slot_bytes", _i64),
+        ("dst_stride", _i64), ("src_stride", _i64), ("layers", _i64),
+        ("dst_layer_stride", _i64), ("src_layer_stride", _i64),
+        ("dst", _p), ("src", _p), ("states", _p), ("source", _p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -75,6 +100,11 @@ def _load():
     lib.gdr_fwd_noalloc.argtypes = [ctypes.POINTER(FwdArgs), _p]
     lib.gdr_tblocks_bytes.restype = ctypes.c_int
     lib.gdr_tblocks_bytes.argtypes = [ctypes.POINTER(FwdArgs), ctypes.POINTER(ctypes.c_size_t)]
+    for name, st in (("gdr_step", PoolArgs), ("gdr_tree", PoolArgs), ("gdr_tree_accept", PoolArgs),
+                     ("gdr_copy_states", CopyArgs)):
+        f = getattr(lib, name)
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.POINTER(st), _p]
     if lib.gdr_abi_version() != ABI_VERSION:
         raise ImportError("libgdr ABI version %d, binding expects %d"
                           % (lib.gdr_abi_version(), ABI_VERSION))
@@ -139,3 +169,27 @@ def bwd(args, stream):
     rc = lib.gdr_bwd(ctypes.byref(args), _p(stream))
     if rc:
         raise GdrError("gdr_bwd", rc)
+
+
+def step(args, stream):
+    rc = lib.gdr_step(ctypes.byref(args), stream)
+    if rc:
+        raise GdrError("gdr_step", rc)
+
+
+def tree(args, stream):
+    rc = lib.gdr_tree(ctypes.byref(args), stream)
+    if rc:
+        raise GdrError("gdr_tree", rc)
+
+
+def tree_accept(args, stream):
+    rc = lib.gdr_tree_accept(ctypes.byref(args), stream)
+    if rc:
+        raise GdrError("gdr_tree_accept", rc)
+
+
+def copy_states(args, stream):
+    rc = lib.gdr_copy_states(ctypes.byref(args), stream)
+    if rc:
+        raise GdrError("gdr_copy_states", rc)

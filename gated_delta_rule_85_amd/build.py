@@ -37,7 +37,8 @@ MAX_ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 # serves it.
 SOURCES = {"gdr_api.hip": VGPR_FORM, "gdr_prep.hip": VGPR_FORM, "gdr_scan.hip": VGPR_FORM + ILP,
            "gdr_bwd.hip": VGPR_FORM, "gdr_bwd_scan.hip": VGPR_FORM,
-           "gdr_bwd_mfma.hip": VGPR_FORM + MAX_ILP, "gdr_noalloc.hip": []}
+           "gdr_bwd_mfma.hip": VGPR_FORM + MAX_ILP, "gdr_noalloc.hip": [],
+           "gdr_step.hip": [], "gdr_tree.hip": VGPR_FORM, "gdr_copy.hip": [], "gdr_pool_api.hip": []}
 
 
 def _compile(src):

@@ -1,0 +1,170 @@
+// gdr_step: the recurrent form of the gated delta rule, a token at a time on a
+// pool of states; gdr_tree_accept: the same over the tokens of an accepted path.
+//
+// Per (sequence, v head), with the state h (K x V, fp32):
+//     u = beta (v - e^g k h),   h <- e^g h + k u^T,   o = scale q h.
+// Columns of h are independent, and both products are taken of the old state:
+// q h_new = e^g q h + (q . k) u, so that one pass over the state's registers and
+// one sum over the lanes serve u and o together.
+//
+// A wave holds K rows x 32 columns of the state in registers over all of the
+// sequence's tokens: lane l has columns 4 (l & 7) .. + 3 of rows R (l >> 3) ..
+// + R - 1, R = K / 8, so that a load or store of the state is 8 rows x 128 bytes
+// and the rows of k and q that a lane needs are consecutive.  No LDS, no barriers.
+#include "gdr_pool.hpp"
+
+namespace gdr {
+namespace {
+
+// sum over the lanes l ^ 8, l ^ 16, l ^ 32 (the row groups), in every lane
+__device__ __forceinline__ float sum_row_groups(float x) {
+    x += dpp_mov<0x128>(x);  // row_ror:8
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+    return x;
+}
+
+// R consecutive inputs
+template <typename In, int R> struct Rows {
+    typename Vec16<In>::type x[R / Vec16<In>::n];
+    __device__ __forceinline__ void load(const In *p) {
+#pragma unroll
+        for (int i = 0; i < R / Vec16<In>::n; ++i)
+            x[i] = *reinterpret_cast<const typename Vec16<In>::type *>(p + i * Vec16<In>::n);
+    }
+    __device__ __forceinline__ float operator[](int r) const {
+        return to_f32(x[r / Vec16<In>::n][r % Vec16<In>::n]);
+    }
+};
+
+template <typename In, int R, bool OUT> struct Token {
+    Rows<In, R> k, q;
+    f32x4 v;
+    float g, beta;
+};
+
+template <typename In, typename Out, int K, bool ACCEPT>
+__global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
+    constexpr int R = K / 8;
+    const int item = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)));
+    const int n_vt = V >> 5, unit = item / n_vt, vt = item - unit * n_vt;
+    const int j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
+    if (j >= p.n_seq) return;
+    const int l = lane_id(), col = vt * 32 + 4 * (l & 7), row0 = R * (l >> 3);
+    int64_t bos, eos;
+    token_range(p, j, bos, eos);
+    if (bos >= eos) return;
+    const int slot = slot_of(p, j);
+    Out *o = reinterpret_cast<Out *>(p.o) + hv * V + col;
+    uint64_t path = 0;  // the accepted nodes
+    if constexpr (ACCEPT) {
+        if (slot < 0 || eos - bos > TREE_MAX) return;
+        const int n = (int)(eos - bos);
+        const int parent = l < n ? p.parents[bos + l] : -1;
+        int node = p.accepted[j];
+        if (node >= n) node = -1;
+        while (node >= 0) {  // a parent that is no earlier node counts as -1: at most n steps
+            path |= 1ull << node;
+            const int up = __builtin_amdgcn_readlane(parent, node);
+            node = up < node ? up : -1;
+        }
+        if (!path) return;
+    }
+    if (slot < 0 || slot_taken(p, j, slot)) {
+        if constexpr (!ACCEPT) {
+            if (l < 8)
+                for (int64_t i = bos; i < eos; ++i) store4(o + i * p.Hv * V, zero4());
+        }
+        return;
+    }
+
+    float *h0 = p.states + (int64_t)slot * p.slot_stride + ((int64_t)hv * K + row0) * V + col;
+    f32x4 h[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) h[r] = load4(h0 + r * V);
+
+    const In *kp = reinterpret_cast<const In *>(p.k) + hq * K + row0;
+    const In *qp = reinterpret_cast<const In *>(p.q) + hq * K + row0;
+    const In *vp = reinterpret_cast<const In *>(p.v) + hv * V + col;
+    Token<In, R, !ACCEPT> now, next;
+    auto fetch = [&](Token<In, R, !ACCEPT> &t, int64_t i) {
+        t.k.load(kp + row_offset(p, j, i, p.k_batch, p.k_row));
+        if constexpr (!ACCEPT) t.q.load(qp + row_offset(p, j, i, p.q_batch, p.q_row));
+        t.v = load4(vp + row_offset(p, j, i, p.v_batch, p.v_row));
+        t.g = p.g[i * p.Hv + hv];
+        t.beta = p.beta[i * p.Hv + hv];
+    };
+    auto step = [&](const Token<In, R, !ACCEPT> &t, int64_t i) {
+        f32x4 kh = zero4(), qh = zero4();
+        float qk = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            kh += t.k[r] * h[r];
+            if constexpr (!ACCEPT) {
+                qh += t.q[r] * h[r];
+                qk += t.q[r] * t.k[r];
+            }
+        }
+        // full-precision exponential: its error would otherwise grow with every token
+        const float eg = expf(t.g);
+        f32x4 u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) u[c] = t.beta * (t.v[c] - eg * sum_row_groups(kh[c]));
+#pragma unroll
+        for (int r = 0; r < R; ++r) h[r] = eg * h[r] + t.k[r] * u;
+        if constexpr (!ACCEPT) {
+            qk = sum_row_groups(qk);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) qh[c] = p.scale * (eg * sum_row_groups(qh[c]) + qk * u[c]);
+            if (l < 8) store4(o + i * p.Hv * V, qh);
+        }
+    };
+    if constexpr (ACCEPT) {
+        fetch(now, bos + __builtin_ctzll(path));
+        for (;;) {
+            const int64_t i = bos + __builtin_ctzll(path);
+            path &= path - 1;
+            if (path) fetch(next, bos + __builtin_ctzll(path));
+            step(now, i);
+            if (!path) break;
+            now = next;
+        }
+    } else {
+        fetch(now, bos);
+        for (int64_t i = bos;;) {
+            if (i + 1 < eos) fetch(next, i + 1);
+            step(now, i);
+            if (++i >= eos) break;
+            now = next;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) store4(h0 + r * V, h[r]);
+}
+
+template <typename In, typename Out, bool ACCEPT>
+hipError_t launch(int K, int V, const PoolParams &p, hipStream_t s) {
+    const int64_t waves = (int64_t)p.n_seq * p.Hv * (V / 32);
+    // a head's waves in one workgroup share its k and q rows in the L1
+    const int block = 64 * (V / 32);
+    const dim3 grid((uint32_t)(waves / (V / 32)));
+    if (K == 128)
+        launch_k(gdr_step_kernel<In, Out, 128, ACCEPT>, grid, dim3(block), 0, s, p, V);
+    else
+        launch_k(gdr_step_kernel<In, Out, 64, ACCEPT>, grid, dim3(block), 0, s, p, V);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s) {
+    if (dt == Dt::BF16)
+        return out == Dt::BF16 ? launch<bf16, bf16, false>(K, V, p, s) : launch<bf16, float, false>(K, V, p, s);
+    return out == Dt::BF16 ? launch<float, bf16, false>(K, V, p, s) : launch<float, float, false>(K, V, p, s);
+}
+
+hipError_t launch_accept(Dt dt, int K, int V, const PoolParams &p, hipStream_t s) {
+    return dt == Dt::BF16 ? launch<bf16, float, true>(K, V, p, s) : launch<float, float, true>(K, V, p, s);
+}
+
+}  // namespace gdr

@@ -1,0 +1,317 @@
+"""Serving operators of the gated delta rule on a pool of recurrent states.
+
+A serving program keeps one K x V state (fp32) per (sequence, v head) in a pool
+``states [n_slots, H_v, K, V]``, the layout of the chunked operator's initial and
+final states, and names a sequence's state by its slot:
+
+- :func:`recurrent_gated_delta_rule` takes every sequence's next token (or few
+  tokens) into its state, in place;
+- :func:`tree_gated_delta_rule` evaluates trees of drafted tokens against the
+  states, which stay as they are, and :func:`tree_gated_delta_rule_accept` takes the
+  accepted path into them;
+- :func:`copy_states` copies, forks, moves and clears states.
+
+They are inference operators: no gradients (the chunked operator has them), no
+workspace, no synchronisation, and all of them may be captured into a graph.
+``slots``, ``parents``, ``accepted`` and ``cu_seqlens`` are int32.  On the host
+they are checked here; on the device the library clamps or skips what is out of
+range (reading them here would synchronise the stream).
+"""
+import torch
+
+from . import _lib
+from .api import _DT, _c, check_offsets
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _refuse_gradients(*tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()")
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one GPU")
+
+
+def _rows(x):
+    """x with the strides of its tokens and batch rows in elements, copied if the
+    kernels cannot read it in place: they need one token's [H, D] contiguous and
+    rows at multiples of 16 bytes."""
+    B, T, H, D = x.shape
+    batch, row, head, one = x.stride()
+    per16 = 16 // x.element_size()
+    if B < 2:
+        batch = 0
+    if T < 2:
+        row = 0
+    if one != 1 or (head != D and H > 1) or batch % per16 or row % per16 or x.data_ptr() % 16:
+        x = x.contiguous()
+        batch, row = T * H * D, H * D
+    return x, row, batch
+
+
+def _check_tokens(q, k, v, g, beta, cu_seqlens):
+    if k.dim() != 4 or v.dim() != 4 or v.shape[:2] != k.shape[:2] or (q is not None and q.shape != k.shape):
+        raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
+    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k, v must share one dtype, bfloat16 or float32")
+    if g.shape != v.shape[:3] or beta.shape != v.shape[:3]:
+        raise ValueError("g and beta must be [B,T,H_v]")
+    if cu_seqlens is not None:
+        if k.shape[0] != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be int32 [N+1] with B == 1")
+        if not cu_seqlens.is_cuda:
+            check_offsets(cu_seqlens, k.shape[1])
+
+
+def _check_states(states, H_v, K, V, name="states"):
+    if states.dim() != 4 or states.dtype != torch.float32 or (H_v is not None and states.shape[1:] != (H_v, K, V)):
+        raise ValueError("%s must be float32 [n_slots,H_v,K,V]" % name)
+    n, H, K, V = states.shape
+    slot, head, row, one = states.stride()
+    if n < 1 or one != 1 or row != V or (head != K * V and H > 1) or states.data_ptr() % 16 or \
+            (n > 1 and (slot % 4 or slot < H * K * V)):
+        raise ValueError("a slot of %s must be contiguous and 16-byte aligned" % name)
+
+
+def _indices(x, n, what, lo, hi):
+    """An int32 index array of n entries; on the host its range is checked."""
+    if x.dtype != torch.int32 or x.dim() != 1 or x.numel() != n:
+        raise ValueError("%s must be int32 [%d]" % (what, n))
+    if not x.is_cuda and n and (int(x.min()) < lo or int(x.max()) >= hi):
+        raise ValueError("%s out of range [%d, %d)" % (what, lo, hi))
+    return x
+
+
+def _check_slots(slots, n_seq, n_slots):
+    if slots is None:
+        if n_slots < n_seq:
+            raise ValueError("states has %d slots for %d sequences" % (n_slots, n_seq))
+        return
+    _indices(slots, n_seq, "slots", -1, n_slots)
+
+
+def _check_distinct(slots):
+    if slots is not None and not slots.is_cuda:
+        used = slots[slots >= 0]
+        if used.unique().numel() != used.numel():
+            raise ValueError("slots names a slot twice")
+
+
+def _check_parents(parents, B, T, cu_seqlens):
+    if parents.dtype != torch.int32 or parents.shape != (B, T):
+        raise ValueError("parents must be int32 [B,T]")
+    if cu_seqlens is None and T > _lib.TREE_MAX:
+        raise ValueError("a tree has at most %d nodes" % _lib.TREE_MAX)
+    if cu_seqlens is not None and not cu_seqlens.is_cuda and \
+            int((cu_seqlens[1:] - cu_seqlens[:-1]).amax()) > _lib.TREE_MAX:
+        raise ValueError("a tree has at most %d nodes" % _lib.TREE_MAX)
+    if not parents.is_cuda and (cu_seqlens is None or not cu_seqlens.is_cuda):
+        at = torch.arange(T, dtype=torch.int32).expand(B, T)
+        if cu_seqlens is not None:
+            lens = (cu_seqlens[1:] - cu_seqlens[:-1]).long()
+            at = at - torch.repeat_interleave(cu_seqlens[:-1], lens)
+        if bool((parents < -1).any()) or bool((parents >= at).any()):
+            raise ValueError("a node's parent is -1 or an earlier node of its tree")
+
+
+def _output(out, output_dtype, shape, dev, *inputs):
+    if out is None:
+        if output_dtype not in _DT:
+            raise ValueError("output_dtype must be bfloat16 or float32")
+        return torch.empty(shape, dtype=output_dtype, device=dev)
+    if out.shape != shape or out.dtype not in _DT or not out.is_contiguous() or out.data_ptr() % 16:
+        raise ValueError("out must be contiguous [B,T,H_v,V], bfloat16 or float32, 16-byte aligned")
+    _same_device(dev, out)
+    for x in inputs:
+        if _overlap(out, x):
+            raise ValueError("out overlaps an input")
+    return out
+
+
+def _span(t):
+    """First byte of a tensor and the byte past its last one."""
+    a = t.data_ptr()
+    return a, a + ((sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size() if t.numel() else 0)
+
+
+def _overlap(a, b):
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a.device == b.device and a0 < b1 and b0 < a1
+
+
+def _launch(call, args, dev):
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        call(args, stream)
+    else:
+        with torch.cuda.device(dev):
+            call(args, stream)
+
+
+def _pool_call(call, q, k, v, g, beta, parents, accepted, states, scale, cu_seqlens, slots, o):
+    dev = states.device
+    B, T, H_q, K = k.shape
+    H_v, V = v.shape[2], v.shape[3]
+    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    k, k_row, k_batch = _rows(k)
+    v, v_row, v_batch = _rows(v)
+    q, q_row, q_batch = (None, 0, 0) if q is None else _rows(q)
+    g, beta = _c(g, torch.float32), _c(beta, torch.float32)
+    on = lambda x: None if x is None else _c(x).to(dev)  # noqa: E731
+    cu_seqlens, slots, parents, accepted = on(cu_seqlens), on(slots), on(parents), on(accepted)
+    args = _lib.PoolArgs(
+        B, T, H_q, H_v, K, V, n_seq, states.shape[0], states.stride(0), q_row, k_row, v_row, q_batch, k_batch, v_batch,
+        _DT[k.dtype], _lib.F32 if o is None else _DT[o.dtype], float(scale), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+        _ptr(beta), _ptr(cu_seqlens), _ptr(slots), _ptr(parents), _ptr(accepted), _ptr(states), _ptr(o))
+    _launch(call, args, dev)
+
+
+def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=None, *, slots=None,
+                               output_dtype=torch.float32, out=None):
+    """The recurrent form: every sequence's tokens are taken into its state, in place.
+    Returns ``o`` [B,T,H_v,V].
+
+    q, k [B,T,H_q,K], v [B,T,H_v,V], g and beta [B,T,H_v] as for
+    :func:`chunk_gated_delta_rule`, with B sequences of T tokens, or packed sequences
+    with ``cu_seqlens``; the result is that of the chunked operator with the states as
+    initial states and the final states written over them.  Meant for one token per
+    sequence or a few (the state is read and written once a call, and the tokens are
+    taken one after the other).  q, k and v may be slices of a wider projection: they
+    are read in place where a token's heads are contiguous.
+
+    ``states`` float32 [n_slots,H_v,K,V], the slots any distance apart; ``slots`` int32
+    [N] names each sequence's slot (default: slot j for sequence j).  A sequence whose
+    slot is negative (the padding of a batch) is skipped and its rows of ``o`` are
+    zero; so is a sequence that names a slot which an earlier one has.  ``out``: a
+    contiguous tensor to write; rows that belong to no sequence are left as they are.
+    """
+    _check_tokens(q, k, v, g, beta, cu_seqlens)
+    B, T, K = q.shape[0], q.shape[1], q.shape[3]
+    _check_states(states, v.shape[2], K, v.shape[3])
+    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _check_slots(slots, n_seq, states.shape[0])
+    _check_distinct(slots)
+    _refuse_gradients(q, k, v, g, beta, states)
+    if not states.is_cuda:
+        raise ValueError("inputs must be on the GPU")
+    _same_device(states.device, q, k, v, g, beta)
+    o = _output(out, output_dtype, v.shape, states.device, q, k, v, g, beta, states)
+    _pool_call(_lib.step, q, k, v, g, beta, None, None, states, K ** -0.5 if scale is None else scale, cu_seqlens,
+               slots, o)
+    return o
+
+
+def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seqlens=None, *, slots=None,
+                          output_dtype=torch.float32, out=None):
+    """Trees of drafted tokens over the cached states, which are only read.  Returns
+    ``o`` [B,T,H_v,V]: of every node, what :func:`recurrent_gated_delta_rule` would
+    give for it after the nodes on its path.
+
+    A sequence is one tree of at most 64 nodes: B trees of T nodes, or packed trees
+    with ``cu_seqlens``.  ``parents`` int32 [B,T] holds the place of a node's parent
+    among its tree's nodes, which come after their parents, or -1 for a child of the
+    cached state; an entry that is no earlier node counts as -1.  A node influences
+    its own row and its descendants', whatever its values.  Several trees may name one
+    slot; a tree whose slot is negative gets rows of zeros, and a packed tree of more
+    than 64 nodes rows of NaN.  The other arguments are those of
+    :func:`recurrent_gated_delta_rule`.
+    """
+    _check_tokens(q, k, v, g, beta, cu_seqlens)
+    B, T, K = q.shape[0], q.shape[1], q.shape[3]
+    _check_parents(parents, B, T, cu_seqlens)
+    _check_states(states, v.shape[2], K, v.shape[3])
+    _check_slots(slots, B if cu_seqlens is None else cu_seqlens.numel() - 1, states.shape[0])
+    _refuse_gradients(q, k, v, g, beta, states)
+    if not states.is_cuda:
+        raise ValueError("inputs must be on the GPU")
+    _same_device(states.device, q, k, v, g, beta)
+    o = _output(out, output_dtype, v.shape, states.device, q, k, v, g, beta, states)
+    _pool_call(_lib.tree, q, k, v, g, beta, parents, None, states, K ** -0.5 if scale is None else scale, cu_seqlens,
+               slots, o)
+    return o
+
+
+def tree_gated_delta_rule_accept(k, v, g, beta, parents, accepted, states, cu_seqlens=None, *, slots=None):
+    """Takes the tokens on the path to an accepted node into each sequence's state, in
+    place, with the very results of :func:`recurrent_gated_delta_rule` on those tokens.
+    Returns ``states``.
+
+    k, v, g, beta, parents, cu_seqlens and slots as given to
+    :func:`tree_gated_delta_rule`; ``accepted`` int32 [N] is the last accepted node of
+    each tree, or -1 for none (the state then stays as it is).  A sequence that names
+    a slot which an earlier one has is skipped.
+    """
+    _check_tokens(None, k, v, g, beta, cu_seqlens)
+    B, T, K = k.shape[0], k.shape[1], k.shape[3]
+    _check_parents(parents, B, T, cu_seqlens)
+    _check_states(states, v.shape[2], K, v.shape[3])
+    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _check_slots(slots, n_seq, states.shape[0])
+    _check_distinct(slots)
+    _indices(accepted, n_seq, "accepted", -1, _lib.TREE_MAX if cu_seqlens is not None else T)
+    _refuse_gradients(k, v, g, beta, states)
+    if not states.is_cuda:
+        raise ValueError("inputs must be on the GPU")
+    _same_device(states.device, k, v, g, beta)
+    _pool_call(_lib.tree_accept, None, k, v, g, beta, parents, accepted, states, 1.0, cu_seqlens, slots, None)
+    return states
+
+
+def copy_states(states, dst, src, source=None):
+    """For every entry i, slot ``dst[i]`` of ``states`` becomes what slot ``src[i]`` of
+    ``source`` (default: ``states``) was before the call, or zero where ``src[i]`` is
+    -1.  Returns ``states``.
+
+    One list of up to 4096 entries may thus fork a state (a source named several
+    times), move, swap or reorder states within a pool, and clear slots for new
+    sequences.  Entries with ``dst`` -1 are skipped; of entries with the same ``dst``
+    the last one stands.  On the device, entries past either pool are skipped too.
+
+    ``states`` and ``source``: float32 [n_slots,H_v,K,V], or [layers,n_slots,H_v,K,V]
+    for the pools of several layers copied by the same list; ``dst``, ``src``: int32
+    [n].  ``source`` may be another pool, such as the final states of a prefill; it
+    must not overlap ``states`` in memory, unless it is the same pool.
+    """
+    pools = [states] if source is None else [states, source]
+    for x, name in zip(pools, ("states", "source")):
+        if x.dim() not in (4, 5):
+            raise ValueError("%s must be float32 [n_slots,H_v,K,V] or [layers,n_slots,H_v,K,V]" % name)
+        if x.dim() == 5 and x.shape[0] > 0:
+            _check_states(x[0], None, None, None, name)
+            if x.shape[0] > 1 and (x.stride(0) % 4 or x.stride(0) < x[0, 0].numel()):
+                raise ValueError("a slot of %s must be contiguous and 16-byte aligned" % name)
+        elif x.dim() == 4:
+            _check_states(x, None, None, None, name)
+    if source is None or (source.data_ptr() == states.data_ptr() and source.shape == states.shape
+                          and source.stride() == states.stride()):
+        source = states
+    elif source.dim() != states.dim() or source.shape[-3:] != states.shape[-3:] or \
+            (states.dim() == 5 and source.shape[0] != states.shape[0]):
+        raise ValueError("states and source must hold states of one shape and as many layers")
+    elif _overlap(states, source):
+        raise ValueError("source overlaps states")
+    n, n_dst, n_src = dst.numel(), states.shape[-4], source.shape[-4]
+    if n > _lib.COPY_MAX:
+        raise ValueError("at most %d entries" % _lib.COPY_MAX)
+    _indices(dst, n, "dst", -1, n_dst)
+    _indices(src, n, "src", -1, n_src)
+    _refuse_gradients(states, source)
+    if not states.is_cuda:
+        raise ValueError("inputs must be on the GPU")
+    dev = states.device
+    _same_device(dev, source)
+    dst, src = _c(dst).to(dev), _c(src).to(dev)
+    layered = states.dim() == 5
+    H, K, V = states.shape[-3:]
+    args = _lib.CopyArgs(
+        n, n_dst, n_src, 4 * H * K * V, 4 * states.stride(-4), 4 * source.stride(-4),
+        states.shape[0] if layered else 1, 4 * states.stride(0) if layered else 0,
+        4 * source.stride(0) if layered else 0, _ptr(dst), _ptr(src), _ptr(states), _ptr(source))
+    _launch(_lib.copy_states, args, dev)
+    return states

@@ -48,10 +48,12 @@
 extern "C" {
 #endif
 
-#define GDR_ABI_VERSION 7
+#define GDR_ABI_VERSION 8
 #define GDR_CHUNK 64
 #define GDR_FWD_STAGES 3
 #define GDR_BWD_STAGES 4
+#define GDR_TREE_MAX 64   /* nodes of a tree (gdr_tree, gdr_tree_accept) */
+#define GDR_COPY_MAX 4096 /* entries of one gdr_copy_states */
 
 /* return codes */
 #define GDR_OK 0
@@ -198,6 +200,56 @@ typedef struct {
     size_t workspace_bytes;
 } gdr_bwd_args;
 
+/* A pool of recurrent states and the tokens that meet it (gdr_step, gdr_tree,
+   gdr_tree_accept).  The pool holds one state h = S^T (K x V, fp32) per (slot, v
+   head); slots[j] is the slot of sequence j.  Index arrays are device data that
+   the host cannot check without a synchronisation: an entry of slots outside
+   [0, n_slots) means that the sequence has no state (it is skipped, and its rows
+   of o are set to zero), and offsets outside [0, T] are clamped to it, an end
+   before its start to the start.  Rows of o that belong to no sequence are left
+   as they were, and so is the state of an empty sequence. */
+typedef struct {
+    /* sizes as in gdr_fwd_args; B, T and n_seq may be 0 */
+    int64_t B, T, H_q, H_v, K, V, n_seq;
+    int64_t n_slots;
+    int64_t slot_stride;  /* floats from a slot's state to the next slot's: a multiple of 4, at
+                             least H_v K V (not read if n_slots is 1) */
+    /* elements from a token's row of q, k or v to the next token's, and from a batch
+       row's to the next one's (not read with cu_seqlens): multiples of 16 bytes, >= 0.
+       The [H, K] (or [H, V]) values of one token are contiguous */
+    int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;
+    int32_t dtype;     /* element type of q, k, v */
+    int32_t out_dtype; /* element type of o */
+    float scale;
+    const void *q;             /* H_q x K per token; not read by gdr_tree_accept */
+    const void *k, *v;         /* H_q x K and H_v x V per token */
+    const float *g, *beta;     /* [B,T,H_v] */
+    const int32_t *cu_seqlens; /* [n_seq+1] token offsets (B = 1), or NULL */
+    const int32_t *slots;      /* [n_seq]; NULL: sequence j has slot j (n_slots >= n_seq) */
+    const int32_t *parents;    /* [B,T]: a node's parent, counted from its tree's first node; -1, and
+                                  any entry that is not an earlier node, is the cached state.  Not
+                                  read by gdr_step */
+    const int32_t *accepted;   /* [n_seq], gdr_tree_accept only: the last accepted node of each tree;
+                                  -1, or any entry that is no node, accepts nothing */
+    float *states;             /* [n_slots][H_v,K,V], slot_stride apart; gdr_tree only reads it */
+    void *o;                   /* [B,T,H_v,V] out_dtype; not written by gdr_tree_accept */
+} gdr_pool_args;
+
+/* Copies of states between slots (gdr_copy_states); bytes throughout. */
+typedef struct {
+    int64_t n;                 /* entries, 0 .. GDR_COPY_MAX */
+    int64_t n_dst, n_src;      /* slots of the destination and of the source */
+    int64_t slot_bytes;        /* bytes of a state, a multiple of 16 */
+    int64_t dst_stride, src_stride;              /* between slots: multiples of 16, at least slot_bytes
+                                                    (not read where there is one slot) */
+    int64_t layers;                              /* pools copied by the same list, >= 0 */
+    int64_t dst_layer_stride, src_layer_stride;  /* between layers: multiples of 16, >= 0 (a layer's
+                                                    slots may lie between another's) */
+    const int32_t *dst, *src;  /* [n]: slots of each entry */
+    void *states;
+    const void *source;        /* states itself, or memory that does not overlap it */
+} gdr_copy_args;
+
 /* GDR_ABI_VERSION of the loaded library. */
 int gdr_abi_version(void);
 
@@ -291,6 +343,36 @@ int gdr_bwd_workspace(const gdr_bwd_args *args, size_t *bytes);
    transitions).  Returns GDR_ELAUNCH if the stream's device cannot be
    queried. */
 int gdr_bwd(const gdr_bwd_args *args, hipStream_t stream);
+
+/* The recurrent form on `stream`: every sequence's tokens are taken in turn into
+   its state, in place, and o gets their outputs.  For one token or a few per
+   sequence (decode); the chunked gdr_fwd is faster for long ones.  Where two
+   sequences with tokens name one slot, the first has it and the others are
+   skipped, as if they had none.  Needs no workspace and may be captured. */
+int gdr_step(const gdr_pool_args *args, hipStream_t stream);
+
+/* Trees of drafted tokens on `stream`: o of every node as if the recurrence had
+   been run from the sequence's state over the node's ancestors and the node; the
+   states are left as they are (sequences may share a slot).  A sequence is one tree
+   of at most GDR_TREE_MAX nodes, parents before children (T above that without
+   cu_seqlens is GDR_EINVAL; a longer packed sequence gets rows of NaN).  A node
+   influences its descendants only, with non-finite values too.  Needs no workspace
+   and may be captured. */
+int gdr_tree(const gdr_pool_args *args, hipStream_t stream);
+
+/* Acceptance on `stream`: the tokens on the path to node accepted[j] are taken into
+   the state of sequence j, in place, as gdr_step would take them.  Slots named twice
+   are treated as by gdr_step; a tree of more than GDR_TREE_MAX nodes accepts
+   nothing.  Needs no workspace and may be captured. */
+int gdr_tree_accept(const gdr_pool_args *args, hipStream_t stream);
+
+/* Copies on `stream`: for every entry, the state of slot dst[i] becomes that which
+   slot src[i] of `source` had before the call, or zero if src[i] is negative.  Every
+   source is read before any state is written, so a list may move, swap and fork the
+   slots of one pool.  Of entries with the same dst the last one stands.  Entries with
+   dst outside [0, n_dst) or src at or past n_src are skipped.  Needs no workspace and
+   may be captured. */
+int gdr_copy_states(const gdr_copy_args *args, hipStream_t stream);
 
 #ifdef __cplusplus
 }

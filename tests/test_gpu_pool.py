@@ -1,0 +1,620 @@
+"""The operators on a pool of states against 64 bits (pool_reference), on the GPU."""
+import pytest
+import torch
+
+import gated_delta_rule_85_amd as gdr
+import pool_reference as ref
+from gated_delta_rule_85_amd import _lib
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+I32 = dict(dtype=torch.int32)
+# dtype, output, Hq, Hv, K, V
+KINDS = [(BF, BF, 2, 4, 128, 128), (BF, F32, 1, 3, 128, 64), (F32, F32, 2, 2, 64, 128), (F32, BF, 3, 6, 64, 64),
+         (BF, F32, 2, 4, 64, 64), (F32, F32, 1, 2, 128, 128), (BF, BF, 1, 1, 64, 128), (BF, F32, 2, 4, 128, 128)]
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def untouched(states, before, slots):
+    """The pool's other slots hold what they held, to the bit."""
+    rest = [s for s in range(before.shape[0]) if s not in slots]
+    assert torch.equal(states[rest].cpu(), before[rest])
+
+
+def run_recurrent(d, **kw):
+    return gdr.recurrent_gated_delta_rule(d["q"], d["k"], d["v"], d["g"], d["beta"], d["states"], cu_seqlens=d["cu"],
+                                          slots=d["slots"], **kw)
+
+
+def run_tree(d, **kw):
+    return gdr.tree_gated_delta_rule(d["q"], d["k"], d["v"], d["g"], d["beta"], d["parents"], d["states"],
+                                     cu_seqlens=d["cu"], slots=d["slots"], **kw)
+
+
+def run_accept(d):
+    return gdr.tree_gated_delta_rule_accept(d["k"], d["v"], d["g"], d["beta"], d["parents"], d["accepted"], d["states"],
+                                            cu_seqlens=d["cu"], slots=d["slots"])
+
+
+# ---------------------------------------------------------------- recurrent
+@pytest.mark.parametrize("dtype,out,Hq,Hv,K,V", KINDS)
+@pytest.mark.parametrize("N,T,lens", [(1, 1, None), (5, 1, None), (3, 2, None), (2, 9, None), (0, 0, [1, 0, 3, 1, 7])])
+def test_recurrent(dtype, out, Hq, Hv, K, V, N, T, lens):
+    say("recurrent", dtype, out, Hq, Hv, K, V, N, T, lens)
+    x = ref.make(N, T, Hq, Hv, K, V, dtype, lens, seed=3)
+    o_want, s_want, X = ref.recurrent(x)
+    d = ref.cuda(x)
+    o = run_recurrent(d, output_dtype=out)
+    n = T if lens is None else max(lens)
+    ref.near(o, o_want, n, K, X, "o")
+    ref.near(d["states"], s_want, n, K, X, "states")
+    untouched(d["states"], x["states"], x["slots"].tolist())
+
+
+def test_recurrent_is_the_chunked_operator_on_long_sequences():
+    x = ref.make(2, 300, 2, 4, 128, 128, BF, seed=4)
+    d = ref.cuda(x)
+    h0 = d["states"][d["slots"].long()]
+    o, ht = gdr.chunk_gated_delta_rule(d["q"], d["k"], d["v"], d["g"], d["beta"], initial_state=h0,
+                                       output_final_state=True)
+    o2 = run_recurrent(d)
+    # the chunked operator's own parity bar is 2e-2 of the rms; it measures 1e-4 to 2.5e-4
+    for a, b in ((o, o2), (ht, d["states"][d["slots"].long()])):
+        assert float((a - b).abs().max()) <= 1e-3 * float(b.square().mean().sqrt())
+
+
+def test_recurrent_without_slots_and_with_a_scale():
+    x = ref.make(3, 2, 1, 2, 64, 64, F32, seed=5)
+    x["slots"] = torch.arange(3, **I32)
+    o_want, s_want, X = ref.recurrent(x, scale=0.75)
+    d = ref.cuda(x)
+    d["slots"] = None
+    ref.near(run_recurrent(d, scale=0.75), o_want, 2, 64, X)
+    ref.near(d["states"], s_want, 2, 64, X)
+
+
+def test_indices_on_the_host_are_taken():
+    x = ref.make(0, 0, 1, 2, 64, 64, F32, [2, 1], seed=5)
+    o_want, s_want, X = ref.recurrent(x)
+    d = ref.cuda(x)
+    d["slots"], d["cu"] = x["slots"], x["cu"]
+    ref.near(run_recurrent(d), o_want, 2, 64, X)
+    ref.near(d["states"], s_want, 2, 64, X)
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_recurrent_reads_slices_of_a_projection(T, dtype):
+    """q, k, v as parts of one row, of odd batch and row strides, and one part that has to be copied."""
+    x = ref.make(4, T, 2, 4, 64, 64, dtype, seed=6)
+    o_want, s_want, X = ref.recurrent(x)
+    d = ref.cuda(x)
+    parts = [d[n].flatten(2) for n in ("q", "k", "v")]
+    for pad, copied in ((8, False), (3, True)):
+        row = torch.cat(parts + [torch.zeros(4, T, pad, dtype=dtype, device="cuda")], dim=-1)
+        wide = torch.zeros(4, T + 2, row.shape[-1], dtype=dtype, device="cuda")
+        wide[:, :T] = row
+        e = dict(d, states=d["states"].clone())
+        e["q"], e["k"] = wide[:, :T, :128].view(4, T, 2, 64), wide[:, :T, 128:256].view(4, T, 2, 64)
+        e["v"] = wide[:, :T, 256:512].view(4, T, 4, 64)
+        o = run_recurrent(e)
+        ref.near(o, o_want, T, 64, X, "o %s" % copied)
+        ref.near(e["states"], s_want, T, 64, X, "states %s" % copied)
+
+
+def test_recurrent_on_a_pool_with_other_things_between_its_slots():
+    x = ref.make(3, 1, 2, 4, 64, 64, BF, seed=7)
+    o_want, s_want, X = ref.recurrent(x)
+    d = ref.cuda(x)
+    wide = torch.full((5, 4 * 64 * 64 + 12), 7.0, device="cuda")
+    pool = wide[:, 8:8 + 4 * 64 * 64].view(5, 4, 64, 64)
+    pool.copy_(d["states"])
+    d["states"] = pool
+    ref.near(run_recurrent(d), o_want, 1, 64, X)
+    ref.near(d["states"].clone(), s_want, 1, 64, X)
+    assert bool((wide[:, :8] == 7).all()) and bool((wide[:, -4:] == 7).all())
+
+
+def test_padding_and_repeated_slots_are_skipped():
+    """Slots of -1 and past the pool, and a slot that an earlier sequence has: zero rows, no state touched."""
+    x = ref.make(0, 0, 1, 2, 64, 64, F32, [2, 1, 0, 3, 1, 1], seed=8)
+    for n in ("q", "k", "v", "g", "beta"):
+        x[n][:, 2] = float("nan")  # of the skipped sequence 1
+    d = ref.cuda(x)
+    # sequence 2 is empty and owns nothing, so that sequence 3 has slot 4; 4 repeats 0's
+    d["slots"] = torch.tensor([5, -1, 4, 4, 5, 1000], **I32, device="cuda")
+    o = run_recurrent(d)
+    y = dict(x, q=x["q"][:, [0, 1, 3, 4, 5]], k=x["k"][:, [0, 1, 3, 4, 5]], v=x["v"][:, [0, 1, 3, 4, 5]],
+             g=x["g"][:, [0, 1, 3, 4, 5]], beta=x["beta"][:, [0, 1, 3, 4, 5]], cu=torch.tensor([0, 2, 5]),
+             slots=torch.tensor([5, 4]))
+    o_want, s_want, X = ref.recurrent(y)
+    ref.near(o[:, [0, 1, 3, 4, 5]], o_want, 3, 64, X)
+    assert bool((o[:, [2, 6, 7]] == 0).all())
+    ref.near(d["states"], s_want, 3, 64, X)
+    untouched(d["states"], x["states"], [4, 5])
+
+
+def test_many_sequences_with_a_repeated_slot():
+    """The lookup of earlier owners over more sequences than a wave has lanes."""
+    N = 300
+    x = ref.make(N, 1, 1, 1, 64, 64, F32, seed=9)
+    d = ref.cuda(x)
+    slots = x["slots"].clone()
+    slots[257] = slots[3]
+    slots[299] = slots[130]
+    d["slots"] = slots.cuda()
+    o = run_recurrent(d)
+    keep = [i for i in range(N) if i not in (257, 299)]
+    o_want, s_want, X = ref.recurrent(dict(x, slots=x["slots"]))
+    ref.near(o[keep], o_want[keep], 1, 64, X)
+    assert bool((o[[257, 299]] == 0).all())
+    lost = [int(x["slots"][i]) for i in (257, 299)]
+    rest = [s for s in range(N + 2) if s not in lost]
+    ref.near(d["states"][rest], s_want[rest], 1, 64, X)
+    assert torch.equal(d["states"][lost].cpu(), x["states"][lost])
+
+
+def test_rows_behind_the_last_sequence_are_left():
+    x = ref.make(0, 0, 1, 2, 64, 64, F32, [2, 1, 2], seed=10)
+    x["cu"] = torch.tensor([0, 2, 3, 3], **I32)
+    x["parents"] = torch.tensor([[-1, 0, -1, 0, 0]], **I32)
+    for run in (run_recurrent, run_tree):
+        d = ref.cuda(x)
+        out = torch.full((1, 5, 2, 64), 9.0, device="cuda")
+        assert run(d, out=out) is out
+        assert bool((out[:, 3:] == 9).all()) and bool((out[:, :3] != 9).all())
+
+
+def test_offsets_out_of_range_on_the_device_touch_nothing_else():
+    x = ref.make(0, 0, 1, 2, 64, 64, F32, [2, 1, 2], seed=10)
+    x["parents"] = torch.tensor([[-1, 0, -1, 0, 0]], **I32)
+    x["accepted"] = torch.tensor([9, 0, -7], **I32)
+    for cu in ([-5, 2, 900, 4], [4, 1, 1, 3], [2 ** 31 - 1, -2 ** 31, 7, 7]):
+        for run in (run_recurrent, run_tree, run_accept):
+            d = ref.cuda(x)
+            d["cu"] = torch.tensor(cu, **I32, device="cuda")
+            guard = torch.full((12, 2, 64), 5.0, device="cuda")
+            if run is run_accept:
+                run(d)
+            else:
+                run(d, out=guard[4:9].view(1, 5, 2, 64))
+            torch.cuda.synchronize()
+            assert bool((guard[:4] == 5).all()) and bool((guard[9:] == 5).all())
+            untouched(d["states"], x["states"], x["slots"].tolist())
+
+
+def test_out_is_checked():
+    d = ref.cuda(ref.make(2, 1, 1, 2, 64, 64, F32, seed=1))
+    for out in (torch.empty(2, 1, 2, 65, device="cuda"), torch.empty(2, 1, 2, 64, device="cuda").half(),
+                torch.empty(2, 1, 64, 2, device="cuda").mT, torch.empty(2, 1, 2, 64), d["v"],
+                d["states"].view(-1)[:256].view(2, 1, 2, 64)):
+        with pytest.raises(ValueError):
+            run_recurrent(d, out=out)
+
+
+def test_empty_batches():
+    x = ref.make(2, 1, 1, 2, 64, 64, F32, seed=1)
+    for y in (dict(x, **{n: x[n][:0] for n in ("q", "k", "v", "g", "beta", "slots")}),
+              dict(x, **{n: x[n][:, :0] for n in ("q", "k", "v", "g", "beta")}),
+              dict(x, **{n: x[n][:1, :0] for n in ("q", "k", "v", "g", "beta")}, cu=torch.tensor([0, 0, 0], **I32)),
+              dict(x, **{n: x[n][:1, :0] for n in ("q", "k", "v", "g", "beta")}, cu=torch.tensor([0], **I32),
+                   slots=x["slots"][:0])):
+        B, T = y["q"].shape[:2]
+        y["parents"] = torch.zeros(B, T, **I32)
+        y["accepted"] = torch.zeros(len(y["slots"]), **I32) - 1
+        d = ref.cuda(y)
+        assert run_recurrent(d).shape == y["v"].shape and run_tree(d).shape == y["v"].shape
+        run_accept(d)
+        assert torch.equal(d["states"].cpu(), x["states"])
+
+
+def test_gates_that_forget_everything():
+    """g = -inf and far below any exponent: the state is cleared, and later nodes are exact."""
+    x = ref.make(2, 6, 1, 2, 128, 64, F32, seed=12)
+    x["g"][0, 2] = float("-inf")
+    x["g"][1, 1] = -3e5
+    x["g"][1, 4] = -1e30
+    x["parents"] = torch.tensor([[-1, 0, 1, 2, 3, 3], [-1, 0, 1, 2, 3, 1]], **I32)
+    x["accepted"] = torch.tensor([4, 5], **I32)
+    o_want, s_want, X = ref.recurrent(x)
+    d = ref.cuda(x)
+    ref.near(run_recurrent(d), o_want, 6, 128, X)
+    ref.near(d["states"], s_want, 6, 128, X)
+    d = ref.cuda(x)
+    o_want, X = ref.tree(x, x["parents"])
+    ref.near(run_tree(d), o_want, 6, 128, X)
+    run_accept(d)
+    s_want, X = ref.accept(x, x["parents"], x["accepted"])
+    ref.near(d["states"], s_want, 6, 128, X)
+
+
+def test_offsets_past_32_bits():
+    """Slots at the far end of a pool of more than 2^31 values."""
+    Hv, K, V, n = 32, 128, 128, 4100
+    pool = torch.empty(n, Hv, K, V, device="cuda")
+    x = ref.make(2, 3, 2, Hv, K, V, BF, seed=13)
+    x["parents"], x["accepted"] = torch.tensor([[-1, 0, 0], [-1, -1, 1]], **I32), torch.tensor([2, 2], **I32)
+    small = dict(x, slots=torch.tensor([0, 1]), states=x["states"][:2])
+    d = ref.cuda(x)
+    d["states"], d["slots"] = pool, torch.tensor([n - 1, n - 3], **I32, device="cuda")
+    far = [n - 1, n - 3]
+    for run, want in ((run_recurrent, lambda: ref.recurrent(small)), (run_tree, lambda: ref.tree(small, x["parents"])),
+                      (run_accept, lambda: ref.accept(small, x["parents"], x["accepted"]))):
+        pool[far] = small["states"].cuda()
+        got = run(d)
+        w = want()
+        if run is not run_accept:
+            ref.near(got, w[0], 3, K, w[-1])
+        if run is not run_tree:
+            ref.near(pool[far], w[-2], 3, K, w[-1])
+    pool[far] = small["states"].cuda()
+    pool[:4] = 1.0
+    gdr.copy_states(pool, torch.tensor([0, n - 3, n - 1], **I32, device="cuda"),
+                    torch.tensor([n - 3, n - 1, 2], **I32, device="cuda"))
+    assert torch.equal(pool[0].cpu(), small["states"][1]) and torch.equal(pool[n - 3].cpu(), small["states"][0])
+    assert bool((pool[n - 1] == 1).all())
+
+
+# ---------------------------------------------------------------- trees
+def shape_of(kind, n, gen):
+    if kind == "chain":
+        return [i - 1 for i in range(n)]
+    if kind == "star":
+        return [-1] + [0] * (n - 1)
+    if kind == "roots":
+        return [-1] * n
+    if kind == "binary":
+        return [(i - 1) // 2 if i else -1 for i in range(n)]
+    return [int(torch.randint(-1, i, (1,), generator=gen)) if i else -1 for i in range(n)]
+
+
+@pytest.mark.parametrize("dtype,out,Hq,Hv,K,V", KINDS)
+@pytest.mark.parametrize("n", [1, 2, 7, 15, 16, 17, 32, 33, 47, 48, 49, 63, 64])
+def test_tree(dtype, out, Hq, Hv, K, V, n):
+    gen = torch.Generator().manual_seed(n)
+    kinds = ["random", ["chain", "star", "roots", "binary"][n % 4]]
+    say("tree", dtype, out, Hq, Hv, K, V, n, kinds)
+    x = ref.make(2, n, Hq, Hv, K, V, dtype, seed=n)
+    x["parents"] = torch.tensor([shape_of(k, n, gen) for k in kinds], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    d = ref.cuda(x)
+    o = run_tree(d, output_dtype=out)
+    assert torch.equal(d["states"].cpu(), x["states"])
+    ref.near(o, o_want, n, K, X, "o")
+
+
+@pytest.mark.parametrize("kind", ["chain", "star", "roots", "binary", "random"])
+def test_tree_shapes(kind):
+    gen = torch.Generator().manual_seed(1)
+    x = ref.make(3, 64, 1, 2, 128, 128, BF, seed=2)
+    x["parents"] = torch.tensor([shape_of(kind, 64, gen) for _ in range(3)], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    ref.near(run_tree(ref.cuda(x)), o_want, 64, 128, X)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_packed_trees(dtype):
+    lens = [5, 0, 64, 1, 17, 33, 48]
+    gen = torch.Generator().manual_seed(3)
+    x = ref.make(0, 0, 2, 4, 128, 64, dtype, lens, seed=3)
+    x["parents"] = torch.tensor([sum((shape_of("random", n, gen) for n in lens), [])], **I32)
+    x["accepted"] = torch.tensor([4, -1, 63, 0, 11, 30, -1], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    d = ref.cuda(x)
+    ref.near(run_tree(d), o_want, 64, 128, X)
+    run_accept(d)
+    s_want, X = ref.accept(x, x["parents"], x["accepted"])
+    ref.near(d["states"], s_want, 64, 128, X)
+    untouched(d["states"], x["states"], [int(s) for s, n in zip(x["slots"], x["accepted"]) if n >= 0])
+
+
+def test_a_chain_is_the_recurrent_form_and_trees_may_share_a_slot():
+    x = ref.make(1, 8, 2, 4, 128, 128, BF, seed=4)
+    d = ref.cuda(x)
+    d["parents"] = torch.tensor([[-1, 0, 1, 2, 3, 4, 5, 6]], **I32, device="cuda")
+    two = {n: torch.cat([d[n], d[n]]) for n in ("q", "k", "v", "g", "beta", "parents", "slots")}
+    o = run_tree(dict(d, **two))
+    assert torch.equal(o[0], o[1])
+    want, _, X = ref.recurrent(x)
+    ref.near(o[:1], want, 8, 128, X)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, F32), (BF, BF), (F32, F32)])
+@pytest.mark.parametrize("n", [14, 50])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nonfinite_nodes_reach_their_descendants_only(dtype, out, n, name, value):
+    """Siblings and ancestors of a node with NaN or an infinity (a g of -inf is legal) are as without it."""
+    x = ref.make(1, n, 1, 2, 128, 128, dtype, seed=5)
+    parents = shape_of("random", n, torch.Generator().manual_seed(n))
+    x["parents"] = torch.tensor([parents], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    bad, col = n // 3, 37
+    y = dict(x)
+    y[name] = x[name].clone()
+    if name in ("g", "beta"):
+        y[name][0, bad, 0] = value
+    else:
+        y[name][0, bad, 0, col] = value
+    o = run_tree(ref.cuda(y), output_dtype=out)
+    hit = [i for i in range(n) if (i == bad if name == "q" else bad in ref.path_of(parents, i))]
+    fine = [i for i in range(n) if i not in hit]
+    assert fine and hit
+    # head 1 shares q and k with head 0, but not v, g and beta
+    heads = [0, 1] if name in ("q", "k") else [0]
+    cols = [col] if name == "v" else list(range(128))
+    ok = torch.ones(1, n, 2, 128, dtype=torch.bool)
+    for i in hit:
+        for h in heads:
+            ok[0, i, h, cols] = False
+    got = o.cpu()
+    assert not bool(torch.isfinite(got[~ok]).any())
+    ref.near(torch.where(ok, got, 0), torch.where(ok, o_want, 0.0), n, 128, X)
+
+
+def test_parents_that_are_no_earlier_nodes_count_as_none():
+    x = ref.make(1, 5, 1, 1, 64, 64, F32, seed=6)
+    x["parents"] = torch.tensor([[-1, 0, -1, -1, 2]], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    x["accepted"] = torch.tensor([3], **I32)
+    s_want, X2 = ref.accept(x, x["parents"], x["accepted"])
+    d = ref.cuda(x)
+    d["parents"] = torch.tensor([[0, 0, 2, 64, 2]], **I32, device="cuda")
+    ref.near(run_tree(d), o_want, 5, 64, X)
+    run_accept(d)
+    ref.near(d["states"], s_want, 5, 64, X2)
+
+
+def test_trees_without_a_slot_or_of_too_many_nodes():
+    x = ref.make(0, 0, 1, 2, 64, 64, BF, [3, 65, 64], seed=7)
+    x["parents"] = torch.full((1, 132), -1, **I32)
+    d = ref.cuda(x)
+    d["slots"] = torch.tensor([-1, 0, 1], **I32, device="cuda")
+    d["accepted"] = torch.tensor([2, 64, 63], **I32, device="cuda")
+    o = run_tree(d)
+    assert bool((o[:, :3] == 0).all()) and bool(torch.isnan(o[:, 3:68]).all()) and bool(torch.isfinite(o[:, 68:]).all())
+    run_accept(d)
+    untouched(d["states"], x["states"], [1])
+    assert not torch.equal(d["states"][1].cpu(), x["states"][1])
+
+
+# ---------------------------------------------------------------- acceptance
+@pytest.mark.parametrize("dtype,out,Hq,Hv,K,V", KINDS)
+def test_accept_is_decoding_the_path(dtype, out, Hq, Hv, K, V):
+    """Against 64 bits, and to the bit against the recurrent form on the path's tokens."""
+    n = 21
+    gen = torch.Generator().manual_seed(2)
+    parents = [shape_of(k, n, gen) for k in ("random", "chain", "binary", "star")]
+    x = ref.make(4, n, Hq, Hv, K, V, dtype, seed=11)
+    x["parents"], x["accepted"] = torch.tensor(parents, **I32), torch.tensor([20, 13, 17, -1], **I32)
+    s_want, X = ref.accept(x, x["parents"], x["accepted"])
+    d = ref.cuda(x)
+    assert run_accept(d) is d["states"]
+    ref.near(d["states"], s_want, n, K, X)
+    untouched(d["states"], x["states"], x["slots"][:3].tolist())
+    e = ref.cuda(x)
+    for j in range(3):
+        p = ref.path_of(parents[j], int(x["accepted"][j]))
+        part = {m: e[m][j:j + 1, p] for m in ("q", "k", "v", "g", "beta")}
+        run_recurrent(dict(part, states=e["states"], slots=e["slots"][j:j + 1], cu=None))
+    assert torch.equal(d["states"], e["states"])
+
+
+def test_accept_skips_padding_and_repeated_slots():
+    x = ref.make(4, 3, 1, 2, 64, 64, F32, seed=12)
+    x["parents"], x["accepted"] = torch.tensor([[-1, 0, 1]] * 4, **I32), torch.tensor([2, 1, 2, 3], **I32)
+    x["slots"] = torch.tensor([5, 4, 3, 0], **I32)
+    s_want, X = ref.accept(x, x["parents"], torch.tensor([2, 1, -1, -1]))
+    d = ref.cuda(x)
+    d["slots"] = torch.tensor([5, 4, 5, 0], **I32, device="cuda")  # the third repeats; the fourth accepts no node
+    run_accept(d)
+    ref.near(d["states"], s_want, 3, 64, X)
+    untouched(d["states"], x["states"], [4, 5])
+
+
+# ---------------------------------------------------------------- copies
+def copied(states, dst, src, source=None):
+    before, after = (states if source is None else source).clone(), states.clone()
+    for a, b in zip(dst.tolist(), src.tolist()):
+        if 0 <= a < states.shape[-4] and b < before.shape[-4]:
+            after[..., a, :, :, :] = before[..., b, :, :, :] if b >= 0 else 0.0
+    return after
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 3, 4, 5, 16, 17, 64, 65, 200, 256, 257, 1024, 1025, 4096])
+def test_copies_of_any_number(n):
+    say("copy", n)
+    gen = torch.Generator().manual_seed(n)
+    slots = max(4, n + 3)
+    states = torch.randn(slots, 1, 64, 64, generator=gen)
+    dst = torch.randperm(slots, generator=gen)[:n].to(torch.int32)
+    src = torch.randint(-1, slots, (n,), generator=gen, dtype=torch.int32)
+    want = copied(states, dst, src)
+    pool = states.cuda()
+    assert gdr.copy_states(pool, dst.cuda(), src.cuda()) is pool
+    assert torch.equal(pool.cpu(), want)
+
+
+@pytest.mark.parametrize("Hv,K,V", [(1, 64, 64), (3, 128, 64), (5, 64, 64), (32, 128, 128)])
+def test_permutations_forks_and_clears(Hv, K, V):
+    states = torch.randn(9, Hv, K, V, generator=torch.Generator().manual_seed(1))
+    for dst, src in (([1, 2, 3, 0], [0, 1, 2, 3]), ([8, 7], [7, 8]), ([0, 1, 2, 3, 4, 5, 6, 7, 8], [4] * 9),
+                     ([3, 2, 1], [2, 1, -1]), ([5], [5]), ([0, 1, 2, 3, 4, 5, 6, 7, 8], [-1] * 9)):
+        dst, src = torch.tensor(dst, **I32), torch.tensor(src, **I32)
+        pool = states.cuda()
+        gdr.copy_states(pool, dst, src.cuda())  # dst on the host
+        assert torch.equal(pool.cpu(), copied(states, dst, src)), (dst, src)
+
+
+@pytest.mark.parametrize("n", [6, 40, 300, 1500])
+def test_the_last_of_equal_destinations_stands_and_bad_entries_are_skipped(n):
+    gen = torch.Generator().manual_seed(n)
+    states = torch.randn(n, 2, 64, 64, generator=gen)
+    dst = torch.randint(-3, n // 2, (n,), generator=gen, dtype=torch.int32)
+    src = torch.randint(-2, n + 4, (n,), generator=gen, dtype=torch.int32)
+    dst[n // 2], src[n // 3] = 2 ** 31 - 1, 2 ** 31 - 1
+    dst[1], src[1] = -2 ** 31, 0
+    for _ in range(2):
+        pool = states.cuda()
+        gdr.copy_states(pool, dst.cuda(), src.cuda())
+        assert torch.equal(pool.cpu(), copied(states, dst, src))
+
+
+@pytest.mark.parametrize("slots_first", [False, True])
+def test_copies_in_every_layer(slots_first):
+    states = torch.randn(3, 7, 2, 64, 128, generator=torch.Generator().manual_seed(2))
+    dst, src = torch.tensor([0, 3, 6, 1], **I32), torch.tensor([3, 0, -1, 0], **I32)
+    pool = states.transpose(0, 1).contiguous().cuda().transpose(0, 1) if slots_first else states.cuda()
+    gdr.copy_states(pool, dst.cuda(), src.cuda())
+    assert torch.equal(pool.cpu(), copied(states, dst, src))
+    part = (states.transpose(0, 1).contiguous().cuda().transpose(0, 1) if slots_first else states.cuda())
+    gdr.copy_states(part[:, ::2], dst.clamp(max=3).cuda(), src.clamp(max=3).cuda())
+    want = states.clone()
+    want[:, ::2] = copied(states[:, ::2], dst.clamp(max=3), src.clamp(max=3))
+    assert torch.equal(part.cpu(), want)
+
+
+def test_copies_from_another_pool():
+    gen = torch.Generator().manual_seed(3)
+    states, source = torch.randn(5, 2, 64, 64, generator=gen), torch.randn(8, 2, 64, 64, generator=gen)
+    dst, src = torch.tensor([4, 0, 2], **I32), torch.tensor([7, 7, -1], **I32)
+    pool = states.cuda()
+    gdr.copy_states(pool, dst.cuda(), src.cuda(), source.cuda())
+    assert torch.equal(pool.cpu(), copied(states, dst, src, source))
+    pool = states.cuda()
+    gdr.copy_states(pool[:2], torch.tensor([0, 1], **I32), torch.tensor([1, 2], **I32), pool[2:])
+    assert torch.equal(pool.cpu(), torch.cat([states[3:5], states[2:]]))
+
+
+# ---------------------------------------------------------------- together
+def test_serving_from_prefill_to_release():
+    """Prefill, placement in the pool, decode, verification of trees, acceptance, a fork and a
+    compaction, against 64 bits over the whole run."""
+    Hq, Hv, K, V, N = 2, 4, 128, 128, 3
+    lens = [70, 5, 129]
+    x = ref.make(0, 0, Hq, Hv, K, V, BF, lens, seed=20)
+    d = ref.cuda(x)
+    _, final = gdr.chunk_gated_delta_rule(d["q"], d["k"], d["v"], d["g"], d["beta"], cu_seqlens=d["cu"],
+                                          output_final_state=True)
+    slots = torch.tensor([6, 1, 3], **I32)
+    pool = torch.full((8, Hv, K, V), float("nan"), device="cuda")
+    gdr.copy_states(pool, slots.cuda(), torch.arange(N, **I32, device="cuda"), final)
+    zero = dict(x, states=torch.zeros(N, Hv, K, V), slots=torch.arange(N))
+    _, want, X = ref.recurrent(zero)
+    # the prefill's states carry its own error (two bf16 pieces per product: about 2e-5 of the
+    # rms); later tokens do not enlarge it
+    bar = 1e-3 * float(want.square().mean().sqrt())
+    assert float((pool[slots.long()].cpu() - want).abs().max()) <= bar
+    for t in range(3):
+        y = ref.make(N, 1, Hq, Hv, K, V, BF, seed=21 + t)
+        e = dict(ref.cuda(y), states=pool, slots=slots.cuda())
+        o = run_recurrent(e)
+        o_want, want, _ = ref.recurrent(dict(y, states=want, slots=torch.arange(N)))
+        assert float((o.cpu() - o_want).abs().max()) <= bar
+    n = 13
+    y = ref.make(N, n, Hq, Hv, K, V, BF, seed=30)
+    y["parents"] = torch.tensor([shape_of("random", n, torch.Generator().manual_seed(j)) for j in range(N)], **I32)
+    y["accepted"] = torch.tensor([12, -1, 5], **I32)
+    e = dict(ref.cuda(y), states=pool, slots=slots.cuda())
+    o = run_tree(e)
+    ref_in = dict(y, states=want, slots=torch.arange(N))
+    o_want, _ = ref.tree(ref_in, y["parents"])
+    assert float((o.cpu() - o_want).abs().max()) <= bar
+    run_accept(e)
+    want, _ = ref.accept(ref_in, y["parents"], y["accepted"])
+    assert float((pool[slots.long()].cpu() - want).abs().max()) <= bar
+    # fork sequence 0 into slots 0 and 2, release sequence 1, move sequence 2 down to its slot
+    gdr.copy_states(pool, torch.tensor([0, 2, 1, 3], **I32), torch.tensor([6, 6, 3, -1], **I32))
+    for s, j in ((0, 0), (2, 0), (6, 0), (1, 2)):
+        assert float((pool[s].cpu() - want[j]).abs().max()) <= bar
+    assert bool((pool[3] == 0).all())
+
+
+def test_captured_calls_replay_as_eager_ones():
+    """All four in one graph, replayed with new inputs and eager work in between."""
+    N, n, Hq, Hv, K, V = 3, 9, 2, 4, 64, 128
+    def fresh(seed):
+        x = ref.make(N, 1, Hq, Hv, K, V, BF, seed=seed)
+        t = ref.make(N, n, Hq, Hv, K, V, BF, seed=seed + 50)
+        gen = torch.Generator().manual_seed(seed)
+        t["parents"] = torch.tensor([shape_of("random", n, gen) for _ in range(N)], **I32)
+        t["accepted"] = torch.randint(-1, n, (N,), generator=gen, dtype=torch.int32)
+        t["slots"] = x["slots"]
+        m = dict(dst=torch.randperm(5, generator=gen)[:4].to(torch.int32),
+                 src=torch.randint(-1, 5, (4,), generator=gen, dtype=torch.int32))
+        return ref.cuda(x), ref.cuda(t), ref.cuda(m)
+    def go(x, t, m, o, ot):
+        run_recurrent(x, out=o)
+        t = dict(t, states=x["states"])
+        run_tree(t, out=ot)
+        run_accept(t)
+        gdr.copy_states(x["states"], m["dst"], m["src"])
+    x, t, m = fresh(1)
+    o, ot = torch.zeros(N, 1, Hv, V, device="cuda"), torch.zeros(N, n, Hv, V, device="cuda")
+    go(*fresh(7), o, ot)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(x, t, m, o, ot)
+    for rep in range(3):
+        say("replay", rep)
+        for have, new in zip((x, t, m), fresh(10 + rep)):
+            for name, v in new.items():
+                if v is not None:
+                    have[name].copy_(v)
+        e = [{a: b.clone() if b is not None else None for a, b in s.items()} for s in (x, t, m)]
+        oe, ote = torch.full_like(o, 3), torch.full_like(ot, 3)
+        go(*e, oe, ote)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, oe) and torch.equal(ot, ote) and torch.equal(x["states"], e[0]["states"])
+    del graph
+
+
+def test_calls_on_two_streams():
+    """The call's own stream is the current one, and calls on several streams do not meet."""
+    xs = [ref.make(4, 2, 2, 4, 128, 128, BF, seed=s) for s in (1, 2)]
+    ds = [ref.cuda(x) for x in xs]
+    for x in xs:
+        x["parents"] = torch.tensor([[-1, 0]] * 4, **I32)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = []
+    for d, s, x in zip(ds, streams, xs):
+        with torch.cuda.stream(s):
+            p = x["parents"].cuda()
+            outs.append((run_tree(dict(d, parents=p)), run_recurrent(d)))
+    torch.cuda.synchronize()
+    for x, d, (ot, o) in zip(xs, ds, outs):
+        o_want, s_want, X = ref.recurrent(x)
+        ref.near(o, o_want, 2, 128, X)
+        ref.near(ot, o_want, 2, 128, X)
+        ref.near(d["states"], s_want, 2, 128, X)
+
+
+def test_the_tensors_device_is_used_whatever_the_current_one(monkeypatch):
+    """A call on another device than the current one makes that device current for its launch."""
+    from gated_delta_rule_85_amd import pool
+    seen = []
+    monkeypatch.setattr(pool.torch.cuda, "current_device", lambda: 1)
+    class Guard:
+        def __init__(self, dev):
+            seen.append(dev)
+        def __enter__(self):
+            pass
+        def __exit__(self, *a):
+            pass
+    monkeypatch.setattr(pool.torch.cuda, "device", Guard)
+    d = ref.cuda(ref.make(1, 1, 1, 1, 64, 64, F32))
+    run_recurrent(d)
+    assert seen == [d["q"].device]
+
+
+def test_errors_of_the_library_name_their_entry_point():
+    a = _lib.PoolArgs()
+    with pytest.raises(_lib.GdrError, match="gdr_step"):
+        _lib.step(a, 0)

@@ -1,0 +1,246 @@
+"""Refusals of the operators on a pool of states, without a GPU: everything here ends
+before anything is launched."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import gated_delta_rule_85_amd as gdr
+from gated_delta_rule_85_amd import _lib
+from pool_reference import make
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def tree_inputs(**kw):
+    x = make(2, 3, 2, 4, 64, 128, **kw)
+    x["parents"] = torch.tensor([[-1, 0, 0], [-1, -1, 1]], dtype=torch.int32)
+    x["accepted"] = torch.tensor([2, -1], dtype=torch.int32)
+    return x
+
+
+def call(op, x):
+    x = dict(x)
+    cu = x.pop("cu")
+    if op == "recurrent":
+        return gdr.recurrent_gated_delta_rule(x["q"], x["k"], x["v"], x["g"], x["beta"], x["states"], cu_seqlens=cu,
+                                              slots=x["slots"], output_dtype=x.get("output_dtype", torch.float32),
+                                              out=x.get("out"))
+    if op == "tree":
+        return gdr.tree_gated_delta_rule(x["q"], x["k"], x["v"], x["g"], x["beta"], x["parents"], x["states"],
+                                         cu_seqlens=cu, slots=x["slots"])
+    return gdr.tree_gated_delta_rule_accept(x["k"], x["v"], x["g"], x["beta"], x["parents"], x["accepted"], x["states"],
+                                            cu_seqlens=cu, slots=x["slots"])
+
+
+@pytest.mark.parametrize("op", ["recurrent", "tree", "accept"])
+@pytest.mark.parametrize("name,change", [
+    ("v tokens", lambda x: x.update(v=x["v"][:, :2])),
+    ("q shape", lambda x: x.update(q=x["q"][:, :, :1], k=x["k"][:, :, 0])),
+    ("v dtype", lambda x: x.update(v=x["v"].float())),
+    ("fp16", lambda x: x.update(q=x["q"].half(), k=x["k"].half(), v=x["v"].half())),
+    ("g shape", lambda x: x.update(g=x["g"][:, :, :2])),
+    ("beta shape", lambda x: x.update(beta=x["beta"][:1])),
+    ("states dtype", lambda x: x.update(states=x["states"].bfloat16())),
+    ("states heads", lambda x: x.update(states=x["states"][:, :2])),
+    ("states transposed", lambda x: x.update(states=x["states"].mT.contiguous().mT)),
+    ("states unaligned slots", lambda x: x.update(states=torch.zeros(4, 4 * 64 * 128 + 2)[:, :4 * 64 * 128].view(4, 4, 64, 128))),
+    ("states expanded", lambda x: x.update(states=x["states"][:1].expand(4, -1, -1, -1))),
+    ("slots past the pool", lambda x: x.update(slots=torch.tensor([0, 4], dtype=torch.int32))),
+    ("slots below -1", lambda x: x.update(slots=torch.tensor([0, -2], dtype=torch.int32))),
+    ("slots dtype", lambda x: x.update(slots=x["slots"].long())),
+    ("slots count", lambda x: x.update(slots=x["slots"][:1])),
+    ("too few slots", lambda x: x.update(slots=None, states=x["states"][:1])),
+    ("cu with a batch", lambda x: x.update(cu=torch.tensor([0, 3], dtype=torch.int32))),
+    ("host tensors", lambda x: None),
+])
+def test_arguments_are_refused(op, name, change):
+    x = tree_inputs()
+    change(x)
+    with pytest.raises(ValueError):
+        call(op, x)
+
+
+@pytest.mark.parametrize("op", ["recurrent", "accept"])
+def test_a_slot_named_twice_on_the_host_is_refused(op):
+    x = tree_inputs()
+    x["slots"] = torch.tensor([1, 1], dtype=torch.int32)
+    with pytest.raises(ValueError, match="twice"):
+        call(op, x)
+    x["slots"] = torch.tensor([-1, -1], dtype=torch.int32)  # padding: refused for the device alone
+    with pytest.raises(ValueError, match="GPU"):
+        call(op, x)
+
+
+@pytest.mark.parametrize("op", ["tree", "accept"])
+@pytest.mark.parametrize("parents", [
+    torch.tensor([[-1, 0, 2], [-1, 0, 0]], dtype=torch.int32),  # its own
+    torch.tensor([[-1, 0, 0], [1, -1, 0]], dtype=torch.int32),  # a later node
+    torch.tensor([[-1, 0, -2], [-1, 0, 0]], dtype=torch.int32),
+    torch.tensor([[-1, 0, 0]], dtype=torch.int32),
+    torch.tensor([[-1, 0, 0], [-1, 0, 0]]),
+])
+def test_parents_are_refused(op, parents):
+    x = tree_inputs()
+    x["parents"] = parents
+    with pytest.raises(ValueError, match="parent"):
+        call(op, x)
+
+
+def test_packed_parents_are_counted_within_their_tree():
+    x = make(0, 0, 2, 4, 64, 64, lens=[2, 0, 3])
+    x["accepted"] = torch.tensor([0, -1, 2], dtype=torch.int32)
+    x["parents"] = torch.tensor([[-1, 0, -1, 0, 1]], dtype=torch.int32)
+    for op in ("tree", "accept"):
+        with pytest.raises(ValueError, match="GPU"):
+            call(op, x)
+    x["parents"] = torch.tensor([[-1, 0, -1, 2, 1]], dtype=torch.int32)
+    for op in ("tree", "accept"):
+        with pytest.raises(ValueError, match="parent"):
+            call(op, x)
+
+
+def test_trees_of_more_than_64_nodes_are_refused():
+    x = make(1, 65, 1, 1, 64, 64)
+    x["parents"], x["accepted"] = torch.full((1, 65), -1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    packed = make(0, 0, 1, 1, 64, 64, lens=[1, 65])
+    packed["parents"], packed["accepted"] = torch.full((1, 66), -1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for op in ("tree", "accept"):
+        for y in (x, packed):
+            with pytest.raises(ValueError, match="64"):
+                call(op, y)
+
+
+@pytest.mark.parametrize("accepted", [torch.tensor([3, 0]), torch.tensor([0, -2]), torch.tensor([0])])
+def test_accepted_is_refused(accepted):
+    x = tree_inputs()
+    x["accepted"] = accepted.to(torch.int32)
+    with pytest.raises(ValueError, match="accepted"):
+        call("accept", x)
+
+
+@pytest.mark.parametrize("op", ["recurrent", "tree", "accept"])
+@pytest.mark.parametrize("name", ["k", "v", "g", "beta", "states"])
+def test_gradients_are_refused(op, name):
+    x = tree_inputs()
+    x[name].requires_grad_()
+    with pytest.raises(ValueError, match="no gradient"):
+        call(op, x)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        call(op, x)
+
+
+def test_offsets_on_the_host_are_refused():
+    x = make(0, 0, 1, 1, 64, 64, lens=[2, 3])
+    for cu in ([0, 2, 4], [1, 2, 5], [0, 6, 5]):
+        x["cu"] = torch.tensor(cu, dtype=torch.int32)
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            call("recurrent", x)
+
+
+I32 = dict(dtype=torch.int32)
+
+
+@pytest.mark.parametrize("name,args", [
+    ("dtype", (torch.zeros(4, 1, 64, 64).bfloat16(), torch.zeros(1, **I32), torch.zeros(1, **I32))),
+    ("three dimensions", (torch.zeros(4, 64, 64), torch.zeros(1, **I32), torch.zeros(1, **I32))),
+    ("dst range", (torch.zeros(4, 1, 64, 64), torch.tensor([4], **I32), torch.zeros(1, **I32))),
+    ("src range", (torch.zeros(4, 1, 64, 64), torch.zeros(1, **I32), torch.tensor([4], **I32))),
+    ("src below -1", (torch.zeros(4, 1, 64, 64), torch.zeros(1, **I32), torch.tensor([-2], **I32))),
+    ("lengths", (torch.zeros(4, 1, 64, 64), torch.zeros(2, **I32), torch.zeros(1, **I32))),
+    ("int64", (torch.zeros(4, 1, 64, 64), torch.zeros(1).long(), torch.zeros(1).long())),
+    ("4097 entries", (torch.zeros(4, 1, 64, 64), torch.zeros(4097, **I32), torch.zeros(4097, **I32))),
+    ("source shape", (torch.zeros(4, 1, 64, 64), torch.zeros(1, **I32), torch.zeros(1, **I32), torch.zeros(4, 1, 64, 128))),
+    ("source layers", (torch.zeros(2, 4, 1, 64, 64), torch.zeros(1, **I32), torch.zeros(1, **I32), torch.zeros(3, 4, 1, 64, 64))),
+    ("expanded layers", (torch.zeros(1, 4, 1, 64, 64).expand(2, -1, -1, -1, -1), torch.zeros(1, **I32), torch.zeros(1, **I32))),
+    ("host tensors", (torch.zeros(4, 1, 64, 64), torch.zeros(1, **I32), torch.zeros(1, **I32))),
+])
+def test_copies_are_refused(name, args):
+    with pytest.raises(ValueError):
+        gdr.copy_states(*args)
+
+
+def test_a_source_that_overlaps_the_pool_is_refused():
+    pool = torch.zeros(6, 1, 64, 64)
+    with pytest.raises(ValueError, match="overlaps"):
+        gdr.copy_states(pool[:4], torch.zeros(1, **I32), torch.zeros(1, **I32), pool[2:])
+    with pytest.raises(ValueError, match="GPU"):  # apart
+        gdr.copy_states(pool[:3], torch.zeros(1, **I32), torch.zeros(1, **I32), pool[3:])
+    with pytest.raises(ValueError, match="GPU"):  # the same pool
+        gdr.copy_states(pool, torch.zeros(1, **I32), torch.zeros(1, **I32), pool)
+
+
+# ---------------------------------------------------------------- the C entry points
+@pytest.mark.parametrize("st,name", [(_lib.PoolArgs, "gdr_pool_args"), (_lib.CopyArgs, "gdr_copy_args")])
+def test_struct_layouts_match_the_header(tmp_path, st, name):
+    names = [f[0] for f in st._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("#include <stdio.h>\n#include <stddef.h>\n#include \"gdr.h\"\nint main(void){\n"
+                   + 'printf("%%zu\\n", sizeof(%s));\n' % name
+                   + "".join('printf("%%zu\\n", offsetof(%s, %s));\n' % (name, f) for f in names) + "return 0;}\n")
+    exe = str(tmp_path / "layout")
+    subprocess.run(["gcc", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROOT, "include"), "-I/opt/rocm/include",
+                    str(src), "-o", exe], check=True)
+    out = [int(v) for v in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()]
+    assert out == [ctypes.sizeof(st)] + [getattr(st, f).offset for f in names]
+
+
+def test_limits_match_the_header():
+    text = open(os.path.join(ROOT, "include", "gdr.h")).read()
+    assert "#define GDR_TREE_MAX %d " % _lib.TREE_MAX in text
+    assert "#define GDR_COPY_MAX %d " % _lib.COPY_MAX in text
+
+
+def pool_args(**kw):
+    a = _lib.PoolArgs(2, 3, 2, 4, 128, 128, 0, 5, 4 * 128 * 128, 256, 256, 512, 768, 768, 1536, _lib.BF16, _lib.F32,
+                      0.1, 16, 16, 16, 16, 16, None, 16, 16, 16, 16, 16)
+    for n, v in kw.items():
+        setattr(a, n, v)
+    return a
+
+
+ENTRIES = ["gdr_step", "gdr_tree", "gdr_tree_accept"]
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), -1), (dict(T=-1), -1), (dict(H_v=3), -1), (dict(H_q=0), -1), (dict(K=96), -2), (dict(V=32), -2),
+    (dict(dtype=2), -2), (dict(B=2, cu_seqlens=16, n_seq=1), -1), (dict(B=1, cu_seqlens=16, n_seq=-1), -1),
+    (dict(n_slots=0), -1), (dict(n_slots=1, slots=None), -1), (dict(slot_stride=4 * 128 * 128 - 4), -1),
+    (dict(slot_stride=4 * 128 * 128 + 2), -1), (dict(k_row=257), -1), (dict(v_row=-8), -1), (dict(v_batch=4), -1),
+    (dict(k=None), -1), (dict(v=24), -1), (dict(g=None), -1), (dict(beta=None), -1), (dict(states=None), -1),
+    (dict(states=8), -1), (dict(B=1 << 20, H_v=8), -1), (dict(B=1, T=1 << 31), -1),
+    (dict(T=0), 0), (dict(B=0), 0), (dict(B=1, cu_seqlens=16, n_seq=0), 0),
+])
+def test_pool_arguments_are_checked_before_any_launch(entry, kw, code):
+    assert getattr(_lib.lib, entry)(ctypes.byref(pool_args(**kw)), None) == code
+
+
+def test_entry_specific_arguments_are_checked():
+    rc = lambda entry, **kw: getattr(_lib.lib, entry)(ctypes.byref(pool_args(**kw)), None)  # noqa: E731
+    for entry in ENTRIES:
+        assert getattr(_lib.lib, entry)(None, None) == -1
+    for entry in ("gdr_step", "gdr_tree"):
+        for kw in (dict(q=None), dict(o=None), dict(q=8), dict(o=8), dict(q_row=4), dict(q_batch=-8)):
+            assert rc(entry, **kw) == -1, (entry, kw)
+        assert rc(entry, out_dtype=5) == -2
+    for entry in ("gdr_tree", "gdr_tree_accept"):
+        assert rc(entry, parents=None) == -1 and rc(entry, T=65) == -1
+    assert rc("gdr_tree_accept", accepted=None) == -1
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), -1), (dict(n=4097), -1), (dict(n_dst=0), -1), (dict(n_src=0), -1), (dict(slot_bytes=24), -1),
+    (dict(dst_stride=48), -1), (dict(src_stride=72), -1), (dict(layers=-1), -1), (dict(dst_layer_stride=8), -1),
+    (dict(layers=2, dst_layer_stride=0), -1), (dict(layers=2, dst_layer_stride=128), -1), (dict(src_layer_stride=-16), -1),
+    (dict(dst=None), -1), (dict(src=None), -1), (dict(states=None), -1), (dict(source=None), -1), (dict(states=8), -1),
+    (dict(n=0), 0), (dict(layers=0), 0), (dict(slot_bytes=0), 0),
+])
+def test_copy_arguments_are_checked_before_any_launch(kw, code):
+    a = _lib.CopyArgs(2, 4, 4, 64, 64, 64, 1, 0, 0, 16, 16, 16, 16)
+    for n, v in kw.items():
+        setattr(a, n, v)
+    assert _lib.lib.gdr_copy_states(ctypes.byref(a), None) == code
+    assert _lib.lib.gdr_copy_states(None, None) == -1
