@@ -68,6 +68,20 @@ __device__ __forceinline__ bool slot_taken(const PoolParams &p, int j, int slot)
     return __ballot(taken) != 0;
 }
 
+// Workgroup id -> head such that an XCD takes runs of 8 consecutive heads (the hardware
+// deals workgroups to the 8 XCDs round robin).  A last partial run of 64 stays as dealt.
+__device__ __forceinline__ int xcd_runs(int id, int nb) {
+    return (id | 63) < nb ? (id & ~63) | (id & 7) << 3 | (id >> 3 & 7) : id;
+}
+
+// state values are read and written once a call
+__device__ __forceinline__ f32x4 load4_once(const float *p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
+}
+__device__ __forceinline__ void store4_once(float *p, f32x4 x) {
+    __builtin_nontemporal_store(x, reinterpret_cast<f32x4 *>(p));
+}
+
 // four values at a column, as the output's type
 __device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
 __device__ __forceinline__ void store4(bf16 *p, f32x4 x) {

@@ -46,10 +46,8 @@ template <typename In, int R, bool OUT> struct Token {
 template <typename In, typename Out, int K, bool ACCEPT>
 __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     constexpr int R = K / 8;
-    const int item = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6)));
-    const int n_vt = V >> 5, unit = item / n_vt, vt = item - unit * n_vt;
+    const int unit = xcd_runs(blockIdx.x, gridDim.x), vt = __builtin_amdgcn_readfirstlane(wave_id());
     const int j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
-    if (j >= p.n_seq) return;
     const int l = lane_id(), col = vt * 32 + 4 * (l & 7), row0 = R * (l >> 3);
     int64_t bos, eos;
     token_range(p, j, bos, eos);
@@ -81,7 +79,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     float *h0 = p.states + (int64_t)slot * p.slot_stride + ((int64_t)hv * K + row0) * V + col;
     f32x4 h[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) h[r] = load4(h0 + r * V);
+    for (int r = 0; r < R; ++r) h[r] = load4_once(h0 + r * V);
 
     const In *kp = reinterpret_cast<const In *>(p.k) + hq * K + row0;
     const In *qp = reinterpret_cast<const In *>(p.q) + hq * K + row0;
@@ -139,15 +137,14 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) store4(h0 + r * V, h[r]);
+    for (int r = 0; r < R; ++r) store4_once(h0 + r * V, h[r]);
 }
 
 template <typename In, typename Out, bool ACCEPT>
 hipError_t launch(int K, int V, const PoolParams &p, hipStream_t s) {
-    const int64_t waves = (int64_t)p.n_seq * p.Hv * (V / 32);
     // a head's waves in one workgroup share its k and q rows in the L1
     const int block = 64 * (V / 32);
-    const dim3 grid((uint32_t)(waves / (V / 32)));
+    const dim3 grid((uint32_t)p.n_seq * p.Hv);
     if (K == 128)
         launch_k(gdr_step_kernel<In, Out, 128, ACCEPT>, grid, dim3(block), 0, s, p, V);
     else

@@ -23,28 +23,31 @@ from . import _lib
 from .api import _DT, _c, check_offsets
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _refuse_gradients(*tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()")
+def _refuse_gradients():
+    raise ValueError("the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()")
 
 
-def _same_device(dev, *tensors):
+def _one_gpu(dev, *tensors):
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on the GPU")
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t.device != dev:
             raise ValueError("all tensors must be on one GPU")
 
 
-def _rows(x):
-    """x with the strides of its tokens and batch rows in elements, copied if the
-    kernels cannot read it in place: they need one token's [H, D] contiguous and
-    rows at multiples of 16 bytes."""
+def _rows(x, per16):
+    """x with the elements between its tokens and between its batch rows, copied if the
+    kernels cannot read it in place: they need one token's [H, D] contiguous and rows at
+    multiples of 16 bytes (per16 elements)."""
     B, T, H, D = x.shape
     batch, row, head, one = x.stride()
-    per16 = 16 // x.element_size()
     if B < 2:
         batch = 0
     if T < 2:
@@ -56,17 +59,25 @@ def _rows(x):
 
 
 def _check_tokens(q, k, v, g, beta, cu_seqlens):
-    if k.dim() != 4 or v.dim() != 4 or v.shape[:2] != k.shape[:2] or (q is not None and q.shape != k.shape):
+    """The sizes B, T, H_q, K, H_v, V and the number of sequences."""
+    dtype = k.dtype
+    if k.dim() != 4 or v.dim() != 4 or (q is not None and q.shape != k.shape):
         raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
-    if k.dtype not in _DT or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    B, T, H_q, K = k.shape
+    B_v, T_v, H_v, V = v.shape
+    if B_v != B or T_v != T:
+        raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
+    if dtype not in _DT or v.dtype != dtype or (q is not None and q.dtype != dtype):
         raise ValueError("q, k, v must share one dtype, bfloat16 or float32")
-    if g.shape != v.shape[:3] or beta.shape != v.shape[:3]:
+    if g.shape != (B, T, H_v) or beta.shape != (B, T, H_v):
         raise ValueError("g and beta must be [B,T,H_v]")
-    if cu_seqlens is not None:
-        if k.shape[0] != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be int32 [N+1] with B == 1")
-        if not cu_seqlens.is_cuda:
-            check_offsets(cu_seqlens, k.shape[1])
+    if cu_seqlens is None:
+        return B, T, H_q, K, H_v, V, B
+    if B != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [N+1] with B == 1")
+    if not cu_seqlens.is_cuda:
+        check_offsets(cu_seqlens, T)
+    return B, T, H_q, K, H_v, V, cu_seqlens.numel() - 1
 
 
 def _check_states(states, H_v, K, V, name="states"):
@@ -85,19 +96,15 @@ def _indices(x, n, what, lo, hi):
         raise ValueError("%s must be int32 [%d]" % (what, n))
     if not x.is_cuda and n and (int(x.min()) < lo or int(x.max()) >= hi):
         raise ValueError("%s out of range [%d, %d)" % (what, lo, hi))
-    return x
 
 
-def _check_slots(slots, n_seq, n_slots):
+def _check_slots(slots, n_seq, n_slots, distinct):
     if slots is None:
         if n_slots < n_seq:
             raise ValueError("states has %d slots for %d sequences" % (n_slots, n_seq))
         return
     _indices(slots, n_seq, "slots", -1, n_slots)
-
-
-def _check_distinct(slots):
-    if slots is not None and not slots.is_cuda:
+    if distinct and not slots.is_cuda:
         used = slots[slots >= 0]
         if used.unique().numel() != used.numel():
             raise ValueError("slots names a slot twice")
@@ -108,27 +115,28 @@ def _check_parents(parents, B, T, cu_seqlens):
         raise ValueError("parents must be int32 [B,T]")
     if cu_seqlens is None and T > _lib.TREE_MAX:
         raise ValueError("a tree has at most %d nodes" % _lib.TREE_MAX)
-    if cu_seqlens is not None and not cu_seqlens.is_cuda and \
-            int((cu_seqlens[1:] - cu_seqlens[:-1]).amax()) > _lib.TREE_MAX:
-        raise ValueError("a tree has at most %d nodes" % _lib.TREE_MAX)
-    if not parents.is_cuda and (cu_seqlens is None or not cu_seqlens.is_cuda):
+    lens = None
+    if cu_seqlens is not None and not cu_seqlens.is_cuda:
+        lens = (cu_seqlens[1:] - cu_seqlens[:-1]).long()
+        if lens.numel() and int(lens.max()) > _lib.TREE_MAX:
+            raise ValueError("a tree has at most %d nodes" % _lib.TREE_MAX)
+    if not parents.is_cuda and (cu_seqlens is None or lens is not None):
         at = torch.arange(T, dtype=torch.int32).expand(B, T)
-        if cu_seqlens is not None:
-            lens = (cu_seqlens[1:] - cu_seqlens[:-1]).long()
+        if lens is not None:
             at = at - torch.repeat_interleave(cu_seqlens[:-1], lens)
         if bool((parents < -1).any()) or bool((parents >= at).any()):
             raise ValueError("a node's parent is -1 or an earlier node of its tree")
 
 
-def _output(out, output_dtype, shape, dev, *inputs):
+def _output(out, output_dtype, v, *inputs):
     if out is None:
         if output_dtype not in _DT:
             raise ValueError("output_dtype must be bfloat16 or float32")
-        return torch.empty(shape, dtype=output_dtype, device=dev)
-    if out.shape != shape or out.dtype not in _DT or not out.is_contiguous() or out.data_ptr() % 16:
+        return torch.empty_like(v, dtype=output_dtype, memory_format=torch.contiguous_format)
+    if out.shape != v.shape or out.dtype not in _DT or not out.is_contiguous() or out.data_ptr() % 16:
         raise ValueError("out must be contiguous [B,T,H_v,V], bfloat16 or float32, 16-byte aligned")
-    _same_device(dev, out)
-    for x in inputs:
+    _one_gpu(v.device, out)
+    for x in (v,) + inputs:
         if _overlap(out, x):
             raise ValueError("out overlaps an input")
     return out
@@ -146,29 +154,41 @@ def _overlap(a, b):
 
 
 def _launch(call, args, dev):
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        call(args, stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        call(args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            call(args, stream)
+            call(args, _raw_stream(index))
 
 
-def _pool_call(call, q, k, v, g, beta, parents, accepted, states, scale, cu_seqlens, slots, o):
-    dev = states.device
-    B, T, H_q, K = k.shape
-    H_v, V = v.shape[2], v.shape[3]
-    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    k, k_row, k_batch = _rows(k)
-    v, v_row, v_batch = _rows(v)
-    q, q_row, q_batch = (None, 0, 0) if q is None else _rows(q)
+def _on(x, dev):
+    """An index array where the kernels read it."""
+    if x.device != dev:
+        x = x.to(dev)
+    return x.contiguous()
+
+
+def _pool_call(call, sizes, q, k, v, g, beta, parents, accepted, states, scale, cu_seqlens, slots, o):
+    B, T, H_q, K, H_v, V, n_seq = sizes
+    dev, dtype = states.device, _DT[k.dtype]
+    per16 = 8 if dtype == _lib.BF16 else 4
+    k, k_row, k_batch = _rows(k, per16)
+    v, v_row, v_batch = _rows(v, per16)
+    q, q_row, q_batch = (None, 0, 0) if q is None else _rows(q, per16)
     g, beta = _c(g, torch.float32), _c(beta, torch.float32)
-    on = lambda x: None if x is None else _c(x).to(dev)  # noqa: E731
-    cu_seqlens, slots, parents, accepted = on(cu_seqlens), on(slots), on(parents), on(accepted)
+    if cu_seqlens is not None:
+        cu_seqlens = _on(cu_seqlens, dev)
+    if slots is not None:
+        slots = _on(slots, dev)
+    if parents is not None:
+        parents = _on(parents, dev)
+    if accepted is not None:
+        accepted = _on(accepted, dev)
     args = _lib.PoolArgs(
         B, T, H_q, H_v, K, V, n_seq, states.shape[0], states.stride(0), q_row, k_row, v_row, q_batch, k_batch, v_batch,
-        _DT[k.dtype], _lib.F32 if o is None else _DT[o.dtype], float(scale), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-        _ptr(beta), _ptr(cu_seqlens), _ptr(slots), _ptr(parents), _ptr(accepted), _ptr(states), _ptr(o))
+        dtype, _lib.F32 if o is None else _DT[o.dtype], scale, _ptr(q), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+        beta.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _ptr(parents), _ptr(accepted), states.data_ptr(), _ptr(o))
     _launch(call, args, dev)
 
 
@@ -191,19 +211,17 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=
     zero; so is a sequence that names a slot which an earlier one has.  ``out``: a
     contiguous tensor to write; rows that belong to no sequence are left as they are.
     """
-    _check_tokens(q, k, v, g, beta, cu_seqlens)
-    B, T, K = q.shape[0], q.shape[1], q.shape[3]
-    _check_states(states, v.shape[2], K, v.shape[3])
-    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _check_slots(slots, n_seq, states.shape[0])
-    _check_distinct(slots)
-    _refuse_gradients(q, k, v, g, beta, states)
-    if not states.is_cuda:
-        raise ValueError("inputs must be on the GPU")
-    _same_device(states.device, q, k, v, g, beta)
-    o = _output(out, output_dtype, v.shape, states.device, q, k, v, g, beta, states)
-    _pool_call(_lib.step, q, k, v, g, beta, None, None, states, K ** -0.5 if scale is None else scale, cu_seqlens,
-               slots, o)
+    sizes = _check_tokens(q, k, v, g, beta, cu_seqlens)
+    _, _, _, K, H_v, V, n_seq = sizes
+    _check_states(states, H_v, K, V)
+    _check_slots(slots, n_seq, states.shape[0], True)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
+                                    or beta.requires_grad or states.requires_grad):
+        _refuse_gradients()
+    _one_gpu(states.device, q, k, v, g, beta)
+    o = _output(out, output_dtype, v, q, k, g, beta, states)
+    _pool_call(_lib.step, sizes, q, k, v, g, beta, None, None, states, K ** -0.5 if scale is None else float(scale),
+               cu_seqlens, slots, o)
     return o
 
 
@@ -222,18 +240,18 @@ def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seql
     than 64 nodes rows of NaN.  The other arguments are those of
     :func:`recurrent_gated_delta_rule`.
     """
-    _check_tokens(q, k, v, g, beta, cu_seqlens)
-    B, T, K = q.shape[0], q.shape[1], q.shape[3]
+    sizes = _check_tokens(q, k, v, g, beta, cu_seqlens)
+    B, T, _, K, H_v, V, n_seq = sizes
     _check_parents(parents, B, T, cu_seqlens)
-    _check_states(states, v.shape[2], K, v.shape[3])
-    _check_slots(slots, B if cu_seqlens is None else cu_seqlens.numel() - 1, states.shape[0])
-    _refuse_gradients(q, k, v, g, beta, states)
-    if not states.is_cuda:
-        raise ValueError("inputs must be on the GPU")
-    _same_device(states.device, q, k, v, g, beta)
-    o = _output(out, output_dtype, v.shape, states.device, q, k, v, g, beta, states)
-    _pool_call(_lib.tree, q, k, v, g, beta, parents, None, states, K ** -0.5 if scale is None else scale, cu_seqlens,
-               slots, o)
+    _check_states(states, H_v, K, V)
+    _check_slots(slots, n_seq, states.shape[0], False)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
+                                    or beta.requires_grad or states.requires_grad):
+        _refuse_gradients()
+    _one_gpu(states.device, q, k, v, g, beta)
+    o = _output(out, output_dtype, v, q, k, g, beta, states)
+    _pool_call(_lib.tree, sizes, q, k, v, g, beta, parents, None, states, K ** -0.5 if scale is None else float(scale),
+               cu_seqlens, slots, o)
     return o
 
 
@@ -247,20 +265,32 @@ def tree_gated_delta_rule_accept(k, v, g, beta, parents, accepted, states, cu_se
     each tree, or -1 for none (the state then stays as it is).  A sequence that names
     a slot which an earlier one has is skipped.
     """
-    _check_tokens(None, k, v, g, beta, cu_seqlens)
-    B, T, K = k.shape[0], k.shape[1], k.shape[3]
+    sizes = _check_tokens(None, k, v, g, beta, cu_seqlens)
+    B, T, _, K, H_v, V, n_seq = sizes
     _check_parents(parents, B, T, cu_seqlens)
-    _check_states(states, v.shape[2], K, v.shape[3])
-    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _check_slots(slots, n_seq, states.shape[0])
-    _check_distinct(slots)
+    _check_states(states, H_v, K, V)
+    _check_slots(slots, n_seq, states.shape[0], True)
     _indices(accepted, n_seq, "accepted", -1, _lib.TREE_MAX if cu_seqlens is not None else T)
-    _refuse_gradients(k, v, g, beta, states)
-    if not states.is_cuda:
-        raise ValueError("inputs must be on the GPU")
-    _same_device(states.device, k, v, g, beta)
-    _pool_call(_lib.tree_accept, None, k, v, g, beta, parents, accepted, states, 1.0, cu_seqlens, slots, None)
+    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad or g.requires_grad or beta.requires_grad
+                                    or states.requires_grad):
+        _refuse_gradients()
+    _one_gpu(states.device, k, v, g, beta)
+    _pool_call(_lib.tree_accept, sizes, None, k, v, g, beta, parents, accepted, states, 1.0, cu_seqlens, slots, None)
     return states
+
+
+def _check_pool(x, name):
+    """One layer's pool, or [layers, ...] of them."""
+    if x.dim() == 5:
+        n, inner = x.shape[0], x.shape[2] * x.shape[3] * x.shape[4]
+        if n > 1 and (x.stride(0) % 4 or x.stride(0) < inner):
+            raise ValueError("a slot of %s must be contiguous and 16-byte aligned" % name)
+        if n > 0:
+            _check_states(x[0], None, None, None, name)
+    elif x.dim() == 4:
+        _check_states(x, None, None, None, name)
+    else:
+        raise ValueError("%s must be float32 [n_slots,H_v,K,V] or [layers,n_slots,H_v,K,V]" % name)
 
 
 def copy_states(states, dst, src, source=None):
@@ -278,40 +308,33 @@ def copy_states(states, dst, src, source=None):
     [n].  ``source`` may be another pool, such as the final states of a prefill; it
     must not overlap ``states`` in memory, unless it is the same pool.
     """
-    pools = [states] if source is None else [states, source]
-    for x, name in zip(pools, ("states", "source")):
-        if x.dim() not in (4, 5):
-            raise ValueError("%s must be float32 [n_slots,H_v,K,V] or [layers,n_slots,H_v,K,V]" % name)
-        if x.dim() == 5 and x.shape[0] > 0:
-            _check_states(x[0], None, None, None, name)
-            if x.shape[0] > 1 and (x.stride(0) % 4 or x.stride(0) < x[0, 0].numel()):
-                raise ValueError("a slot of %s must be contiguous and 16-byte aligned" % name)
-        elif x.dim() == 4:
-            _check_states(x, None, None, None, name)
-    if source is None or (source.data_ptr() == states.data_ptr() and source.shape == states.shape
-                          and source.stride() == states.stride()):
+    _check_pool(states, "states")
+    if source is None or source is states:
         source = states
-    elif source.dim() != states.dim() or source.shape[-3:] != states.shape[-3:] or \
-            (states.dim() == 5 and source.shape[0] != states.shape[0]):
-        raise ValueError("states and source must hold states of one shape and as many layers")
-    elif _overlap(states, source):
-        raise ValueError("source overlaps states")
+    else:
+        _check_pool(source, "source")
+        if source.dim() != states.dim() or source.shape[-3:] != states.shape[-3:] or \
+                (states.dim() == 5 and source.shape[0] != states.shape[0]):
+            raise ValueError("states and source must hold states of one shape and as many layers")
+        same = source.data_ptr() == states.data_ptr() and source.shape == states.shape and \
+            source.stride() == states.stride()
+        if not same and _overlap(states, source):
+            raise ValueError("source overlaps states")
     n, n_dst, n_src = dst.numel(), states.shape[-4], source.shape[-4]
     if n > _lib.COPY_MAX:
         raise ValueError("at most %d entries" % _lib.COPY_MAX)
     _indices(dst, n, "dst", -1, n_dst)
     _indices(src, n, "src", -1, n_src)
-    _refuse_gradients(states, source)
-    if not states.is_cuda:
-        raise ValueError("inputs must be on the GPU")
+    if torch.is_grad_enabled() and (states.requires_grad or source.requires_grad):
+        _refuse_gradients()
     dev = states.device
-    _same_device(dev, source)
-    dst, src = _c(dst).to(dev), _c(src).to(dev)
-    layered = states.dim() == 5
+    _one_gpu(dev, source)
+    dst, src = _on(dst, dev), _on(src, dev)
     H, K, V = states.shape[-3:]
-    args = _lib.CopyArgs(
-        n, n_dst, n_src, 4 * H * K * V, 4 * states.stride(-4), 4 * source.stride(-4),
-        states.shape[0] if layered else 1, 4 * states.stride(0) if layered else 0,
-        4 * source.stride(0) if layered else 0, _ptr(dst), _ptr(src), _ptr(states), _ptr(source))
+    layers, layer, source_layer = 1, 0, 0
+    if states.dim() == 5:
+        layers, layer, source_layer = states.shape[0], 4 * states.stride(0), 4 * source.stride(0)
+    args = _lib.CopyArgs(n, n_dst, n_src, 4 * H * K * V, 4 * states.stride(-4), 4 * source.stride(-4), layers, layer,
+                         source_layer, dst.data_ptr(), src.data_ptr(), states.data_ptr(), source.data_ptr())
     _launch(_lib.copy_states, args, dev)
     return states
