@@ -8,14 +8,19 @@
 //     O = scale (e^G Q h + P U),          P_ij = D_ij (q_i . k_j), j an ancestor of i, or i
 // Parents come before their children, so A is strictly lower triangular.
 //
+// Only O is wanted, so U is never formed: with M (I + A) = P,
+//     O = scale (e^G Q h + M R),   R = beta (V - e^G K h),
+// and M, a matrix of nodes by nodes, is the same for all value columns.
+//
 // One workgroup per (sequence, v head), one wave per 32 value columns, nodes in
 // NT tiles of 16.  The state is read once, straight into the registers that feed
 // the products: lane (c, g) = (l & 15, l >> 4) of a wave loads h[32 kb + 8 g + i][2 c
 // + t], the B operands of two 16-column tiles whose columns are 2 c and 2 c + 1.
-// K, Q, A and P go through LDS.  The loads of the state are issued first and are in
-// flight while the waves share out the 16 x 16 tiles of A and P and the inverses of
-// I + A's diagonal tiles; after that each wave solves its own columns, tile by
-// tile, with U in registers as the B operand of the next product.
+// These loads are issued first and are in flight while the waves share out A and
+// P (from K and Q in LDS).  A wave that has P's tiles of rows r in registers, transposed,
+// solves M's rows r from the right: M^T_c = D_c^T (P^T_c + sum over k > c of (-A_kc)^T M^T_k), D
+// the inverses of I + A's diagonal tiles.  An accumulator tile of M^T is an A operand
+// tile of M, so M goes to LDS as it stands (in the place of K and Q), in bf16 pieces.
 //
 // Non-finite values.  Node j must not reach nodes that are no descendants of it,
 // though a product with a masked zero would turn its NaN or infinity into NaN there.
@@ -30,24 +35,40 @@ namespace {
 
 constexpr int LDT = 20;  // floats per row of a 16 x 16 tile in LDS (16 and padding: conflict-free rows)
 
-template <typename In, int K, int NT> struct TreeLds {
+template <typename In, int K, int NT, int PIECES> struct TreeLds {
     static constexpr int ROWB = K * sizeof(In) + 16;  // a row of K or Q with padding
-    static constexpr int TILES = NT * (NT + 1) / 2;
-    static constexpr int k = 0, q = k + 16 * NT * ROWB, a = q + 16 * NT * ROWB, p = a + TILES * 16 * LDT * 4,
-                         G = p + TILES * 16 * LDT * 4, mask = G + 16 * NT * 8, eg = mask + 16 * NT * 8,
-                         beta = eg + 16 * NT * 4, bad = beta + 16 * NT * 4, bytes = bad + 16;
+    static constexpr int TILES = NT * (NT + 1) / 2, NP = (NT + 1) / 2;
+    static constexpr int k = 0, q = k + 16 * NT * ROWB, a = q + 16 * NT * ROWB, G = a + TILES * 16 * LDT * 4,
+                         mask = G + 16 * NT * 8, eg = mask + 16 * NT * 8, beta = eg + 16 * NT * 4,
+                         bad = beta + 16 * NT * 4, bytes = bad + 16;
+    // M, in the place of K and Q: per row tile r, pairs of column tiles, piece and lane, 16 bytes
+    static constexpr int m = 0, PAIR = PIECES * 1024;
+    static __device__ __forceinline__ int pair_at(int r, int cp) { return m + ((r + 1) / 2 * (r / 2 + 1) + cp) * PAIR; }
+    static_assert(((NT + 1) / 2 * (NT / 2 + 1)) * PAIR <= a, "M fits in the place of K and Q");
 };
 
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+__device__ __forceinline__ bool finite4(f32x4 x) {
+    return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))) < __builtin_inff() &&
+           x[0] == x[0] && x[1] == x[1] && x[2] == x[2] && x[3] == x[3];
+}
 // tile (r, c) of a lower triangle of 16 x 16 tiles
 __device__ __forceinline__ int tile_at(int r, int c) { return (r * (r + 1) / 2 + c) * 16 * LDT; }
 
-// fp32 product of a 16 x 16 tile of LDS (A operand) and an accumulator tile
-__device__ __forceinline__ f32x4 tile_mul(const float *tile, f32x4 b, f32x4 c) {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + ln16() * LDT + 4 * lg4());
+// fp32 product of the transpose of a 16 x 16 tile of LDS and an accumulator tile
+__device__ __forceinline__ f32x4 tile_t_mul(const float *tile, f32x4 b, f32x4 c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    for (int j = 0; j < 4; ++j)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(tile[(4 * lg4() + j) * LDT + ln16()], b[j], c, 0, 0, 0);
     return c;
+}
+
+// x as a sum of bf16 values: 3 keep 24 bits (an fp32 output), 2 keep 16 (a bf16 output has 8)
+template <int PIECES> __device__ __forceinline__ void pieces4(f32x4 x, bf16x4 *y) {
+#pragma unroll
+    for (int s = 0; s < PIECES; ++s) {
+        y[s] = __builtin_convertvector(x, bf16x4);
+        x -= __builtin_convertvector(y[s], f32x4);
+    }
 }
 
 // eight consecutive values of an operand's row, and a tile's product over 32 of them
@@ -74,8 +95,7 @@ template <> struct Row8<float> {
     }
 };
 
-// eight state values of a column as an operand.  With bf16 rows the state is the sum
-// of PIECES bf16 values: 3 keep 24 bits (an fp32 output), 2 keep 16 (a bf16 output has 8).
+// eight state values of a column as an operand, in bf16 pieces where the rows are bf16
 template <typename In, int PIECES> struct State8;
 template <int PIECES> struct State8<bf16, PIECES> {
     bf16x8 x[PIECES];
@@ -107,27 +127,29 @@ template <int PIECES> struct State8<float, PIECES> {
 };
 
 typedef float pair __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ pair load2(const float *p) { return *reinterpret_cast<const pair *>(p); }
-__device__ __forceinline__ pair load2(const bf16 *p) {
-    return __builtin_convertvector(*reinterpret_cast<const bf16x2 *>(p), pair);
-}
 __device__ __forceinline__ void store2(float *p, pair x) { *reinterpret_cast<pair *>(p) = x; }
 __device__ __forceinline__ void store2(bf16 *p, pair x) {
     *reinterpret_cast<bf16x2 *>(p) = __builtin_convertvector(x, bf16x2);
 }
 
+// waves per SIMD that the registers leave room for: what the LDS of NT = 4 leaves room for too
+template <typename In, int V, int NT> constexpr int waves_per_simd() {
+    return NT < 4 ? 3 : sizeof(In) == 4 ? 1 : V == 64 ? 2 : 3;
+}
+
 template <typename In, typename Out, int K, int V, int NT>
-__global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
-    using L = TreeLds<In, K, NT>;
+__global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree_kernel(PoolParams p) {
     constexpr int NTHREADS = 2 * V, NW = V / 32, PIECES = sizeof(Out) == 4 ? 3 : 2;
+    using L = TreeLds<In, K, NT, PIECES>;
+    constexpr int NP = L::NP;
     extern __shared__ __align__(16) char smem[];
-    float *At = reinterpret_cast<float *>(smem + L::a), *Pt = reinterpret_cast<float *>(smem + L::p);
+    float *At = reinterpret_cast<float *>(smem + L::a);  // -A, later with D in the diagonal tiles
     double *G = reinterpret_cast<double *>(smem + L::G);
     uint64_t *mask = reinterpret_cast<uint64_t *>(smem + L::mask);
     float *eg = reinterpret_cast<float *>(smem + L::eg), *beta = reinterpret_cast<float *>(smem + L::beta);
     unsigned *bad = reinterpret_cast<unsigned *>(smem + L::bad);  // two words of node bits
 
-    const int unit = blockIdx.x, j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
+    const int unit = xcd_runs(blockIdx.x, gridDim.x), j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), c = ln16(), g = lg4();
     const int col = 32 * w + 2 * c;
     int64_t bos, eos;
@@ -142,23 +164,6 @@ __global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
     }
     const int n = (int)(eos - bos), nt = (n + 15) >> 4;
 
-    // K and Q, zero past the last node, to LDS
-    constexpr int PER = Vec16<In>::n, CHUNKS = K / PER, TURNS = (16 * NT * CHUNKS + NTHREADS - 1) / NTHREADS;
-    typedef typename Vec16<In>::type V16;
-    V16 kx[TURNS], qx[TURNS];
-    {
-        const In *kp = reinterpret_cast<const In *>(p.k) + hq * K, *qp = reinterpret_cast<const In *>(p.q) + hq * K;
-#pragma unroll
-        for (int t = 0; t < TURNS; ++t) {
-            const int at = t * NTHREADS + threadIdx.x, i = at / CHUNKS, d = at % CHUNKS * PER;
-            kx[t] = V16{};
-            qx[t] = V16{};
-            if (i < n) {
-                kx[t] = *reinterpret_cast<const V16 *>(kp + row_offset(p, j, bos + i, p.k_batch, p.k_row) + d);
-                qx[t] = *reinterpret_cast<const V16 *>(qp + row_offset(p, j, bos + i, p.q_batch, p.q_row) + d);
-            }
-        }
-    }
     // wave 0: parents, gates and beta, a node per lane
     int up = -1;
     float gate = 0.f, b = 0.f;
@@ -167,23 +172,52 @@ __global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
         gate = p.g[(bos + l) * p.Hv + hv];
         b = p.beta[(bos + l) * p.Hv + hv];
     }
-    // the state
+    // K and Q, zero past the last node
+    constexpr int PER = Vec16<In>::n, CHUNKS = K / PER, ROWS = NTHREADS / CHUNKS, TURNS = 16 * NT / ROWS > 0 ? 16 * NT / ROWS : 1;
+    static_assert(NTHREADS % CHUNKS == 0 && ((16 * NT) % ROWS == 0 || ROWS > 16 * NT), "whole turns");
+    typedef typename Vec16<In>::type V16;
+    const int kq_row = threadIdx.x / CHUNKS, kq_chunk = threadIdx.x % CHUNKS;
+    V16 kx[TURNS], qx[TURNS];
+    {
+        const In *kp = reinterpret_cast<const In *>(p.k) + row_offset(p, j, bos + kq_row, p.k_batch, p.k_row) + hq * K + kq_chunk * PER;
+        const In *qp = reinterpret_cast<const In *>(p.q) + row_offset(p, j, bos + kq_row, p.q_batch, p.q_row) + hq * K + kq_chunk * PER;
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) {
+            kx[t] = V16{};
+            qx[t] = V16{};
+            if (t * ROWS + kq_row < n) {
+                kx[t] = *reinterpret_cast<const V16 *>(kp + t * ROWS * p.k_row);
+                qx[t] = *reinterpret_cast<const V16 *>(qp + t * ROWS * p.q_row);
+            }
+        }
+    }
+    // the state and V
     pair h[K / 32][8];
     {
         const float *hp = p.states + (int64_t)slot * p.slot_stride + ((int64_t)hv * K + 8 * g) * V + col;
 #pragma unroll
         for (int kb = 0; kb < K / 32; ++kb)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[kb][i] = load2(hp + (32 * kb + i) * V);
+            for (int i = 0; i < 8; ++i) h[kb][i] = *reinterpret_cast<const pair *>(hp + (32 * kb + i) * V);
+    }
+    typedef In InPair __attribute__((ext_vector_type(2)));
+    InPair v[NT][4];
+    {
+        const In *vp = reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos + 4 * g, p.v_batch, p.v_row) + hv * V + col;
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[rt][i] = InPair{};
+                if (16 * rt + 4 * g + i < n) v[rt][i] = *reinterpret_cast<const InPair *>(vp + (16 * rt + i) * p.v_row);
+            }
     }
 #pragma unroll
-    for (int t = 0; t < TURNS; ++t) {
-        const int at = t * NTHREADS + threadIdx.x, i = at / CHUNKS, d = at % CHUNKS;
-        if (TURNS * NTHREADS == 16 * NT * CHUNKS || i < 16 * NT) {
-            *reinterpret_cast<V16 *>(smem + L::k + i * L::ROWB + 16 * d) = kx[t];
-            *reinterpret_cast<V16 *>(smem + L::q + i * L::ROWB + 16 * d) = qx[t];
+    for (int t = 0; t < TURNS; ++t)
+        if (ROWS <= 16 * NT || kq_row < 16 * NT) {
+            *reinterpret_cast<V16 *>(smem + L::k + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = kx[t];
+            *reinterpret_cast<V16 *>(smem + L::q + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = qx[t];
         }
-    }
     if (w == 0) {
         // path sums and ancestors by pointer doubling: after a round a lane has its sum
         // over twice as many nodes.  The sums are in 64 bits (their differences would lose
@@ -214,42 +248,73 @@ __global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
     lds_barrier();
 
     auto row = [&](int base, int i, int kb) { return smem + base + i * L::ROWB + (32 * kb + 8 * g) * (int)sizeof(In); };
-    // tiles of A and P, dealt to the waves
-    int turn = 0;
+    // products of the nodes of tile a (rows) with those of tile b (columns); lane (c, g) then
+    // has nodes 16 a + 4 g + i against node 16 b + c
+    auto product = [&](int a, int base_b, int b) {
+        f32x4 x = zero4();
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-        for (int ct = 0; ct <= rt; ++ct, ++turn) {
-            if (turn % NW != w || rt >= nt) continue;
-            f32x4 kk = zero4(), qk = zero4();
-#pragma unroll
-            for (int kb = 0; kb < K / 32; ++kb) {
-                Row8<In> kr, qr, kc;
-                kr.load(row(L::k, 16 * rt + c, kb));
-                qr.load(row(L::q, 16 * rt + c, kb));
-                kc.load(row(L::k, 16 * ct + c, kb));
-                kk = kr.dot(kc, kk);
-                qk = qr.dot(kc, qk);
-            }
-            const int jc = 16 * ct + c;  // the column's node
-            const double Gc = G[jc];
-            unsigned lost = 0;  // rows of this lane group's four that are not finite
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * rt + 4 * g + r;
-                const bool above = mask[i] >> jc & 1;
-                const float d = above ? expf((float)(G[i] - Gc)) : 0.f;
-                float a = above ? beta[i] * d * kk[r] : 0.f;
-                // a product of a row with itself shows whether it is finite
-                if (!finite(a) || (i == jc && !finite(kk[r]))) {
-                    lost |= 1u << r;
-                    a = 0.f;
-                }
-                At[tile_at(rt, ct) + (4 * g + r) * LDT + c] = -a;
-                Pt[tile_at(rt, ct) + (4 * g + r) * LDT + c] = above ? d * qk[r] : i == jc ? qk[r] : 0.f;
-            }
-            if (lost) atomicOr(&bad[rt >> 1], lost << (16 * (rt & 1) + 4 * g));
+        for (int kb = 0; kb < K / 32; ++kb) {
+            Row8<In> ra, rb;
+            ra.load(row(L::k, 16 * a + c, kb));
+            rb.load(row(base_b, 16 * b + c, kb));
+            x = ra.dot(rb, x);
         }
+        return x;
+    };
+    // D of node 16 b + c and its ancestors among nodes 16 a + 4 g + i, zero for the others
+    auto decay = [&](int a, double Gb, uint64_t mb) {
+        f32x4 d;
+        const uint32_t bits = (uint32_t)(mb >> (16 * a + 4 * g));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = bits >> i & 1 ? fast_exp((float)(Gb - G[16 * a + 4 * g + i])) : 0.f;
+        return d;
+    };
+    // a wave takes P's rows r and, so that all waves have as many tiles, A's rows NT - 1 - r
+    constexpr int MINE = NT > NW ? NT / NW : 1;
+    f32x4 mt[MINE][NT];
+#pragma unroll
+    for (int y = 0; y < MINE; ++y) {
+        const int r = y ? NT - 1 - w : w, ra = NT - 1 - r;
+        if (r >= NT) break;
+        if (ra < nt) {
+            const int node = 16 * ra + c;
+            const double Gb = G[node];
+            const uint64_t mb = mask[node];
+            const float minus_beta = -beta[node];
+            bool lost = false;
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct) {
+                if (ct > ra) continue;
+                const f32x4 kk = product(ct, L::k, ra), d = decay(ct, Gb, mb);
+                f32x4 a;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = d[i] != 0.f ? minus_beta * d[i] * kk[i] : 0.f;
+                    // a product of a row with itself shows whether it is finite
+                    if (16 * ct + 4 * g + i == node) lost |= !(fabsf(kk[i]) < __builtin_inff());
+                }
+                if (!finite4(a)) {
+                    lost = true;
+                    a = zero4();
+                }
+                *reinterpret_cast<f32x4 *>(At + tile_at(ra, ct) + c * LDT + 4 * g) = a;
+            }
+            if (lost) atomicOr(&bad[ra >> 1], 1u << (16 * (ra & 1) + c));
+        }
+        if (r < nt) {
+            const int node = 16 * r + c;
+            const double Gb = G[node];
+            const uint64_t mb = mask[node] | 1ull << node;
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct) {
+                mt[y][ct] = zero4();
+                if (ct > r) continue;
+                const f32x4 kq = product(ct, L::q, r), d = decay(ct, Gb, mb);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mt[y][ct][i] = d[i] != 0.f ? d[i] * kq[i] : 0.f;
+            }
+        }
+    }
     lds_barrier();
     // inverses of the diagonal tiles of I + A, a column per lane, in place
 #pragma unroll
@@ -301,37 +366,66 @@ __global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
         }
     }
     lds_barrier();
-    const In *vp = reinterpret_cast<const In *>(p.v) + hv * V + col;
-    uint64_t lost[2] = {0, 0};  // nodes whose right-hand side in this lane's columns is not finite
-    f32x4 u[NT][2];
+    // M's rows r, from the right; the products with K and Q are done, M takes their place
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt) {
-        if (rt >= nt) continue;
-        f32x4 r[2];
-        const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
-        const f32x4 b4 = *reinterpret_cast<const f32x4 *>(beta + 16 * rt + 4 * g);
+    for (int y = 0; y < MINE; ++y) {
+        const int r = y ? NT - 1 - w : w;
+        if (r >= nt) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int node = 16 * rt + 4 * g + i;
-            pair v = {0.f, 0.f};
-            if (node < n) v = load2(vp + row_offset(p, j, bos + node, p.v_batch, p.v_row));
+        for (int ct = NT - 1; ct >= 0; --ct) {
+            if (ct > r) continue;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float x = b4[i] * (v[t] - e4[i] * kh[rt][t][i]);
-                if (!finite(x)) {
-                    lost[t] |= 1ull << node;
-                    x = 0.f;
-                }
-                r[t][i] = x;
-            }
+            for (int k = ct + 1; k < NT; ++k)
+                if (k <= r) mt[y][ct] = tile_t_mul(At + tile_at(k, ct), mt[y][k], mt[y][ct]);
+            mt[y][ct] = tile_t_mul(At + tile_at(ct, ct), mt[y][ct], zero4());
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int cp = 0; cp < NP; ++cp) {
+            if (2 * cp > r) continue;
+            bf16x4 lo[PIECES], hi[PIECES];
+            pieces4<PIECES>(mt[y][2 * cp], lo);
+            pieces4<PIECES>(2 * cp + 1 < NT ? mt[y][2 * cp + 1 < NT ? 2 * cp + 1 : 0] : zero4(), hi);  // zero past r
 #pragma unroll
-            for (int ct = 0; ct < rt; ++ct) r[t] = tile_mul(At + tile_at(rt, ct), u[ct][t], r[t]);
-            u[rt][t] = tile_mul(At + tile_at(rt, rt), r[t], zero4());
+            for (int s = 0; s < PIECES; ++s)
+                *reinterpret_cast<bf16x8 *>(smem + L::pair_at(r, cp) + 1024 * s + 16 * l) = cat(lo[s], hi[s]);
         }
     }
+    // R, where not finite remembered and replaced
+    uint64_t lost[2] = {0, 0};  // nodes, in this lane's columns
+    bf16x8 rs[NP][2][PIECES];
+#pragma unroll
+    for (int cp = 0; cp < NP; ++cp) {
+        bf16x4 half[2][2][PIECES];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int rt = 2 * cp + e;
+            f32x4 x[2] = {zero4(), zero4()};
+            if (rt < NT && rt < nt) {
+                const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
+                const f32x4 b4 = *reinterpret_cast<const f32x4 *>(beta + 16 * rt + 4 * g);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[t][i] = b4[i] * (to_f32(v[rt < NT ? rt : 0][i][t]) - e4[i] * kh[rt < NT ? rt : 0][t][i]);
+                    if (!finite4(x[t]))
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(fabsf(x[t][i]) < __builtin_inff())) {
+                                lost[t] |= 1ull << (16 * rt + 4 * g + i);
+                                x[t][i] = 0.f;
+                            }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) pieces4<PIECES>(x[t], half[e][t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int s = 0; s < PIECES; ++s) rs[cp][t][s] = cat(half[0][t][s], half[1][t][s]);
+    }
+    lds_barrier();
     const uint64_t rows_lost = bad[0] | (uint64_t)bad[1] << 32;
     const bool poisoned = __ballot((lost[0] | lost[1] | rows_lost) != 0) != 0;
     if (poisoned)
@@ -347,11 +441,23 @@ __global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
         const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
         f32x4 y[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            y[t] = e4 * qh[rt][t];
+        for (int t = 0; t < 2; ++t) y[t] = e4 * qh[rt][t];
 #pragma unroll
-            for (int ct = 0; ct <= rt; ++ct) y[t] = tile_mul(Pt + tile_at(rt, ct), u[ct][t], y[t]);
+        for (int cp = 0; cp <= rt / 2; ++cp) {
+            bf16x8 m[PIECES];
+#pragma unroll
+            for (int s = 0; s < PIECES; ++s)
+                m[s] = *reinterpret_cast<const bf16x8 *>(smem + L::pair_at(rt, cp) + 1024 * s + 16 * l);
+            // the products that PIECES pieces of accuracy need, small ones first
+#pragma unroll
+            for (int sum = PIECES - 1; sum >= 0; --sum)
+#pragma unroll
+                for (int s = 0; s <= sum; ++s)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        y[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(m[s], rs[cp][t][sum - s], y[t], 0, 0, 0);
         }
+        Out *orow = o + (bos + 4 * g) * p.Hv * V + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int node = 16 * rt + 4 * g + i;
@@ -361,13 +467,13 @@ __global__ __launch_bounds__(2 * V, 2) void gdr_tree_kernel(PoolParams p) {
                 if (path & lost[0]) x[0] = __builtin_nanf("");
                 if (path & lost[1]) x[1] = __builtin_nanf("");
             }
-            if (node < n) store2(o + (bos + node) * p.Hv * V + col, x);
+            if (node < n) store2(orow + (int64_t)(16 * rt + i) * p.Hv * V, x);
         }
     }
 }
 
 template <typename In, typename Out, int K, int V, int NT> hipError_t launch(const PoolParams &p, hipStream_t s) {
-    constexpr int bytes = TreeLds<In, K, NT>::bytes;
+    constexpr int bytes = TreeLds<In, K, NT, sizeof(Out) == 4 ? 3 : 2>::bytes;
     static const hipError_t attr =
         hipFuncSetAttribute(reinterpret_cast<const void *>(&gdr_tree_kernel<In, Out, K, V, NT>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
