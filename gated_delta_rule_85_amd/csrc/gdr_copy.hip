@@ -64,7 +64,7 @@ __global__ __launch_bounds__(NT) void gdr_copy_kernel(CopyParams p, int64_t colu
         }
     }
     const int64_t width = 16 * LW, per_layer = (p.slot_bytes + width - 1) / width;
-    for (int64_t c = blockIdx.x; c < columns; c += gridDim.x) {
+    for (int64_t c = xcd_runs(blockIdx.x, gridDim.x); c < columns; c += gridDim.x) {
         const int64_t layer = c / per_layer, at = (c - layer * per_layer) * width + 16 * lane;
         const bool inside = at < p.slot_bytes;
         const char *src = p.src + layer * p.src_layer_stride + at;
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(NT) void gdr_copy_kernel(CopyParams p, int64_t colu
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < RN; ++r)
-            if (inside && to[r] >= 0) *reinterpret_cast<f32x4 *>(dst + to[r] * p.dst_stride) = x[r];
+            if (inside && to[r] >= 0) store4_once(reinterpret_cast<float *>(dst + to[r] * p.dst_stride), x[r]);
     }
 }
 
@@ -91,7 +91,9 @@ template <int LW, int NT, int RN> hipError_t launch(const CopyParams &p, hipStre
     int bits = 1;
     while ((1 << bits) < 2 * p.n) ++bits;
     const int64_t columns = p.layers * ((p.slot_bytes + 16 * LW - 1) / (16 * LW));
-    const int64_t most = 256 * (2048 / NT);  // as many threads as the device's 256 compute units hold
+    // two workgroups per compute unit keep enough loads in flight where each has many;
+    // with few entries, as many threads as the 256 compute units hold
+    const int64_t most = 256 * (RN >= 8 ? 2 : 2048 / NT);
     const uint32_t lds = 8u << bits;
     launch_k(gdr_copy_kernel<LW, NT, RN>, dim3((uint32_t)(columns < most ? columns : most)), dim3(NT), lds, s, p, columns,
              bits);
@@ -100,11 +102,17 @@ template <int LW, int NT, int RN> hipError_t launch(const CopyParams &p, hipStre
 
 }  // namespace
 
+// Few entries: wide columns, so that a slot's bytes move in runs of 1 KB.  Many: narrow
+// ones, since all entries' columns are held at once.  Measured at slots of 2 MB in a pool of
+// 2 GB, states read and written per second: 250 entries at 5.0 TB/s with 256-byte columns
+// (5.2 with 1 KB ones and 1024 threads, but 100 entries at 7.2 instead of 7.7), 900 entries
+// 4.8 (4.2 with 128-byte columns and 512 threads), 3000 of 512 KB at 3.4; 61 entries of 12
+// layers at 6.0 (5.2 with a store through the caches and columns dealt round robin).
 hipError_t launch_copy(const CopyParams &p, hipStream_t s) {
     if (p.n <= 4) return launch<64, 256, 1>(p, s);
     if (p.n <= 16) return launch<64, 256, 4>(p, s);
     if (p.n <= 64) return launch<64, 256, 16>(p, s);
-    if (p.n <= 256) return launch<16, 256, 16>(p, s);
+    if (p.n <= 256) return launch<16, 512, 8>(p, s);
     if (p.n <= 1024) return launch<16, 1024, 16>(p, s);
     return launch<4, 1024, 16>(p, s);  // up to COPY_MAX = 4096
 }
