@@ -31,6 +31,9 @@ int plan(const gdr_pool_args *a, Op op, PoolParams &p, bool &idle) {
     for (const int64_t st : {a->k_row, a->v_row, op == Op::ACCEPT ? 0 : a->q_row, varlen ? 0 : a->k_batch,
                              varlen ? 0 : a->v_batch, varlen || op == Op::ACCEPT ? 0 : a->q_batch})
         if (st < 0 || st % per16 != 0) return GDR_EINVAL;
+    // 64 rows of a tree lie within 32-bit byte offsets
+    if (a->H_v >= 65536 || a->k_row >= 1 << 23 || a->v_row >= 1 << 23 || (op != Op::ACCEPT && a->q_row >= 1 << 23))
+        return GDR_EINVAL;
     idle = n_seq == 0 || a->T == 0;
     if (idle) return GDR_OK;
     if (!a->k || !a->v || !a->g || !a->beta || !a->states) return GDR_EINVAL;

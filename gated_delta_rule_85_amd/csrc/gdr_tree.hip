@@ -127,9 +127,20 @@ template <int PIECES> struct State8<float, PIECES> {
 };
 
 typedef float pair __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void store2(float *p, pair x) { *reinterpret_cast<pair *>(p) = x; }
-__device__ __forceinline__ void store2(bf16 *p, pair x) {
-    *reinterpret_cast<bf16x2 *>(p) = __builtin_convertvector(x, bf16x2);
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A buffer of n rows, `stride` bytes apart, of `bytes` bytes each: loads past its end give
+// zero and stores there are dropped, so that rows need no conditions
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rows_of(const void *base, int n, int stride, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (n - 1) * stride + bytes, 0x00027000);
+}
+__device__ __forceinline__ void store2(float, Rsrc r, int lane, int at, pair x) {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, lane, at, 0);
+}
+__device__ __forceinline__ void store2(bf16, Rsrc r, int lane, int at, pair x) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2)), r, lane, at, 0);
 }
 
 // waves per SIMD that the registers leave room for: what the LDS of NT = 4 leaves room for too
@@ -172,51 +183,53 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
         gate = p.g[(bos + l) * p.Hv + hv];
         b = p.beta[(bos + l) * p.Hv + hv];
     }
-    // K and Q, zero past the last node
+    // K and Q; rows past the last node read as zero (or, where rows overlap, as any values:
+    // nothing below depends on them)
     constexpr int PER = Vec16<In>::n, CHUNKS = K / PER, ROWS = NTHREADS / CHUNKS, TURNS = 16 * NT / ROWS > 0 ? 16 * NT / ROWS : 1;
     static_assert(NTHREADS % CHUNKS == 0 && ((16 * NT) % ROWS == 0 || ROWS > 16 * NT), "whole turns");
-    typedef typename Vec16<In>::type V16;
     const int kq_row = threadIdx.x / CHUNKS, kq_chunk = threadIdx.x % CHUNKS;
-    V16 kx[TURNS], qx[TURNS];
+    u32x4 kx[TURNS], qx[TURNS];
     {
-        const In *kp = reinterpret_cast<const In *>(p.k) + row_offset(p, j, bos + kq_row, p.k_batch, p.k_row) + hq * K + kq_chunk * PER;
-        const In *qp = reinterpret_cast<const In *>(p.q) + row_offset(p, j, bos + kq_row, p.q_batch, p.q_row) + hq * K + kq_chunk * PER;
+        const int kb = (int)p.k_row * (int)sizeof(In), qb = (int)p.q_row * (int)sizeof(In);
+        const Rsrc kr = rows_of(reinterpret_cast<const In *>(p.k) + row_offset(p, j, bos, p.k_batch, p.k_row) + hq * K, n, kb, K * sizeof(In));
+        const Rsrc qr = rows_of(reinterpret_cast<const In *>(p.q) + row_offset(p, j, bos, p.q_batch, p.q_row) + hq * K, n, qb, K * sizeof(In));
 #pragma unroll
         for (int t = 0; t < TURNS; ++t) {
-            kx[t] = V16{};
-            qx[t] = V16{};
-            if (t * ROWS + kq_row < n) {
-                kx[t] = *reinterpret_cast<const V16 *>(kp + t * ROWS * p.k_row);
-                qx[t] = *reinterpret_cast<const V16 *>(qp + t * ROWS * p.q_row);
-            }
+            kx[t] = __builtin_amdgcn_raw_buffer_load_b128(kr, kq_row * kb + 16 * kq_chunk, t * ROWS * kb, 0);
+            qx[t] = __builtin_amdgcn_raw_buffer_load_b128(qr, kq_row * qb + 16 * kq_chunk, t * ROWS * qb, 0);
         }
     }
     // the state and V
     pair h[K / 32][8];
     {
-        const float *hp = p.states + (int64_t)slot * p.slot_stride + ((int64_t)hv * K + 8 * g) * V + col;
+        const Rsrc hr = rows_of(p.states + (int64_t)slot * p.slot_stride + (int64_t)hv * K * V, K, 4 * V, 4 * V);
 #pragma unroll
         for (int kb = 0; kb < K / 32; ++kb)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[kb][i] = *reinterpret_cast<const pair *>(hp + (32 * kb + i) * V);
+            for (int i = 0; i < 8; ++i)
+                h[kb][i] = __builtin_bit_cast(pair, __builtin_amdgcn_raw_buffer_load_b64(hr, (8 * g * V + col) * 4, (32 * kb + i) * V * 4, 0));
     }
     typedef In InPair __attribute__((ext_vector_type(2)));
     InPair v[NT][4];
     {
-        const In *vp = reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos + 4 * g, p.v_batch, p.v_row) + hv * V + col;
+        const int vb = (int)p.v_row * (int)sizeof(In);
+        const Rsrc vr = rows_of(reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos, p.v_batch, p.v_row) + hv * V, n, vb, V * sizeof(In));
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[rt][i] = InPair{};
-                if (16 * rt + 4 * g + i < n) v[rt][i] = *reinterpret_cast<const InPair *>(vp + (16 * rt + i) * p.v_row);
+                const int lane = 4 * g * vb + col * (int)sizeof(In), at = (16 * rt + i) * vb;
+                if constexpr (sizeof(In) == 2)
+                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b32(vr, lane, at, 0));
+                else
+                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b64(vr, lane, at, 0));
             }
     }
 #pragma unroll
     for (int t = 0; t < TURNS; ++t)
         if (ROWS <= 16 * NT || kq_row < 16 * NT) {
-            *reinterpret_cast<V16 *>(smem + L::k + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = kx[t];
-            *reinterpret_cast<V16 *>(smem + L::q + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = qx[t];
+            *reinterpret_cast<u32x4 *>(smem + L::k + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = kx[t];
+            *reinterpret_cast<u32x4 *>(smem + L::q + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = qx[t];
         }
     if (w == 0) {
         // path sums and ancestors by pointer doubling: after a round a lane has its sum
@@ -426,6 +439,8 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
             for (int s = 0; s < PIECES; ++s) rs[cp][t][s] = cat(half[0][t][s], half[1][t][s]);
     }
     lds_barrier();
+    const int ob = p.Hv * V * (int)sizeof(Out);
+    const Rsrc out = rows_of(o + bos * p.Hv * V, n, ob, V * sizeof(Out));
     const uint64_t rows_lost = bad[0] | (uint64_t)bad[1] << 32;
     const bool poisoned = __ballot((lost[0] | lost[1] | rows_lost) != 0) != 0;
     if (poisoned)
@@ -457,7 +472,6 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
                     for (int t = 0; t < 2; ++t)
                         y[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(m[s], rs[cp][t][sum - s], y[t], 0, 0, 0);
         }
-        Out *orow = o + (bos + 4 * g) * p.Hv * V + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int node = 16 * rt + 4 * g + i;
@@ -467,7 +481,7 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
                 if (path & lost[0]) x[0] = __builtin_nanf("");
                 if (path & lost[1]) x[1] = __builtin_nanf("");
             }
-            if (node < n) store2(orow + (int64_t)(16 * rt + i) * p.Hv * V, x);
+            store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * rt + i) * ob, x);
         }
     }
 }

@@ -45,14 +45,14 @@ def _one_gpu(dev, *tensors):
 def _rows(x, per16):
     """x with the elements between its tokens and between its batch rows, copied if the
     kernels cannot read it in place: they need one token's [H, D] contiguous and rows at
-    multiples of 16 bytes (per16 elements)."""
+    multiples of 16 bytes (per16 elements), less than 2^23 elements apart."""
     B, T, H, D = x.shape
     batch, row, head, one = x.stride()
     if B < 2:
         batch = 0
     if T < 2:
         row = 0
-    if one != 1 or (head != D and H > 1) or batch % per16 or row % per16 or x.data_ptr() % 16:
+    if one != 1 or (head != D and H > 1) or batch % per16 or row % per16 or row >= 1 << 23 or x.data_ptr() % 16:
         x = x.contiguous()
         batch, row = T * H * D, H * D
     return x, row, batch

@@ -209,13 +209,15 @@ typedef struct {
    before its start to the start.  Rows of o that belong to no sequence are left
    as they were, and so is the state of an empty sequence. */
 typedef struct {
-    /* sizes as in gdr_fwd_args; B, T and n_seq may be 0 */
+    /* sizes as in gdr_fwd_args; B, T and n_seq may be 0, H_v is below 2^16 and n_seq H_v (B H_v
+       without cu_seqlens) at most 2^22 */
     int64_t B, T, H_q, H_v, K, V, n_seq;
     int64_t n_slots;
     int64_t slot_stride;  /* floats from a slot's state to the next slot's: a multiple of 4, at
                              least H_v K V (not read if n_slots is 1) */
     /* elements from a token's row of q, k or v to the next token's, and from a batch
-       row's to the next one's (not read with cu_seqlens): multiples of 16 bytes, >= 0.
+       row's to the next one's (not read with cu_seqlens): multiples of 16 bytes, >= 0; those
+       between tokens below 2^23.
        The [H, K] (or [H, V]) values of one token are contiguous */
     int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;
     int32_t dtype;     /* element type of q, k, v */

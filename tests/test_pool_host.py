@@ -209,7 +209,7 @@ ENTRIES = ["gdr_step", "gdr_tree", "gdr_tree_accept"]
     (dict(B=-1), -1), (dict(T=-1), -1), (dict(H_v=3), -1), (dict(H_q=0), -1), (dict(K=96), -2), (dict(V=32), -2),
     (dict(dtype=2), -2), (dict(B=2, cu_seqlens=16, n_seq=1), -1), (dict(B=1, cu_seqlens=16, n_seq=-1), -1),
     (dict(n_slots=0), -1), (dict(n_slots=1, slots=None), -1), (dict(slot_stride=4 * 128 * 128 - 4), -1),
-    (dict(slot_stride=4 * 128 * 128 + 2), -1), (dict(k_row=257), -1), (dict(v_row=-8), -1), (dict(v_batch=4), -1),
+    (dict(slot_stride=4 * 128 * 128 + 2), -1), (dict(k_row=257), -1), (dict(k_row=1 << 23), -1), (dict(v_row=1 << 23), -1), (dict(H_q=65536, H_v=65536), -1), (dict(v_row=-8), -1), (dict(v_batch=4), -1),
     (dict(k=None), -1), (dict(v=24), -1), (dict(g=None), -1), (dict(beta=None), -1), (dict(states=None), -1),
     (dict(states=8), -1), (dict(B=1 << 20, H_v=8), -1), (dict(B=1, T=1 << 31), -1),
     (dict(T=0), 0), (dict(B=0), 0), (dict(B=1, cu_seqlens=16, n_seq=0), 0),
