@@ -47,10 +47,6 @@ template <typename In, int K, int NT, int PIECES> struct TreeLds {
     static_assert(((NT + 1) / 2 * (NT / 2 + 1)) * PAIR <= a, "M fits in the place of K and Q");
 };
 
-__device__ __forceinline__ bool finite4(f32x4 x) {
-    return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))) < __builtin_inff() &&
-           x[0] == x[0] && x[1] == x[1] && x[2] == x[2] && x[3] == x[3];
-}
 // tile (r, c) of a lower triangle of 16 x 16 tiles
 __device__ __forceinline__ int tile_at(int r, int c) { return (r * (r + 1) / 2 + c) * 16 * LDT; }
 
@@ -63,72 +59,67 @@ __device__ __forceinline__ f32x4 tile_t_mul(const float *tile, f32x4 b, f32x4 c)
 }
 
 // x as a sum of bf16 values: 3 keep 24 bits (an fp32 output), 2 keep 16 (a bf16 output has 8)
-template <int PIECES> __device__ __forceinline__ void pieces4(f32x4 x, bf16x4 *y) {
+template <int PIECES> __device__ __forceinline__ void pieces2(float a, float b, uint32_t *y) {
 #pragma unroll
     for (int s = 0; s < PIECES; ++s) {
-        y[s] = __builtin_convertvector(x, bf16x4);
-        x -= __builtin_convertvector(y[s], f32x4);
+        y[s] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+        a -= __builtin_bit_cast(float, y[s] << 16);
+        b -= __builtin_bit_cast(float, y[s] & 0xffff0000u);
     }
 }
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// eight values, an operand's, in pieces
+template <int PIECES> __device__ __forceinline__ void pieces8(f32x4 x, f32x4 y, bf16x8 *z) {
+    uint32_t a[4][PIECES];
+    pieces2<PIECES>(x[0], x[1], a[0]);
+    pieces2<PIECES>(x[2], x[3], a[1]);
+    pieces2<PIECES>(y[0], y[1], a[2]);
+    pieces2<PIECES>(y[2], y[3], a[3]);
+#pragma unroll
+    for (int s = 0; s < PIECES; ++s) z[s] = __builtin_bit_cast(bf16x8, (u32x4{a[0][s], a[1][s], a[2][s], a[3][s]}));
+}
 
-// eight consecutive values of an operand's row, and a tile's product over 32 of them
-template <typename In> struct Row8;
-template <> struct Row8<bf16> {
-    bf16x8 x;
-    __device__ __forceinline__ void load(const char *p) { x = *reinterpret_cast<const bf16x8 *>(p); }
-    __device__ __forceinline__ f32x4 dot(const Row8 &b, f32x4 c) const {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b.x, c, 0, 0, 0);
+// Products of rows of K or Q (8 consecutive values a lane) with rows of K or Q, and with
+// state columns in pieces, as a sequence of STEPS matrix instructions that is taken step by
+// step over several tiles, so that each waits for no other.
+template <typename In, int PIECES> struct Operands;
+template <int PIECES> struct Operands<bf16, PIECES> {
+    typedef bf16x8 Row;
+    typedef bf16x8 State[PIECES];
+    static constexpr int ROW_STEPS = 1, STATE_STEPS = PIECES;
+    static __device__ __forceinline__ void load(Row &r, const char *p) { r = *reinterpret_cast<const bf16x8 *>(p); }
+    static __device__ __forceinline__ void set(State &s, f32x4 x, f32x4 y) { pieces8<PIECES>(x, y, s); }
+    static __device__ __forceinline__ f32x4 row_step(int, const Row &a, const Row &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x4 state_step(int s, const Row &a, const State &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[PIECES - 1 - s], c, 0, 0, 0);  // small ones first
     }
 };
-template <> struct Row8<float> {
-    f32x4 x0, x1;
-    __device__ __forceinline__ void load(const char *p) {
-        x0 = *reinterpret_cast<const f32x4 *>(p);
-        x1 = *reinterpret_cast<const f32x4 *>(p + 16);
+template <int PIECES> struct Operands<float, PIECES> {
+    struct Row {
+        f32x4 x[2];
+    };
+    typedef Row State;
+    static constexpr int ROW_STEPS = 8, STATE_STEPS = 8;
+    static __device__ __forceinline__ void load(Row &r, const char *p) {
+        r.x[0] = *reinterpret_cast<const f32x4 *>(p);
+        r.x[1] = *reinterpret_cast<const f32x4 *>(p + 16);
     }
-    __device__ __forceinline__ f32x4 dot(const Row8 &b, f32x4 c) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x0[j], b.x0[j], c, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x1[j], b.x1[j], c, 0, 0, 0);
-        return c;
+    static __device__ __forceinline__ void set(State &s, f32x4 x, f32x4 y) {
+        s.x[0] = x;
+        s.x[1] = y;
     }
-};
-
-// eight state values of a column as an operand, in bf16 pieces where the rows are bf16
-template <typename In, int PIECES> struct State8;
-template <int PIECES> struct State8<bf16, PIECES> {
-    bf16x8 x[PIECES];
-    __device__ __forceinline__ void set(const float *h) {
-        float r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = h[i];
-#pragma unroll
-        for (int s = 0; s < PIECES; ++s)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[s][i] = (bf16)r[i];
-                r[i] -= (float)x[s][i];
-            }
+    static __device__ __forceinline__ f32x4 row_step(int s, const Row &a, const Row &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[s / 4][s % 4], b.x[s / 4][s % 4], c, 0, 0, 0);
     }
-    __device__ __forceinline__ f32x4 dot(const Row8<bf16> &a, f32x4 c) const {
-#pragma unroll
-        for (int s = PIECES - 1; s >= 0; --s) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x, x[s], c, 0, 0, 0);
-        return c;
+    static __device__ __forceinline__ f32x4 state_step(int s, const Row &a, const State &b, f32x4 c) {
+        return row_step(s, a, b, c);
     }
-};
-template <int PIECES> struct State8<float, PIECES> {
-    Row8<float> x;
-    __device__ __forceinline__ void set(const float *h) {
-        x.x0 = f32x4{h[0], h[1], h[2], h[3]};
-        x.x1 = f32x4{h[4], h[5], h[6], h[7]};
-    }
-    __device__ __forceinline__ f32x4 dot(const Row8<float> &a, f32x4 c) const { return a.dot(x, c); }
 };
 
 typedef float pair __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // A buffer of n rows, `stride` bytes apart, of `bytes` bytes each: loads past its end give
 // zero and stores there are dropped, so that rows need no conditions
@@ -143,37 +134,20 @@ __device__ __forceinline__ void store2(bf16, Rsrc r, int lane, int at, pair x) {
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2)), r, lane, at, 0);
 }
 
-// waves per SIMD that the registers leave room for: what the LDS of NT = 4 leaves room for too
-template <typename In, int V, int NT> constexpr int waves_per_simd() {
-    return NT < 4 ? 3 : sizeof(In) == 4 ? 1 : V == 64 ? 2 : 3;
-}
-
+// One tree of n nodes, up to 16 NT, and one v head; every wave of the workgroup calls it.
 template <typename In, typename Out, int K, int V, int NT>
-__global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree_kernel(PoolParams p) {
+__device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int hv, int64_t bos, int n) {
     constexpr int NTHREADS = 2 * V, NW = V / 32, PIECES = sizeof(Out) == 4 ? 3 : 2;
     using L = TreeLds<In, K, NT, PIECES>;
+    using X = Operands<In, PIECES>;
     constexpr int NP = L::NP;
-    extern __shared__ __align__(16) char smem[];
     float *At = reinterpret_cast<float *>(smem + L::a);  // -A, later with D in the diagonal tiles
     double *G = reinterpret_cast<double *>(smem + L::G);
     uint64_t *mask = reinterpret_cast<uint64_t *>(smem + L::mask);
     float *eg = reinterpret_cast<float *>(smem + L::eg), *beta = reinterpret_cast<float *>(smem + L::beta);
     unsigned *bad = reinterpret_cast<unsigned *>(smem + L::bad);  // two words of node bits
-
-    const int unit = xcd_runs(blockIdx.x, gridDim.x), j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), c = ln16(), g = lg4();
-    const int col = 32 * w + 2 * c;
-    int64_t bos, eos;
-    token_range(p, j, bos, eos);
-    if (bos >= eos) return;
-    const int slot = slot_of(p, j);
-    Out *o = reinterpret_cast<Out *>(p.o) + hv * V;
-    if (slot < 0 || eos - bos > TREE_MAX) {
-        const float fill = slot < 0 ? 0.f : __builtin_nanf("");
-        for (int64_t i = bos * V + threadIdx.x; i < eos * V; i += NTHREADS) o[i / V * p.Hv * V + i % V] = (Out)fill;
-        return;
-    }
-    const int n = (int)(eos - bos), nt = (n + 15) >> 4;
+    const int col = 32 * w + 2 * c, hq = hv / (p.Hv / p.Hq);
 
     // wave 0: parents, gates and beta, a node per lane
     int up = -1;
@@ -185,35 +159,28 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
     }
     // K and Q; rows past the last node read as zero (or, where rows overlap, as any values:
     // nothing below depends on them)
-    constexpr int PER = Vec16<In>::n, CHUNKS = K / PER, ROWS = NTHREADS / CHUNKS, TURNS = 16 * NT / ROWS > 0 ? 16 * NT / ROWS : 1;
-    static_assert(NTHREADS % CHUNKS == 0 && ((16 * NT) % ROWS == 0 || ROWS > 16 * NT), "whole turns");
+    constexpr int PER = Vec16<In>::n, CHUNKS = K / PER, ROWS = NTHREADS / CHUNKS, TURNS = (16 * NT + ROWS - 1) / ROWS;
     const int kq_row = threadIdx.x / CHUNKS, kq_chunk = threadIdx.x % CHUNKS;
     u32x4 kx[TURNS], qx[TURNS];
     {
         const int kb = (int)p.k_row * (int)sizeof(In), qb = (int)p.q_row * (int)sizeof(In);
-        const Rsrc kr = rows_of(reinterpret_cast<const In *>(p.k) + row_offset(p, j, bos, p.k_batch, p.k_row) + hq * K, n, kb, K * sizeof(In));
-        const Rsrc qr = rows_of(reinterpret_cast<const In *>(p.q) + row_offset(p, j, bos, p.q_batch, p.q_row) + hq * K, n, qb, K * sizeof(In));
+        const Rsrc kr = rows_of(reinterpret_cast<const In *>(p.k) + row_offset(p, j, bos, p.k_batch, p.k_row) + hq * K, n,
+                                kb, K * sizeof(In));
+        const Rsrc qr = rows_of(reinterpret_cast<const In *>(p.q) + row_offset(p, j, bos, p.q_batch, p.q_row) + hq * K, n,
+                                qb, K * sizeof(In));
 #pragma unroll
         for (int t = 0; t < TURNS; ++t) {
             kx[t] = __builtin_amdgcn_raw_buffer_load_b128(kr, kq_row * kb + 16 * kq_chunk, t * ROWS * kb, 0);
             qx[t] = __builtin_amdgcn_raw_buffer_load_b128(qr, kq_row * qb + 16 * kq_chunk, t * ROWS * qb, 0);
         }
     }
-    // the state and V
-    pair h[K / 32][8];
-    {
-        const Rsrc hr = rows_of(p.states + (int64_t)slot * p.slot_stride + (int64_t)hv * K * V, K, 4 * V, 4 * V);
-#pragma unroll
-        for (int kb = 0; kb < K / 32; ++kb)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[kb][i] = __builtin_bit_cast(pair, __builtin_amdgcn_raw_buffer_load_b64(hr, (8 * g * V + col) * 4, (32 * kb + i) * V * 4, 0));
-    }
+    // V and the state, whose slot is looked up only now
     typedef In InPair __attribute__((ext_vector_type(2)));
     InPair v[NT][4];
     {
         const int vb = (int)p.v_row * (int)sizeof(In);
-        const Rsrc vr = rows_of(reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos, p.v_batch, p.v_row) + hv * V, n, vb, V * sizeof(In));
+        const Rsrc vr = rows_of(reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos, p.v_batch, p.v_row) + hv * V, n,
+                                vb, V * sizeof(In));
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
@@ -225,9 +192,28 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
                     v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b64(vr, lane, at, 0));
             }
     }
+    const int ob = p.Hv * V * (int)sizeof(Out);
+    const Rsrc out = rows_of(reinterpret_cast<Out *>(p.o) + (bos * p.Hv + hv) * V, n, ob, V * sizeof(Out));
+    const int slot = slot_of(p, j);
+    if (slot < 0) {
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i)
+            store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * (i / 4) + i % 4) * ob, pair{0.f, 0.f});
+        return;
+    }
+    pair h[K / 32][8];
+    {
+        const Rsrc hr = rows_of(p.states + (int64_t)slot * p.slot_stride + (int64_t)hv * K * V, K, 4 * V, 4 * V);
+#pragma unroll
+        for (int kb = 0; kb < K / 32; ++kb)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[kb][i] = __builtin_bit_cast(
+                    pair, __builtin_amdgcn_raw_buffer_load_b64(hr, (8 * g * V + col) * 4, (32 * kb + i) * V * 4, 0));
+    }
 #pragma unroll
     for (int t = 0; t < TURNS; ++t)
-        if (ROWS <= 16 * NT || kq_row < 16 * NT) {
+        if (16 * NT % ROWS == 0 || t * ROWS + kq_row < 16 * NT) {
             *reinterpret_cast<u32x4 *>(smem + L::k + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = kx[t];
             *reinterpret_cast<u32x4 *>(smem + L::q + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = qx[t];
         }
@@ -261,79 +247,67 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
     lds_barrier();
 
     auto row = [&](int base, int i, int kb) { return smem + base + i * L::ROWB + (32 * kb + 8 * g) * (int)sizeof(In); };
-    // products of the nodes of tile a (rows) with those of tile b (columns); lane (c, g) then
-    // has nodes 16 a + 4 g + i against node 16 b + c
-    auto product = [&](int a, int base_b, int b) {
-        f32x4 x = zero4();
-#pragma unroll
-        for (int kb = 0; kb < K / 32; ++kb) {
-            Row8<In> ra, rb;
-            ra.load(row(L::k, 16 * a + c, kb));
-            rb.load(row(base_b, 16 * b + c, kb));
-            x = ra.dot(rb, x);
-        }
-        return x;
-    };
-    // D of node 16 b + c and its ancestors among nodes 16 a + 4 g + i, zero for the others
-    auto decay = [&](int a, double Gb, uint64_t mb) {
-        f32x4 d;
-        const uint32_t bits = (uint32_t)(mb >> (16 * a + 4 * g));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = bits >> i & 1 ? fast_exp((float)(Gb - G[16 * a + 4 * g + i])) : 0.f;
-        return d;
-    };
-    // a wave takes P's rows r and, so that all waves have as many tiles, A's rows NT - 1 - r
-    constexpr int MINE = NT > NW ? NT / NW : 1;
+    // Rows r of A and of P, transposed: lane (c, g) has node 16 r + c against nodes
+    // 16 ct + 4 g + i, whose decay D both share.  Tiles past the diagonal come out zero.
+    constexpr int MINE = (NT + NW - 1) / NW;
     f32x4 mt[MINE][NT];
 #pragma unroll
     for (int y = 0; y < MINE; ++y) {
-        const int r = y ? NT - 1 - w : w, ra = NT - 1 - r;
+        const int r = w + y * NW;
         if (r >= NT) break;
-        if (ra < nt) {
-            const int node = 16 * ra + c;
-            const double Gb = G[node];
-            const uint64_t mb = mask[node];
-            const float minus_beta = -beta[node];
-            bool lost = false;
+        f32x4 kk[NT];
 #pragma unroll
-            for (int ct = 0; ct < NT; ++ct) {
-                if (ct > ra) continue;
-                const f32x4 kk = product(ct, L::k, ra), d = decay(ct, Gb, mb);
-                f32x4 a;
+        for (int ct = 0; ct < NT; ++ct) kk[ct] = mt[y][ct] = zero4();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = d[i] != 0.f ? minus_beta * d[i] * kk[i] : 0.f;
-                    // a product of a row with itself shows whether it is finite
-                    if (16 * ct + 4 * g + i == node) lost |= !(fabsf(kk[i]) < __builtin_inff());
+        for (int kb = 0; kb < K / 32; ++kb) {
+            typename X::Row kr, qr, kc[NT];
+            X::load(kr, row(L::k, 16 * r + c, kb));
+            X::load(qr, row(L::q, 16 * r + c, kb));
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct) X::load(kc[ct], row(L::k, 16 * ct + c, kb));
+#pragma unroll
+            for (int s = 0; s < X::ROW_STEPS; ++s)
+#pragma unroll
+                for (int ct = 0; ct < NT; ++ct) {
+                    kk[ct] = X::row_step(s, kc[ct], kr, kk[ct]);
+                    mt[y][ct] = X::row_step(s, kc[ct], qr, mt[y][ct]);
                 }
-                if (!finite4(a)) {
-                    lost = true;
-                    a = zero4();
-                }
-                *reinterpret_cast<f32x4 *>(At + tile_at(ra, ct) + c * LDT + 4 * g) = a;
-            }
-            if (lost) atomicOr(&bad[ra >> 1], 1u << (16 * (ra & 1) + c));
         }
-        if (r < nt) {
-            const int node = 16 * r + c;
-            const double Gb = G[node];
-            const uint64_t mb = mask[node] | 1ull << node;
+        const int node = 16 * r + c;
+        const double Gb = G[node];
+        const uint64_t above = mask[node];
+        const float minus_beta = -beta[node];
+        float probe = 0.f;  // becomes NaN where K's row or a row of A is not finite
 #pragma unroll
-            for (int ct = 0; ct < NT; ++ct) {
-                mt[y][ct] = zero4();
-                if (ct > r) continue;
-                const f32x4 kq = product(ct, L::q, r), d = decay(ct, Gb, mb);
+        for (int ct = 0; ct < NT; ++ct) {
+            const uint32_t bits = (uint32_t)(above >> (16 * ct + 4 * g));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mt[y][ct][i] = d[i] != 0.f ? d[i] * kq[i] : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                const bool self = 16 * ct + 4 * g + i == node, on = bits >> i & 1;
+                const float d = fast_exp((float)(Gb - G[16 * ct + 4 * g + i]));
+                if (self) probe += 0.f * kk[ct][i];
+                kk[ct][i] = on ? minus_beta * d * kk[ct][i] : 0.f;
+                probe += 0.f * kk[ct][i];
+                mt[y][ct][i] = on || self ? d * mt[y][ct][i] : 0.f;
             }
         }
+        if (__ballot(probe != probe)) {
+            if (probe != probe) atomicOr(&bad[r >> 1], 1u << (16 * (r & 1) + c));
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kk[ct][i] = fabsf(kk[ct][i]) < __builtin_inff() ? kk[ct][i] : 0.f;
+        }
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct)
+            if (ct <= r) *reinterpret_cast<f32x4 *>(At + tile_at(r, ct) + c * LDT + 4 * g) = kk[ct];
     }
-    lds_barrier();
-    // inverses of the diagonal tiles of I + A, a column per lane, in place
+    // D, the inverses of the diagonal tiles of I + A, in place: a wave's own rows, a column per lane
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt) {
-        if (rt % NW != w || rt >= nt) continue;
-        float *tile = At + tile_at(rt, rt);
+    for (int y = 0; y < MINE; ++y) {
+        const int r = w + y * NW;
+        if (r >= NT) break;
+        float *tile = At + tile_at(r, r);
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
@@ -357,133 +331,160 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
         for (int t = 0; t < 2; ++t) kh[rt][t] = qh[rt][t] = zero4();
 #pragma unroll
     for (int kb = 0; kb < K / 32; ++kb) {
-        State8<In, PIECES> s[2];
+        typename X::State s[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = h[kb][i][t];
-            s[t].set(x);
-        }
+        for (int t = 0; t < 2; ++t)
+            X::set(s[t], f32x4{h[kb][0][t], h[kb][1][t], h[kb][2][t], h[kb][3][t]},
+                   f32x4{h[kb][4][t], h[kb][5][t], h[kb][6][t], h[kb][7][t]});
+        typename X::Row kr[NT], qr[NT];
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
-            if (rt >= nt) continue;
-            Row8<In> kr, qr;
-            kr.load(row(L::k, 16 * rt + c, kb));
-            qr.load(row(L::q, 16 * rt + c, kb));
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                kh[rt][t] = s[t].dot(kr, kh[rt][t]);
-                qh[rt][t] = s[t].dot(qr, qh[rt][t]);
-            }
+            X::load(kr[rt], row(L::k, 16 * rt + c, kb));
+            X::load(qr[rt], row(L::q, 16 * rt + c, kb));
         }
+#pragma unroll
+        for (int step = 0; step < X::STATE_STEPS; ++step)
+#pragma unroll
+            for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    kh[rt][t] = X::state_step(step, kr[rt], s[t], kh[rt][t]);
+                    qh[rt][t] = X::state_step(step, qr[rt], s[t], qh[rt][t]);
+                }
     }
     lds_barrier();
     // M's rows r, from the right; the products with K and Q are done, M takes their place
 #pragma unroll
     for (int y = 0; y < MINE; ++y) {
-        const int r = y ? NT - 1 - w : w;
-        if (r >= nt) break;
+        const int r = w + y * NW;
+        if (r >= NT) break;
 #pragma unroll
         for (int ct = NT - 1; ct >= 0; --ct) {
-            if (ct > r) continue;
 #pragma unroll
-            for (int k = ct + 1; k < NT; ++k)
-                if (k <= r) mt[y][ct] = tile_t_mul(At + tile_at(k, ct), mt[y][k], mt[y][ct]);
+            for (int k = NT - 1; k > ct; --k) mt[y][ct] = tile_t_mul(At + tile_at(k, ct), mt[y][k], mt[y][ct]);
             mt[y][ct] = tile_t_mul(At + tile_at(ct, ct), mt[y][ct], zero4());
         }
 #pragma unroll
         for (int cp = 0; cp < NP; ++cp) {
-            if (2 * cp > r) continue;
-            bf16x4 lo[PIECES], hi[PIECES];
-            pieces4<PIECES>(mt[y][2 * cp], lo);
-            pieces4<PIECES>(2 * cp + 1 < NT ? mt[y][2 * cp + 1 < NT ? 2 * cp + 1 : 0] : zero4(), hi);  // zero past r
+            bf16x8 m[PIECES];
+            pieces8<PIECES>(mt[y][2 * cp], 2 * cp + 1 < NT ? mt[y][2 * cp + 1 < NT ? 2 * cp + 1 : 0] : zero4(), m);
+            if (2 * cp <= r)
 #pragma unroll
-            for (int s = 0; s < PIECES; ++s)
-                *reinterpret_cast<bf16x8 *>(smem + L::pair_at(r, cp) + 1024 * s + 16 * l) = cat(lo[s], hi[s]);
+                for (int s = 0; s < PIECES; ++s)
+                    *reinterpret_cast<bf16x8 *>(smem + L::pair_at(r, cp) + 1024 * s + 16 * l) = m[s];
         }
     }
-    // R, where not finite remembered and replaced
-    uint64_t lost[2] = {0, 0};  // nodes, in this lane's columns
-    bf16x8 rs[NP][2][PIECES];
+    // R, in the place of K h
+    float probe = 0.f;
 #pragma unroll
-    for (int cp = 0; cp < NP; ++cp) {
-        bf16x4 half[2][2][PIECES];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int rt = 2 * cp + e;
-            f32x4 x[2] = {zero4(), zero4()};
-            if (rt < NT && rt < nt) {
-                const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
-                const f32x4 b4 = *reinterpret_cast<const f32x4 *>(beta + 16 * rt + 4 * g);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[t][i] = b4[i] * (to_f32(v[rt < NT ? rt : 0][i][t]) - e4[i] * kh[rt < NT ? rt : 0][t][i]);
-                    if (!finite4(x[t]))
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!(fabsf(x[t][i]) < __builtin_inff())) {
-                                lost[t] |= 1ull << (16 * rt + 4 * g + i);
-                                x[t][i] = 0.f;
-                            }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) pieces4<PIECES>(x[t], half[e][t]);
-        }
+    for (int rt = 0; rt < NT; ++rt) {
+        const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
+        const f32x4 b4 = *reinterpret_cast<const f32x4 *>(beta + 16 * rt + 4 * g);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int s = 0; s < PIECES; ++s) rs[cp][t][s] = cat(half[0][t][s], half[1][t][s]);
+            for (int i = 0; i < 4; ++i) {
+                kh[rt][t][i] = b4[i] * (to_f32(v[rt][i][t]) - e4[i] * kh[rt][t][i]);
+                probe += 0.f * kh[rt][t][i];
+            }
     }
+    uint64_t lost[2] = {0, 0};  // nodes whose right-hand side in this lane's columns is not finite
+    if (__ballot(probe != probe))
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!(fabsf(kh[rt][t][i]) < __builtin_inff())) {
+                        lost[t] |= 1ull << (16 * rt + 4 * g + i);
+                        kh[rt][t][i] = 0.f;
+                    }
+    bf16x8 rs[NP][2][PIECES];
+#pragma unroll
+    for (int cp = 0; cp < NP; ++cp)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            pieces8<PIECES>(kh[2 * cp][t], 2 * cp + 1 < NT ? kh[2 * cp + 1 < NT ? 2 * cp + 1 : 0][t] : zero4(), rs[cp][t]);
     lds_barrier();
-    const int ob = p.Hv * V * (int)sizeof(Out);
-    const Rsrc out = rows_of(o + bos * p.Hv * V, n, ob, V * sizeof(Out));
     const uint64_t rows_lost = bad[0] | (uint64_t)bad[1] << 32;
     const bool poisoned = __ballot((lost[0] | lost[1] | rows_lost) != 0) != 0;
-    if (poisoned)
+    f32x4 o[NT][2];
+#pragma unroll
+    for (int rt = 0; rt < NT; ++rt) {
+        const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) o[rt][t] = e4 * qh[rt][t];
+    }
+#pragma unroll
+    for (int cp = 0; cp < NP; ++cp) {
+        bf16x8 m[NT][PIECES];
+#pragma unroll
+        for (int rt = 2 * cp; rt < NT; ++rt)
+#pragma unroll
+            for (int s = 0; s < PIECES; ++s)
+                m[rt][s] = *reinterpret_cast<const bf16x8 *>(smem + L::pair_at(rt, cp) + 1024 * s + 16 * l);
+        // the products that PIECES pieces of accuracy need, small ones first
+#pragma unroll
+        for (int sum = PIECES - 1; sum >= 0; --sum)
+#pragma unroll
+            for (int s = 0; s <= sum; ++s)
+#pragma unroll
+                for (int rt = 2 * cp; rt < NT; ++rt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(m[rt][s], rs[cp][t][sum - s], o[rt][t], 0, 0, 0);
+    }
+    if (poisoned) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {  // the column's nodes of all lane groups
             lost[t] |= rows_lost;
             lost[t] |= __shfl_xor(lost[t], 16);
             lost[t] |= __shfl_xor(lost[t], 32);
-        }
 #pragma unroll
-    for (int rt = 0; rt < NT; ++rt) {
-        if (rt >= nt) continue;
-        const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
-        f32x4 y[2];
+            for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) y[t] = e4 * qh[rt][t];
-#pragma unroll
-        for (int cp = 0; cp <= rt / 2; ++cp) {
-            bf16x8 m[PIECES];
-#pragma unroll
-            for (int s = 0; s < PIECES; ++s)
-                m[s] = *reinterpret_cast<const bf16x8 *>(smem + L::pair_at(rt, cp) + 1024 * s + 16 * l);
-            // the products that PIECES pieces of accuracy need, small ones first
-#pragma unroll
-            for (int sum = PIECES - 1; sum >= 0; --sum)
-#pragma unroll
-                for (int s = 0; s <= sum; ++s)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        y[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(m[s], rs[cp][t][sum - s], y[t], 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int node = 16 * rt + 4 * g + i;
-            pair x = {p.scale * y[0][i], p.scale * y[1][i]};
-            if (poisoned) {
-                const uint64_t path = mask[node] | 1ull << node;
-                if (path & lost[0]) x[0] = __builtin_nanf("");
-                if (path & lost[1]) x[1] = __builtin_nanf("");
-            }
-            store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * rt + i) * ob, x);
+                for (int i = 0; i < 4; ++i) {
+                    const int node = 16 * rt + 4 * g + i;
+                    if ((mask[node] | 1ull << node) & lost[t]) o[rt][t][i] = __builtin_nanf("");
+                }
         }
     }
+#pragma unroll
+    for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * rt + i) * ob,
+                   pair{p.scale * o[rt][0][i], p.scale * o[rt][1][i]});
+}
+
+// waves per SIMD that the registers leave room for (three spill where NT = 4)
+template <typename In, int V, int NT> constexpr int waves_per_simd() {
+    return NT < 4 ? 3 : sizeof(In) == 4 ? 1 : 2;
+}
+
+// trees of up to 16 NT nodes
+template <typename In, typename Out, int K, int V, int NT>
+__global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree_kernel(PoolParams p) {
+    extern __shared__ __align__(16) char smem[];
+    const int unit = xcd_runs(blockIdx.x, gridDim.x), j = unit / p.Hv, hv = unit - j * p.Hv;
+    int64_t bos, eos;
+    token_range(p, j, bos, eos);
+    const int64_t n = eos - bos;
+    if (n <= 0) return;
+    if (n > 16 * NT) {  // packed trees only: more than TREE_MAX nodes
+        const float fill = slot_of(p, j) < 0 ? 0.f : __builtin_nanf("");
+        Out *o = reinterpret_cast<Out *>(p.o) + hv * V;
+        for (int64_t i = bos * V + threadIdx.x; i < eos * V; i += 2 * V) o[i / V * p.Hv * V + i % V] = (Out)fill;
+        return;
+    }
+    if constexpr (NT == 4) {
+        if (n > 48) return tree<In, Out, K, V, 4>(p, smem, j, hv, bos, (int)n);
+        if (n > 32) return tree<In, Out, K, V, 3>(p, smem, j, hv, bos, (int)n);
+    }
+    if constexpr (NT >= 2)
+        if (n > 16) return tree<In, Out, K, V, 2>(p, smem, j, hv, bos, (int)n);
+    tree<In, Out, K, V, 1>(p, smem, j, hv, bos, (int)n);
 }
 
 template <typename In, typename Out, int K, int V, int NT> hipError_t launch(const PoolParams &p, hipStream_t s) {
