@@ -174,24 +174,6 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
             qx[t] = __builtin_amdgcn_raw_buffer_load_b128(qr, kq_row * qb + 16 * kq_chunk, t * ROWS * qb, 0);
         }
     }
-    // V and the state, whose slot is looked up only now
-    typedef In InPair __attribute__((ext_vector_type(2)));
-    InPair v[NT][4];
-    {
-        const int vb = (int)p.v_row * (int)sizeof(In);
-        const Rsrc vr = rows_of(reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos, p.v_batch, p.v_row) + hv * V, n,
-                                vb, V * sizeof(In));
-#pragma unroll
-        for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int lane = 4 * g * vb + col * (int)sizeof(In), at = (16 * rt + i) * vb;
-                if constexpr (sizeof(In) == 2)
-                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b32(vr, lane, at, 0));
-                else
-                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b64(vr, lane, at, 0));
-            }
-    }
     const int ob = p.Hv * V * (int)sizeof(Out);
     const Rsrc out = rows_of(reinterpret_cast<Out *>(p.o) + (bos * p.Hv + hv) * V, n, ob, V * sizeof(Out));
     const int slot = slot_of(p, j);
@@ -201,6 +183,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
             store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * (i / 4) + i % 4) * ob, pair{0.f, 0.f});
         return;
     }
+    // the state, whose slot is looked up only now
     pair h[K / 32][8];
     {
         const Rsrc hr = rows_of(p.states + (int64_t)slot * p.slot_stride + (int64_t)hv * K * V, K, 4 * V, 4 * V);
@@ -272,6 +255,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                     kk[ct] = X::row_step(s, kc[ct], kr, kk[ct]);
                     mt[y][ct] = X::row_step(s, kc[ct], qr, mt[y][ct]);
                 }
+            if constexpr (NT > 2) __builtin_amdgcn_sched_barrier(0);
         }
         const int node = 16 * r + c;
         const double Gb = G[node];
@@ -336,21 +320,42 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         for (int t = 0; t < 2; ++t)
             X::set(s[t], f32x4{h[kb][0][t], h[kb][1][t], h[kb][2][t], h[kb][3][t]},
                    f32x4{h[kb][4][t], h[kb][5][t], h[kb][6][t], h[kb][7][t]});
-        typename X::Row kr[NT], qr[NT];
+        // K's rows, then Q's: the rows of both at once would not leave the registers for a
+        // third wave per SIMD
 #pragma unroll
-        for (int rt = 0; rt < NT; ++rt) {
-            X::load(kr[rt], row(L::k, 16 * rt + c, kb));
-            X::load(qr[rt], row(L::q, 16 * rt + c, kb));
+        for (int kq = 0; kq < 2; ++kq) {
+            typename X::Row x[NT];
+#pragma unroll
+            for (int rt = 0; rt < NT; ++rt) X::load(x[rt], row(kq ? L::q : L::k, 16 * rt + c, kb));
+#pragma unroll
+            for (int step = 0; step < X::STATE_STEPS; ++step)
+#pragma unroll
+                for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        f32x4 &y = kq ? qh[rt][t] : kh[rt][t];
+                        y = X::state_step(step, x[rt], s[t], y);
+                    }
+            if constexpr (NT > 2) __builtin_amdgcn_sched_barrier(0);
         }
+    }
+    // V, in flight while M is solved (earlier, its registers would be missed)
+    typedef In InPair __attribute__((ext_vector_type(2)));
+    InPair v[NT][4];
+    {
+        const int vb = (int)p.v_row * (int)sizeof(In);
+        const Rsrc vr = rows_of(reinterpret_cast<const In *>(p.v) + row_offset(p, j, bos, p.v_batch, p.v_row) + hv * V, n,
+                                vb, V * sizeof(In));
 #pragma unroll
-        for (int step = 0; step < X::STATE_STEPS; ++step)
+        for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-            for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    kh[rt][t] = X::state_step(step, kr[rt], s[t], kh[rt][t]);
-                    qh[rt][t] = X::state_step(step, qr[rt], s[t], qh[rt][t]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int lane = 4 * g * vb + col * (int)sizeof(In), at = (16 * rt + i) * vb;
+                if constexpr (sizeof(In) == 2)
+                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b32(vr, lane, at, 0));
+                else
+                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b64(vr, lane, at, 0));
+            }
     }
     lds_barrier();
     // M's rows r, from the right; the products with K and Q are done, M takes their place
@@ -458,9 +463,9 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                    pair{p.scale * o[rt][0][i], p.scale * o[rt][1][i]});
 }
 
-// waves per SIMD that the registers leave room for (three spill where NT = 4)
+// waves per SIMD that the registers (and, where NT = 4, LDS) leave room for
 template <typename In, int V, int NT> constexpr int waves_per_simd() {
-    return NT < 4 ? 3 : sizeof(In) == 4 ? 1 : 2;
+    return NT < 4 ? 3 : sizeof(In) == 4 ? 1 : V == 64 ? 2 : 3;
 }
 
 // trees of up to 16 NT nodes
