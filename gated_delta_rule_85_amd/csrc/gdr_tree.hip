@@ -124,14 +124,15 @@ typedef float pair __attribute__((ext_vector_type(2)));
 // A buffer of n rows, `stride` bytes apart, of `bytes` bytes each: loads past its end give
 // zero and stores there are dropped, so that rows need no conditions
 typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr int ONCE = 2;  // nontemporal: the state and the output, which pass by once
 __device__ __forceinline__ Rsrc rows_of(const void *base, int n, int stride, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (n - 1) * stride + bytes, 0x00027000);
 }
 __device__ __forceinline__ void store2(float, Rsrc r, int lane, int at, pair x) {
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, lane, at, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, lane, at, ONCE);
 }
 __device__ __forceinline__ void store2(bf16, Rsrc r, int lane, int at, pair x) {
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2)), r, lane, at, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2)), r, lane, at, ONCE);
 }
 
 // One tree of n nodes, up to 16 NT, and one v head; every wave of the workgroup calls it.
@@ -192,7 +193,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 h[kb][i] = __builtin_bit_cast(
-                    pair, __builtin_amdgcn_raw_buffer_load_b64(hr, (8 * g * V + col) * 4, (32 * kb + i) * V * 4, 0));
+                    pair, __builtin_amdgcn_raw_buffer_load_b64(hr, (8 * g * V + col) * 4, (32 * kb + i) * V * 4, ONCE));
     }
 #pragma unroll
     for (int t = 0; t < TURNS; ++t)
