@@ -102,17 +102,16 @@ template <int LW, int NT, int RN> hipError_t launch(const CopyParams &p, hipStre
 
 }  // namespace
 
-// Few entries: wide columns, so that a slot's bytes move in runs of 1 KB.  Many: narrow
-// ones, since all entries' columns are held at once.  Measured at slots of 2 MB in a pool of
-// 2 GB, states read and written per second: 250 entries at 5.0 TB/s with 256-byte columns
-// (5.2 with 1 KB ones and 1024 threads, but 100 entries at 7.2 instead of 7.7), 900 entries
-// 4.8 (4.2 with 128-byte columns and 512 threads), 3000 of 512 KB at 3.4; 61 entries of 12
-// layers at 6.0 (5.2 with a store through the caches and columns dealt round robin).
+// Few entries: wide columns, so that a slot's bytes move in runs of 1 KB.  Many: narrower
+// ones, since all entries' columns are held at once.  Measured over cold pools, states read
+// and written per second: 61 entries of 12 layers 5.15 TB/s with 512-byte columns and 1024
+// threads (4.7 with 1 KB and 256 threads, 4.6 with 256 bytes and 512), 128 of 12 layers 5.0
+// (4.6 with 256 bytes), 250 of 2 MB 4.7 (4.8); 900 of 2 MB 4.8 with 256-byte columns (4.2 with
+// 128 bytes and 512 threads); 3000 of 512 KB 3.4 with 64 bytes.
 hipError_t launch_copy(const CopyParams &p, hipStream_t s) {
     if (p.n <= 4) return launch<64, 256, 1>(p, s);
     if (p.n <= 16) return launch<64, 256, 4>(p, s);
-    if (p.n <= 64) return launch<64, 256, 16>(p, s);
-    if (p.n <= 256) return launch<16, 512, 8>(p, s);
+    if (p.n <= 256) return launch<32, 1024, 8>(p, s);
     if (p.n <= 1024) return launch<16, 1024, 16>(p, s);
     return launch<4, 1024, 16>(p, s);  // up to COPY_MAX = 4096
 }

@@ -82,16 +82,6 @@ __device__ __forceinline__ void store4_once(float *p, f32x4 x) {
     __builtin_nontemporal_store(x, reinterpret_cast<f32x4 *>(p));
 }
 
-// four values at a column, as the output's type
-__device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
-__device__ __forceinline__ void store4(bf16 *p, f32x4 x) {
-    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(x, bf16x4);
-}
-__device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-__device__ __forceinline__ f32x4 load4(const bf16 *p) {
-    return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), f32x4);
-}
-
 hipError_t launch_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s);
 hipError_t launch_accept(Dt dt, int K, int V, const PoolParams &p, hipStream_t s);
 // most: an upper bound on the nodes of a tree (1 .. TREE_MAX)

@@ -16,12 +16,48 @@
 namespace gdr {
 namespace {
 
-// sum over the lanes l ^ 8, l ^ 16, l ^ 32 (the row groups), in every lane
-__device__ __forceinline__ float sum_row_groups(float x) {
-    x += dpp_mov<0x128>(x);  // row_ror:8
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
+// Sums over the lanes with the same l & 7 (the row groups).  v_permlane32_swap_b32 exchanges
+// the upper half of its first register with the lower half of its second, v_permlane16_swap_b32
+// the odd rows of 16 lanes of the first with the even ones of the second: two values are
+// reduced in one exchange and one addition, and lie in a half (a row) of the lanes each.
+struct Swapped {
+    float a, b;
+};
+__device__ __forceinline__ Swapped swap32(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t r0 = r[0], r1 = r[1];
+    return {__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1)};
+}
+__device__ __forceinline__ Swapped swap16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t r0 = r[0], r1 = r[1];
+    return {__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1)};
+}
+// a second register with x's value, which the exchange writes too
+__device__ __forceinline__ float twin(float x) {
+    asm volatile("" : "+v"(x));
     return x;
+}
+// column of the lane's four whose sum it gets
+__device__ __forceinline__ int my_column(int l) { return (l >> 5 & 1) | (l >> 3 & 2); }
+__device__ __forceinline__ float sum_columns(f32x4 x) {
+    const Swapped p = swap32(x[0], x[1]), q = swap32(x[2], x[3]);
+    const Swapped y = swap16(p.a + p.b, q.a + q.b);
+    const float z = y.a + y.b;
+    return z + dpp_mov<0x128>(z);  // row_ror:8
+}
+__device__ __forceinline__ float sum_all(float x) {
+    x += dpp_mov<0x128>(x);
+    const Swapped y = swap16(x, twin(x));
+    x = y.a + y.b;
+    const Swapped z = swap32(x, twin(x));
+    return z.a + z.b;
+}
+// every column's value from the lanes that have it
+__device__ __forceinline__ f32x4 gather_columns(float x) {
+    const Swapped y = swap16(x, twin(x));
+    const Swapped lo = swap32(y.a, twin(y.a)), hi = swap32(y.b, twin(y.b));
+    return f32x4{lo.a, lo.b, hi.a, hi.b};
 }
 
 // R consecutive inputs
@@ -39,8 +75,7 @@ template <typename In, int R> struct Rows {
 
 template <typename In, int R, bool OUT> struct Token {
     Rows<In, R> k, q;
-    f32x4 v;
-    float g, beta;
+    float v, g, beta;
 };
 
 template <typename In, typename Out, int K, bool ACCEPT>
@@ -48,12 +83,13 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     constexpr int R = K / 8;
     const int unit = xcd_runs(blockIdx.x, gridDim.x), vt = __builtin_amdgcn_readfirstlane(wave_id());
     const int j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
-    const int l = lane_id(), col = vt * 32 + 4 * (l & 7), row0 = R * (l >> 3);
+    const int l = lane_id(), col = vt * 32 + 4 * (l & 7), row0 = R * (l >> 3), mine = col + my_column(l);
     int64_t bos, eos;
     token_range(p, j, bos, eos);
     if (bos >= eos) return;
     const int slot = slot_of(p, j);
-    Out *o = reinterpret_cast<Out *>(p.o) + hv * V + col;
+    Out *o = reinterpret_cast<Out *>(p.o) + hv * V + mine;
+    const bool writes = (l & 8) == 0;
     uint64_t path = 0;  // the accepted nodes
     if constexpr (ACCEPT) {
         if (slot < 0 || eos - bos > TREE_MAX) return;
@@ -70,8 +106,8 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     }
     if (slot < 0 || slot_taken(p, j, slot)) {
         if constexpr (!ACCEPT) {
-            if (l < 8)
-                for (int64_t i = bos; i < eos; ++i) store4(o + i * p.Hv * V, zero4());
+            if (writes)
+                for (int64_t i = bos; i < eos; ++i) o[i * p.Hv * V] = (Out)0.f;
         }
         return;
     }
@@ -83,12 +119,12 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
 
     const In *kp = reinterpret_cast<const In *>(p.k) + hq * K + row0;
     const In *qp = reinterpret_cast<const In *>(p.q) + hq * K + row0;
-    const In *vp = reinterpret_cast<const In *>(p.v) + hv * V + col;
+    const In *vp = reinterpret_cast<const In *>(p.v) + hv * V + mine;
     Token<In, R, !ACCEPT> now, next;
     auto fetch = [&](Token<In, R, !ACCEPT> &t, int64_t i) {
         t.k.load(kp + row_offset(p, j, i, p.k_batch, p.k_row));
         if constexpr (!ACCEPT) t.q.load(qp + row_offset(p, j, i, p.q_batch, p.q_row));
-        t.v = load4(vp + row_offset(p, j, i, p.v_batch, p.v_row));
+        t.v = to_f32(vp[row_offset(p, j, i, p.v_batch, p.v_row)]);
         t.g = p.g[i * p.Hv + hv];
         t.beta = p.beta[i * p.Hv + hv];
     };
@@ -105,16 +141,13 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         }
         // full-precision exponential: its error would otherwise grow with every token
         const float eg = expf(t.g);
-        f32x4 u;
+        const float u = t.beta * (t.v - eg * sum_columns(kh));
+        const f32x4 us = gather_columns(u);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) u[c] = t.beta * (t.v[c] - eg * sum_row_groups(kh[c]));
-#pragma unroll
-        for (int r = 0; r < R; ++r) h[r] = eg * h[r] + t.k[r] * u;
+        for (int r = 0; r < R; ++r) h[r] = eg * h[r] + t.k[r] * us;
         if constexpr (!ACCEPT) {
-            qk = sum_row_groups(qk);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) qh[c] = p.scale * (eg * sum_row_groups(qh[c]) + qk * u[c]);
-            if (l < 8) store4(o + i * p.Hv * V, qh);
+            const float y = p.scale * (eg * sum_columns(qh) + sum_all(qk) * u);
+            if (writes) o[i * p.Hv * V] = (Out)y;
         }
     };
     if constexpr (ACCEPT) {
