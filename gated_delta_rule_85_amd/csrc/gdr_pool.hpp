@@ -60,6 +60,7 @@ __device__ __forceinline__ int64_t row_offset(const PoolParams &p, int j, int64_
 __device__ __forceinline__ bool slot_taken(const PoolParams &p, int j, int slot) {
     if (!p.slots) return false;
     bool taken = false;
+#pragma unroll 4
     for (int i = lane_id(); i < j; i += 64) {
         int64_t b = 0, e = 1;
         if (p.cu) token_range(p, i, b, e);

@@ -122,17 +122,18 @@ template <int PIECES> struct Operands<float, PIECES> {
 typedef float pair __attribute__((ext_vector_type(2)));
 
 // A buffer of n rows, `stride` bytes apart, of `bytes` bytes each: loads past its end give
-// zero and stores there are dropped, so that rows need no conditions
+// zero and stores there are dropped, so that rows need no conditions.  (Where that can
+// happen the whole offset is the lane's, the part that is always compared with the end.)
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr int ONCE = 2;  // nontemporal: the state and the output, which pass by once
 __device__ __forceinline__ Rsrc rows_of(const void *base, int n, int stride, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (n - 1) * stride + bytes, 0x00027000);
 }
-__device__ __forceinline__ void store2(float, Rsrc r, int lane, int at, pair x) {
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, lane, at, ONCE);
+__device__ __forceinline__ void store2(float, Rsrc r, int at, pair x) {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), r, at, 0, ONCE);
 }
-__device__ __forceinline__ void store2(bf16, Rsrc r, int lane, int at, pair x) {
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2)), r, lane, at, ONCE);
+__device__ __forceinline__ void store2(bf16, Rsrc r, int at, pair x) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2)), r, at, 0, ONCE);
 }
 
 // One tree of n nodes, up to 16 NT, and one v head; every wave of the workgroup calls it.
@@ -171,8 +172,8 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                                 qb, K * sizeof(In));
 #pragma unroll
         for (int t = 0; t < TURNS; ++t) {
-            kx[t] = __builtin_amdgcn_raw_buffer_load_b128(kr, kq_row * kb + 16 * kq_chunk, t * ROWS * kb, 0);
-            qx[t] = __builtin_amdgcn_raw_buffer_load_b128(qr, kq_row * qb + 16 * kq_chunk, t * ROWS * qb, 0);
+            kx[t] = __builtin_amdgcn_raw_buffer_load_b128(kr, (t * ROWS + kq_row) * kb + 16 * kq_chunk, 0, 0);
+            qx[t] = __builtin_amdgcn_raw_buffer_load_b128(qr, (t * ROWS + kq_row) * qb + 16 * kq_chunk, 0, 0);
         }
     }
     const int ob = p.Hv * V * (int)sizeof(Out);
@@ -181,7 +182,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     if (slot < 0) {
 #pragma unroll
         for (int i = 0; i < 4 * NT; ++i)
-            store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * (i / 4) + i % 4) * ob, pair{0.f, 0.f});
+            store2(Out(), out, (16 * (i / 4) + 4 * g + i % 4) * ob + col * (int)sizeof(Out), pair{0.f, 0.f});
         return;
     }
     // the state, whose slot is looked up only now
@@ -351,11 +352,11 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int lane = 4 * g * vb + col * (int)sizeof(In), at = (16 * rt + i) * vb;
+                const int at = (16 * rt + 4 * g + i) * vb + col * (int)sizeof(In);
                 if constexpr (sizeof(In) == 2)
-                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b32(vr, lane, at, 0));
+                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b32(vr, at, 0, 0));
                 else
-                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b64(vr, lane, at, 0));
+                    v[rt][i] = __builtin_bit_cast(InPair, __builtin_amdgcn_raw_buffer_load_b64(vr, at, 0, 0));
             }
     }
     lds_barrier();
@@ -460,7 +461,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            store2(Out(), out, 4 * g * ob + col * (int)sizeof(Out), (16 * rt + i) * ob,
+            store2(Out(), out, (16 * rt + 4 * g + i) * ob + col * (int)sizeof(Out),
                    pair{p.scale * o[rt][0][i], p.scale * o[rt][1][i]});
 }
 

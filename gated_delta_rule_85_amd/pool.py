@@ -23,23 +23,12 @@ from . import _lib
 from .api import _DT, _c, check_offsets
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+# the current stream's handle, without a Stream object around it (1.8 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _refuse_gradients():
     raise ValueError("the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()")
-
-
-def _one_gpu(dev, *tensors):
-    if dev.type != "cuda":
-        raise ValueError("inputs must be on the GPU")
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError("all tensors must be on one GPU")
 
 
 def _rows(x, per16):
@@ -53,36 +42,12 @@ def _rows(x, per16):
     if T < 2:
         row = 0
     if one != 1 or (head != D and H > 1) or batch % per16 or row % per16 or row >= 1 << 23 or x.data_ptr() % 16:
-        x = x.contiguous()
+        x = x.clone(memory_format=torch.contiguous_format)  # (also where it is contiguous, but unaligned)
         batch, row = T * H * D, H * D
     return x, row, batch
 
 
-def _check_tokens(q, k, v, g, beta, cu_seqlens):
-    """The sizes B, T, H_q, K, H_v, V and the number of sequences."""
-    dtype = k.dtype
-    if k.dim() != 4 or v.dim() != 4 or (q is not None and q.shape != k.shape):
-        raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
-    B, T, H_q, K = k.shape
-    B_v, T_v, H_v, V = v.shape
-    if B_v != B or T_v != T:
-        raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
-    if dtype not in _DT or v.dtype != dtype or (q is not None and q.dtype != dtype):
-        raise ValueError("q, k, v must share one dtype, bfloat16 or float32")
-    if g.shape != (B, T, H_v) or beta.shape != (B, T, H_v):
-        raise ValueError("g and beta must be [B,T,H_v]")
-    if cu_seqlens is None:
-        return B, T, H_q, K, H_v, V, B
-    if B != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must be int32 [N+1] with B == 1")
-    if not cu_seqlens.is_cuda:
-        check_offsets(cu_seqlens, T)
-    return B, T, H_q, K, H_v, V, cu_seqlens.numel() - 1
-
-
-def _check_states(states, H_v, K, V, name="states"):
-    if states.dim() != 4 or states.dtype != torch.float32 or (H_v is not None and states.shape[1:] != (H_v, K, V)):
-        raise ValueError("%s must be float32 [n_slots,H_v,K,V]" % name)
+def _check_states(states, name="states"):
     n, H, K, V = states.shape
     slot, head, row, one = states.stride()
     if n < 1 or one != 1 or row != V or (head != K * V and H > 1) or states.data_ptr() % 16 or \
@@ -98,16 +63,10 @@ def _indices(x, n, what, lo, hi):
         raise ValueError("%s out of range [%d, %d)" % (what, lo, hi))
 
 
-def _check_slots(slots, n_seq, n_slots, distinct):
-    if slots is None:
-        if n_slots < n_seq:
-            raise ValueError("states has %d slots for %d sequences" % (n_slots, n_seq))
-        return
-    _indices(slots, n_seq, "slots", -1, n_slots)
-    if distinct and not slots.is_cuda:
-        used = slots[slots >= 0]
-        if used.unique().numel() != used.numel():
-            raise ValueError("slots names a slot twice")
+def _check_distinct(slots):
+    used = slots[slots >= 0]
+    if used.unique().numel() != used.numel():
+        raise ValueError("slots names a slot twice")
 
 
 def _check_parents(parents, B, T, cu_seqlens):
@@ -128,18 +87,14 @@ def _check_parents(parents, B, T, cu_seqlens):
             raise ValueError("a node's parent is -1 or an earlier node of its tree")
 
 
-def _output(out, output_dtype, v, *inputs):
-    if out is None:
-        if output_dtype not in _DT:
-            raise ValueError("output_dtype must be bfloat16 or float32")
-        return torch.empty_like(v, dtype=output_dtype, memory_format=torch.contiguous_format)
+def _check_out(out, v, *inputs):
     if out.shape != v.shape or out.dtype not in _DT or not out.is_contiguous() or out.data_ptr() % 16:
         raise ValueError("out must be contiguous [B,T,H_v,V], bfloat16 or float32, 16-byte aligned")
-    _one_gpu(v.device, out)
+    if out.device != v.device:
+        raise ValueError("all tensors must be on one GPU")
     for x in (v,) + inputs:
         if _overlap(out, x):
             raise ValueError("out overlaps an input")
-    return out
 
 
 def _span(t):
@@ -169,27 +124,94 @@ def _on(x, dev):
     return x.contiguous()
 
 
-def _pool_call(call, sizes, q, k, v, g, beta, parents, accepted, states, scale, cu_seqlens, slots, o):
-    B, T, H_q, K, H_v, V, n_seq = sizes
-    dev, dtype = states.device, _DT[k.dtype]
-    per16 = 8 if dtype == _lib.BF16 else 4
-    k, k_row, k_batch = _rows(k, per16)
-    v, v_row, v_batch = _rows(v, per16)
-    q, q_row, q_batch = (None, 0, 0) if q is None else _rows(q, per16)
-    g, beta = _c(g, torch.float32), _c(beta, torch.float32)
+def _run(call, q, k, v, g, beta, parents, accepted, states, scale, cu_seqlens, slots, output_dtype, out):
+    """Checks the arguments of an operator and launches it; returns its output (None for an
+    acceptance, which has no q).  Written out in one piece, since it runs once per token."""
+    if k.dim() != 4 or v.dim() != 4 or (q is not None and q.shape != k.shape):
+        raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
+    B, T, H_q, K = k.shape
+    B_v, T_v, H_v, V = v.shape
+    if B_v != B or T_v != T:
+        raise ValueError("expected q, k [B,T,H_q,K] and v [B,T,H_v,V]")
+    dtype = _DT.get(k.dtype)
+    if dtype is None or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k, v must share one dtype, bfloat16 or float32")
+    tokens = (B, T, H_v)
+    if g.shape != tokens or beta.shape != tokens:
+        raise ValueError("g and beta must be [B,T,H_v]")
+    n_seq = B
     if cu_seqlens is not None:
-        cu_seqlens = _on(cu_seqlens, dev)
-    if slots is not None:
-        slots = _on(slots, dev)
+        if B != 1 or cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be int32 [N+1] with B == 1")
+        if not cu_seqlens.is_cuda:
+            check_offsets(cu_seqlens, T)
+        n_seq = cu_seqlens.numel() - 1
     if parents is not None:
-        parents = _on(parents, dev)
+        _check_parents(parents, B, T, cu_seqlens)
+    if states.dtype != torch.float32 or states.dim() != 4 or states.shape[1:] != (H_v, K, V):
+        raise ValueError("states must be float32 [n_slots,H_v,K,V]")
+    _check_states(states)
+    n_slots = states.shape[0]
+    if slots is None:
+        if n_slots < n_seq:
+            raise ValueError("states has %d slots for %d sequences" % (n_slots, n_seq))
+    else:
+        _indices(slots, n_seq, "slots", -1, n_slots)
+        if not slots.is_cuda and (parents is None or accepted is not None):
+            _check_distinct(slots)  # (trees that are only read may share one)
     if accepted is not None:
-        accepted = _on(accepted, dev)
+        _indices(accepted, n_seq, "accepted", -1, _lib.TREE_MAX if cu_seqlens is not None else T)
+    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad or g.requires_grad or beta.requires_grad
+                                    or states.requires_grad or (q is not None and q.requires_grad)):
+        _refuse_gradients()
+    dev = states.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on the GPU")
+    if k.device != dev or v.device != dev or g.device != dev or beta.device != dev or (q is not None and q.device != dev):
+        raise ValueError("all tensors must be on one GPU")
+    o = None
+    if q is not None:
+        if out is not None:
+            _check_out(out, v, q, k, g, beta, states)
+            o = out
+        elif output_dtype not in _DT:
+            raise ValueError("output_dtype must be bfloat16 or float32")
+        else:
+            o = torch.empty_like(v, dtype=output_dtype, memory_format=torch.contiguous_format)
+    # contiguous rows of 16-byte aligned tensors are read as they are; _rows looks at others
+    per16 = 8 if dtype == _lib.BF16 else 4
+    q_row, k_row, v_row = H_q * K, H_q * K, H_v * V
+    q_batch, k_batch, v_batch = T * q_row, T * k_row, T * v_row
+    kp, vp, qp = k.data_ptr(), v.data_ptr(), 0
+    if kp % 16 or not k.is_contiguous():
+        k, k_row, k_batch = _rows(k, per16)
+        kp = k.data_ptr()
+    if vp % 16 or not v.is_contiguous():
+        v, v_row, v_batch = _rows(v, per16)
+        vp = v.data_ptr()
+    if q is not None:
+        qp = q.data_ptr()
+        if qp % 16 or not q.is_contiguous():
+            q, q_row, q_batch = _rows(q, per16)
+            qp = q.data_ptr()
+    g, beta = _c(g, torch.float32), _c(beta, torch.float32)
+    cu, sl, pa, ac = cu_seqlens, slots, parents, accepted
+    if cu is not None:
+        cu = _on(cu, dev)
+    if sl is not None:
+        sl = _on(sl, dev)
+    if pa is not None:
+        pa = _on(pa, dev)
+    if ac is not None:
+        ac = _on(ac, dev)
     args = _lib.PoolArgs(
-        B, T, H_q, H_v, K, V, n_seq, states.shape[0], states.stride(0), q_row, k_row, v_row, q_batch, k_batch, v_batch,
-        dtype, _lib.F32 if o is None else _DT[o.dtype], scale, _ptr(q), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-        beta.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _ptr(parents), _ptr(accepted), states.data_ptr(), _ptr(o))
+        B, T, H_q, H_v, K, V, n_seq, n_slots, states.stride(0), q_row, k_row, v_row, q_batch, k_batch, v_batch,
+        dtype, _lib.F32 if o is None else _DT[o.dtype], K ** -0.5 if scale is None else float(scale), qp, kp, vp, g.data_ptr(),
+        beta.data_ptr(), None if cu is None else cu.data_ptr(), None if sl is None else sl.data_ptr(),
+        None if pa is None else pa.data_ptr(), None if ac is None else ac.data_ptr(), states.data_ptr(),
+        None if o is None else o.data_ptr())
     _launch(call, args, dev)
+    return o
 
 
 def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=None, *, slots=None,
@@ -211,18 +233,7 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=
     zero; so is a sequence that names a slot which an earlier one has.  ``out``: a
     contiguous tensor to write; rows that belong to no sequence are left as they are.
     """
-    sizes = _check_tokens(q, k, v, g, beta, cu_seqlens)
-    _, _, _, K, H_v, V, n_seq = sizes
-    _check_states(states, H_v, K, V)
-    _check_slots(slots, n_seq, states.shape[0], True)
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
-                                    or beta.requires_grad or states.requires_grad):
-        _refuse_gradients()
-    _one_gpu(states.device, q, k, v, g, beta)
-    o = _output(out, output_dtype, v, q, k, g, beta, states)
-    _pool_call(_lib.step, sizes, q, k, v, g, beta, None, None, states, K ** -0.5 if scale is None else float(scale),
-               cu_seqlens, slots, o)
-    return o
+    return _run(_lib.step, q, k, v, g, beta, None, None, states, scale, cu_seqlens, slots, output_dtype, out)
 
 
 def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seqlens=None, *, slots=None,
@@ -240,19 +251,7 @@ def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seql
     than 64 nodes rows of NaN.  The other arguments are those of
     :func:`recurrent_gated_delta_rule`.
     """
-    sizes = _check_tokens(q, k, v, g, beta, cu_seqlens)
-    B, T, _, K, H_v, V, n_seq = sizes
-    _check_parents(parents, B, T, cu_seqlens)
-    _check_states(states, H_v, K, V)
-    _check_slots(slots, n_seq, states.shape[0], False)
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
-                                    or beta.requires_grad or states.requires_grad):
-        _refuse_gradients()
-    _one_gpu(states.device, q, k, v, g, beta)
-    o = _output(out, output_dtype, v, q, k, g, beta, states)
-    _pool_call(_lib.tree, sizes, q, k, v, g, beta, parents, None, states, K ** -0.5 if scale is None else float(scale),
-               cu_seqlens, slots, o)
-    return o
+    return _run(_lib.tree, q, k, v, g, beta, parents, None, states, scale, cu_seqlens, slots, output_dtype, out)
 
 
 def tree_gated_delta_rule_accept(k, v, g, beta, parents, accepted, states, cu_seqlens=None, *, slots=None):
@@ -265,32 +264,22 @@ def tree_gated_delta_rule_accept(k, v, g, beta, parents, accepted, states, cu_se
     each tree, or -1 for none (the state then stays as it is).  A sequence that names
     a slot which an earlier one has is skipped.
     """
-    sizes = _check_tokens(None, k, v, g, beta, cu_seqlens)
-    B, T, _, K, H_v, V, n_seq = sizes
-    _check_parents(parents, B, T, cu_seqlens)
-    _check_states(states, H_v, K, V)
-    _check_slots(slots, n_seq, states.shape[0], True)
-    _indices(accepted, n_seq, "accepted", -1, _lib.TREE_MAX if cu_seqlens is not None else T)
-    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad or g.requires_grad or beta.requires_grad
-                                    or states.requires_grad):
-        _refuse_gradients()
-    _one_gpu(states.device, k, v, g, beta)
-    _pool_call(_lib.tree_accept, sizes, None, k, v, g, beta, parents, accepted, states, 1.0, cu_seqlens, slots, None)
+    _run(_lib.tree_accept, None, k, v, g, beta, parents, accepted, states, 1.0, cu_seqlens, slots, None, None)
     return states
 
 
 def _check_pool(x, name):
     """One layer's pool, or [layers, ...] of them."""
+    if x.dtype != torch.float32 or x.dim() not in (4, 5):
+        raise ValueError("%s must be float32 [n_slots,H_v,K,V] or [layers,n_slots,H_v,K,V]" % name)
     if x.dim() == 5:
         n, inner = x.shape[0], x.shape[2] * x.shape[3] * x.shape[4]
         if n > 1 and (x.stride(0) % 4 or x.stride(0) < inner):
             raise ValueError("a slot of %s must be contiguous and 16-byte aligned" % name)
         if n > 0:
-            _check_states(x[0], None, None, None, name)
-    elif x.dim() == 4:
-        _check_states(x, None, None, None, name)
+            _check_states(x[0], name)
     else:
-        raise ValueError("%s must be float32 [n_slots,H_v,K,V] or [layers,n_slots,H_v,K,V]" % name)
+        _check_states(x, name)
 
 
 def copy_states(states, dst, src, source=None):
@@ -328,7 +317,10 @@ def copy_states(states, dst, src, source=None):
     if torch.is_grad_enabled() and (states.requires_grad or source.requires_grad):
         _refuse_gradients()
     dev = states.device
-    _one_gpu(dev, source)
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on the GPU")
+    if source.device != dev:
+        raise ValueError("all tensors must be on one GPU")
     dst, src = _on(dst, dev), _on(src, dev)
     H, K, V = states.shape[-3:]
     layers, layer, source_layer = 1, 0, 0

@@ -168,6 +168,41 @@ def test_rows_behind_the_last_sequence_are_left():
         assert bool((out[:, 3:] == 9).all()) and bool((out[:, :3] != 9).all())
 
 
+@pytest.mark.parametrize("n", [1, 3, 17, 33, 49, 63, 64])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_rows_behind_a_tree_are_left(n, out_dtype):
+    """The tiles of 16 nodes end inside the rows: what follows belongs to nobody."""
+    x = ref.make(0, 0, 2, 4, 64, 128, BF, [n, 80 - n], seed=n)
+    x["parents"] = torch.tensor([list(range(-1, n - 1)) + [-1] * (80 - n)], **I32)
+    for name in ("q", "k", "v", "g", "beta"):
+        x[name][:, n:] = float("nan")
+    first = {m: x[m][:, :n] for m in ("q", "k", "v", "g", "beta")}
+    o_want, _, X = ref.recurrent(dict(x, **first, cu=torch.tensor([0, n])))
+    d = ref.cuda(x)
+    out = torch.full((1, 80, 4, 128), 9.0, dtype=out_dtype, device="cuda")
+    run_tree(dict(d, cu=torch.tensor([0, n], **I32, device="cuda"), slots=d["slots"][:1]), out=out)
+    ref.near(out[:, :n], o_want, n, 64, X)
+    assert bool((out[:, n:] == 9).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tensors_that_are_not_aligned_are_copied(dtype):
+    x = ref.make(2, 3, 2, 4, 64, 64, dtype, seed=14)
+    x["parents"], x["accepted"] = torch.tensor([[-1, 0, 1]] * 2, **I32), torch.tensor([2, 2], **I32)
+    o_want, s_want, X = ref.recurrent(x)
+    for name in ("q", "k", "v"):
+        d = ref.cuda(x)
+        off = torch.zeros(d[name].numel() + 1, dtype=dtype, device="cuda")[1:].view(d[name].shape)
+        d[name] = off.copy_(d[name])
+        assert d[name].data_ptr() % 16
+        ref.near(run_tree(d), o_want, 3, 64, X)
+        e = dict(d, states=d["states"].clone())
+        run_accept(e)
+        ref.near(run_recurrent(d), o_want, 3, 64, X)
+        ref.near(d["states"], s_want, 3, 64, X)
+        assert torch.equal(d["states"], e["states"])
+
+
 def test_offsets_out_of_range_on_the_device_touch_nothing_else():
     x = ref.make(0, 0, 1, 2, 64, 64, F32, [2, 1, 2], seed=10)
     x["parents"] = torch.tensor([[-1, 0, -1, 0, 0]], **I32)
