@@ -3,6 +3,7 @@
 #pragma once
 
 #include "gdr_kernels.hpp"
+#include "gdr_lds.hpp"
 
 namespace gdr {
 
@@ -56,17 +57,30 @@ __device__ __forceinline__ int slot_of(const PoolParams &p, int j) {
 __device__ __forceinline__ int64_t row_offset(const PoolParams &p, int j, int64_t i, int64_t batch, int64_t row) {
     return p.cu ? i * row : (int64_t)j * batch + (i - (int64_t)j * p.T) * row;
 }
-// whether an earlier sequence with tokens names the same slot (every lane of the wave calls it)
+// whether an earlier sequence with tokens names the same slot; every thread of the workgroup
+// calls it, for one sequence.  A wave looks through a thousand entries by itself and shares
+// longer lists with the others (32768 sequences of two small heads: 757 us a step without
+// sharing, 540 with it; 368 without slots to look through)
 __device__ __forceinline__ bool slot_taken(const PoolParams &p, int j, int slot) {
     if (!p.slots) return false;
+    __shared__ int found;
+    const bool share = j >= 1024;
+    if (share) {
+        if (threadIdx.x == 0) found = 0;
+        lds_barrier();
+    }
     bool taken = false;
+    const int step = share ? (int)blockDim.x : 64;
 #pragma unroll 4
-    for (int i = lane_id(); i < j; i += 64) {
+    for (int i = share ? (int)threadIdx.x : lane_id(); i < j; i += step) {
         int64_t b = 0, e = 1;
         if (p.cu) token_range(p, i, b, e);
         taken |= p.slots[i] == slot && e > b;
     }
-    return __ballot(taken) != 0;
+    if (!share) return __ballot(taken) != 0;
+    if (taken) found = 1;
+    lds_barrier();
+    return found != 0;
 }
 
 // Workgroup id -> head such that an XCD takes runs of 8 consecutive heads (the hardware

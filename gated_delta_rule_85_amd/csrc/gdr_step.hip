@@ -104,13 +104,11 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         }
         if (!path) return;
     }
-    if (slot < 0 || slot_taken(p, j, slot)) {
-        if constexpr (!ACCEPT) {
-            if (writes)
-                for (int64_t i = bos; i < eos; ++i) o[i * p.Hv * V] = (Out)0.f;
-        }
-        return;
-    }
+    auto skip = [&] {
+        if (!ACCEPT && writes)
+            for (int64_t i = bos; i < eos; ++i) o[i * p.Hv * V] = (Out)0.f;
+    };
+    if (slot < 0) return skip();
 
     float *h0 = p.states + (int64_t)slot * p.slot_stride + ((int64_t)hv * K + row0) * V + col;
     f32x4 h[R];
@@ -150,8 +148,10 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
             if (writes) o[i * p.Hv * V] = (Out)y;
         }
     };
+    fetch(now, ACCEPT ? bos + __builtin_ctzll(path) : bos);
+    // with the loads in flight: a skipped sequence's are not used
+    if (slot_taken(p, j, slot)) return skip();
     if constexpr (ACCEPT) {
-        fetch(now, bos + __builtin_ctzll(path));
         for (;;) {
             const int64_t i = bos + __builtin_ctzll(path);
             path &= path - 1;
@@ -161,7 +161,6 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
             now = next;
         }
     } else {
-        fetch(now, bos);
         for (int64_t i = bos;;) {
             if (i + 1 < eos) fetch(next, i + 1);
             step(now, i);

@@ -137,21 +137,23 @@ def test_padding_and_repeated_slots_are_skipped():
     untouched(d["states"], x["states"], [4, 5])
 
 
-def test_many_sequences_with_a_repeated_slot():
-    """The lookup of earlier owners over more sequences than a wave has lanes."""
-    N = 300
+@pytest.mark.parametrize("N", [300, 1500])
+def test_many_sequences_with_a_repeated_slot(N):
+    """The lookup of earlier owners over more sequences than a wave has lanes, and over more
+    than a wave looks through alone."""
     x = ref.make(N, 1, 1, 1, 64, 64, F32, seed=9)
     d = ref.cuda(x)
+    again = {257: 3, N - 1: 130, N // 2: 0}
     slots = x["slots"].clone()
-    slots[257] = slots[3]
-    slots[299] = slots[130]
+    for late, early in again.items():
+        slots[late] = slots[early]
     d["slots"] = slots.cuda()
     o = run_recurrent(d)
-    keep = [i for i in range(N) if i not in (257, 299)]
-    o_want, s_want, X = ref.recurrent(dict(x, slots=x["slots"]))
+    keep = [i for i in range(N) if i not in again]
+    o_want, s_want, X = ref.recurrent(x)
     ref.near(o[keep], o_want[keep], 1, 64, X)
-    assert bool((o[[257, 299]] == 0).all())
-    lost = [int(x["slots"][i]) for i in (257, 299)]
+    assert bool((o[list(again)] == 0).all())
+    lost = [int(x["slots"][i]) for i in again]
     rest = [s for s in range(N + 2) if s not in lost]
     ref.near(d["states"][rest], s_want[rest], 1, 64, X)
     assert torch.equal(d["states"][lost].cpu(), x["states"][lost])
