@@ -22,6 +22,16 @@
 // the inverses of I + A's diagonal tiles.  An accumulator tile of M^T is an A operand
 // tile of M, so M goes to LDS as it stands (in the place of K and Q), in bf16 pieces.
 //
+// Bound by HBM for large batches: 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128,
+// bf16; 214 MB) take 44 us, 4.9 TB/s, where a large copy runs at 5.0.  By latency for small
+// ones: one tree of 13 nodes takes 6.3 us, of 64 nodes 9 us.  Of the 20,000 cycles of a lone
+// workgroup of 64 nodes, 5,000 pass until K and Q are in LDS, the tiles of A and P take 2,900,
+// D 2,000, K h and Q h 3,300, M 2,300, R 1,200 and the output 1,900.  Three workgroups
+// per compute unit hide most of that from each other: two (registers for K's and Q's rows at
+// once) took 52 us where three took 49, and persistent workgroups with the next tree's loads in
+// flight 75.  Tiles chosen by runtime conditions, each a branch of its own, took 54.6 us
+// against 52; U by forward substitution in every wave instead of M 101 against 60.5.
+//
 // Non-finite values.  Node j must not reach nodes that are no descendants of it,
 // though a product with a masked zero would turn its NaN or infinity into NaN there.
 // Products by rows keep to their rows; entries of A and right-hand sides that are
