@@ -23,8 +23,11 @@ from . import _lib
 from .api import _DT, _c, check_offsets
 
 
-# the current stream's handle, without a Stream object around it (1.8 us a call)
+# torch.cuda.current_stream(i).cuda_stream, current_device() and
+# torch.autograd.graph.increment_version without what they wrap around these (2.5 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_increment_version = torch._C._increment_version
 
 
 def _refuse_gradients():
@@ -48,6 +51,8 @@ def _rows(x, per16):
 
 
 def _check_states(states, name="states"):
+    if states.is_contiguous() and states.shape[0] and not states.data_ptr() % 16:
+        return
     n, H, K, V = states.shape
     slot, head, row, one = states.stride()
     if n < 1 or one != 1 or row != V or (head != K * V and H > 1) or states.data_ptr() % 16 or \
@@ -108,13 +113,17 @@ def _overlap(a, b):
     return a.device == b.device and a0 < b1 and b0 < a1
 
 
-def _launch(call, args, dev):
+def _launch(call, args, dev, written):
+    """`written`: what the kernels write in place.  Autograd is told, so that a backward that
+    has saved it raises an error instead of using the new values."""
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         call(args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
             call(args, _raw_stream(index))
+    if written:
+        _increment_version(written)
 
 
 def _on(x, dev):
@@ -210,7 +219,10 @@ def _run(call, q, k, v, g, beta, parents, accepted, states, scale, cu_seqlens, s
         beta.data_ptr(), None if cu is None else cu.data_ptr(), None if sl is None else sl.data_ptr(),
         None if pa is None else pa.data_ptr(), None if ac is None else ac.data_ptr(), states.data_ptr(),
         None if o is None else o.data_ptr())
-    _launch(call, args, dev)
+    written = [states] if parents is None or accepted is not None else []
+    if out is not None:
+        written.append(out)
+    _launch(call, args, dev, written)
     return o
 
 
@@ -328,5 +340,5 @@ def copy_states(states, dst, src, source=None):
         layers, layer, source_layer = states.shape[0], 4 * states.stride(0), 4 * source.stride(0)
     args = _lib.CopyArgs(n, n_dst, n_src, 4 * H * K * V, 4 * states.stride(-4), 4 * source.stride(-4), layers, layer,
                          source_layer, dst.data_ptr(), src.data_ptr(), states.data_ptr(), source.data_ptr())
-    _launch(_lib.copy_states, args, dev)
+    _launch(_lib.copy_states, args, dev, [states])
     return states

@@ -637,7 +637,7 @@ def test_the_tensors_device_is_used_whatever_the_current_one(monkeypatch):
     """A call on another device than the current one makes that device current for its launch."""
     from gated_delta_rule_85_amd import pool
     seen = []
-    monkeypatch.setattr(pool.torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(pool, "_current_device", lambda: 1)
     class Guard:
         def __init__(self, dev):
             seen.append(dev)
@@ -649,6 +649,47 @@ def test_the_tensors_device_is_used_whatever_the_current_one(monkeypatch):
     d = ref.cuda(ref.make(1, 1, 1, 1, 64, 64, F32))
     run_recurrent(d)
     assert seen == [d["q"].device]
+
+
+@pytest.mark.parametrize("op", ["recurrent", "accept", "copy"])
+def test_a_backward_that_saved_the_states_notices_that_they_changed(op):
+    d = ref.cuda(ref.make(2, 3, 1, 2, 64, 64, F32, seed=3, extra_slots=0))
+    d["slots"] = None
+    q = d["q"].clone().requires_grad_()
+    o, _ = gdr.chunk_gated_delta_rule(q, d["k"], d["v"], d["g"], d["beta"], initial_state=d["states"])
+    run_tree(dict(d, parents=torch.full((2, 3), -1, **I32)))  # reads them only
+    o.sum().backward(retain_graph=True)
+    if op == "recurrent":
+        run_recurrent(d)
+    elif op == "accept":
+        run_accept(dict(d, parents=torch.full((2, 3), -1, **I32), accepted=torch.tensor([0, 1], **I32)))
+    else:
+        gdr.copy_states(d["states"], torch.tensor([0], **I32), torch.tensor([-1], **I32))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+    with torch.inference_mode():
+        e = ref.cuda(ref.make(1, 1, 1, 2, 64, 64, F32))
+        run_recurrent(e, out=torch.empty_like(e["v"]))
+
+
+@pytest.mark.parametrize("n", [1, 5, 40, 300, 1100])
+def test_copies_of_odd_sizes_through_the_c_abi(n):
+    """Slots of any multiple of 16 bytes, unequal strides, bytes between the slots and layers left alone."""
+    import ctypes
+    gen = torch.Generator().manual_seed(n)
+    n_dst, n_src, layers, words = n + 2, n + 5, 3, 4 * 37
+    dst = torch.randint(0, 1 << 30, (layers, n_dst, words + 8), generator=gen, dtype=torch.int32)
+    src = torch.randint(0, 1 << 30, (layers, n_src, words + 4), generator=gen, dtype=torch.int32)
+    to = torch.randperm(n_dst, generator=gen)[:n].to(torch.int32)
+    frm = torch.randint(-1, n_src, (n,), generator=gen, dtype=torch.int32)
+    want = dst.clone()
+    for a, b in zip(to.tolist(), frm.tolist()):
+        want[:, a, :words] = src[:, b, :words] if b >= 0 else 0
+    d, s, t, f = dst.cuda(), src.cuda(), to.cuda(), frm.cuda()
+    a = _lib.CopyArgs(n, n_dst, n_src, 4 * words, 4 * (words + 8), 4 * (words + 4), layers, 4 * n_dst * (words + 8),
+                      4 * n_src * (words + 4), t.data_ptr(), f.data_ptr(), d.data_ptr(), s.data_ptr())
+    assert _lib.lib.gdr_copy_states(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(d.cpu(), want)
 
 
 def test_errors_of_the_library_name_their_entry_point():
