@@ -3,7 +3,8 @@ recurrent operators that serve from its states.
 
 The operator (FlashQLA's GDN chunked prefill) runs in libgdr.so, hand-written
 HIP kernels behind the C ABI of include/gdr.h; this package is a thin
-PyTorch-facing binding of it.
+PyTorch-facing binding of it (ctypes, and compiled for the calls of a decode
+step).
 """
 from .api import (SavedForBackward, chunk_bound, chunk_gated_delta_rule, chunk_gated_delta_rule_bwd,
                   chunk_gated_delta_rule_fwd, num_chunks)

@@ -169,27 +169,3 @@ def bwd(args, stream):
     rc = lib.gdr_bwd(ctypes.byref(args), _p(stream))
     if rc:
         raise GdrError("gdr_bwd", rc)
-
-
-def step(args, stream):
-    rc = lib.gdr_step(ctypes.byref(args), stream)
-    if rc:
-        raise GdrError("gdr_step", rc)
-
-
-def tree(args, stream):
-    rc = lib.gdr_tree(ctypes.byref(args), stream)
-    if rc:
-        raise GdrError("gdr_tree", rc)
-
-
-def tree_accept(args, stream):
-    rc = lib.gdr_tree_accept(ctypes.byref(args), stream)
-    if rc:
-        raise GdrError("gdr_tree_accept", rc)
-
-
-def copy_states(args, stream):
-    rc = lib.gdr_copy_states(ctypes.byref(args), stream)
-    if rc:
-        raise GdrError("gdr_copy_states", rc)

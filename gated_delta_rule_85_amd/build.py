@@ -1,18 +1,23 @@
-"""Build libgdr.so (the HIP kernels and the C ABI of include/gdr.h) for gfx950.
+"""Build libgdr.so (the HIP kernels and the C ABI of include/gdr.h) for gfx950, and
+_gdr_torch.so, the compiled part of the Python binding (host code only).
 
 Each .hip source is compiled with hipcc into an object in _build/, then
 linked into gated_delta_rule_85_amd/libgdr.so.  Packed-fp32 instruction
-selection is switched off for the device code.
+selection is switched off for the device code.  The binding is compiled with
+g++ against torch's headers and linked to libgdr.so.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libgdr.so")
+BINDING = os.path.join(PKG, "_gdr_torch.so")
 BUILD = os.path.join(ROOT, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -53,14 +58,33 @@ def _compile(src):
     return obj
 
 
+def _compile_binding():
+    """The binding's object (torch is found without importing it)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    obj = os.path.join(BUILD, "gdr_torch.o")
+    include = [os.path.join(ROOT, "include"), "/opt/rocm/include", os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__"] + ["-I" + i for i in include]
+                       + ["-c", os.path.join(CSRC, "gdr_torch.cpp"), "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for gdr_torch.cpp:\n%s" % r.stderr)
+    return obj, ["-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding, torch_libs = binding.result()
     tmp = OUT + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs,
                    check=True)
     os.replace(tmp, OUT)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.run(["g++", "-shared", "-o", tmp, binding, "-L" + PKG, "-lgdr", "-Wl,-rpath,$ORIGIN"] + torch_libs,
+                   check=True)
+    os.replace(tmp, BINDING)
     if verbose:
         print(OUT)
     return OUT

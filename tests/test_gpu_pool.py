@@ -633,24 +633,6 @@ def test_calls_on_two_streams():
         ref.near(d["states"], s_want, 2, 128, X)
 
 
-def test_the_tensors_device_is_used_whatever_the_current_one(monkeypatch):
-    """A call on another device than the current one makes that device current for its launch."""
-    from gated_delta_rule_85_amd import pool
-    seen = []
-    monkeypatch.setattr(pool, "_current_device", lambda: 1)
-    class Guard:
-        def __init__(self, dev):
-            seen.append(dev)
-        def __enter__(self):
-            pass
-        def __exit__(self, *a):
-            pass
-    monkeypatch.setattr(pool.torch.cuda, "device", Guard)
-    d = ref.cuda(ref.make(1, 1, 1, 1, 64, 64, F32))
-    run_recurrent(d)
-    assert seen == [d["q"].device]
-
-
 @pytest.mark.parametrize("op", ["recurrent", "accept", "copy"])
 def test_a_backward_that_saved_the_states_notices_that_they_changed(op):
     d = ref.cuda(ref.make(2, 3, 1, 2, 64, 64, F32, seed=3, extra_slots=0))
@@ -693,6 +675,12 @@ def test_copies_of_odd_sizes_through_the_c_abi(n):
 
 
 def test_errors_of_the_library_name_their_entry_point():
-    a = _lib.PoolArgs()
-    with pytest.raises(_lib.GdrError, match="gdr_step"):
-        _lib.step(a, 0)
+    x = ref.cuda(ref.make(1, 1, 1, 1, 96, 64, F32))
+    with pytest.raises(_lib.GdrError, match="gdr_step") as e:
+        run_recurrent(x)
+    assert e.value.code == _lib.ENOTSUP
+    x["parents"] = x["accepted"] = torch.full((1, 1), -1, **I32)
+    with pytest.raises(_lib.GdrError, match="gdr_tree "):
+        run_tree(x)
+    with pytest.raises(_lib.GdrError, match="gdr_tree_accept"):
+        run_accept(dict(x, accepted=x["accepted"][0]))

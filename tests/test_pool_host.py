@@ -63,6 +63,20 @@ def test_arguments_are_refused(op, name, change):
         call(op, x)
 
 
+@pytest.mark.parametrize("op", ["recurrent", "tree", "accept"])
+def test_what_is_no_tensor_is_a_type_error(op):
+    for name in ("k", "v", "g", "beta", "states"):
+        for value in (None, 1.0, [1]):
+            with pytest.raises(TypeError, match=name):
+                call(op, dict(tree_inputs(), **{name: value}))
+    with pytest.raises(TypeError, match="slots"):
+        call(op, dict(tree_inputs(), slots=[0, 1]))
+    with pytest.raises(TypeError, match="dst"):
+        gdr.copy_states(torch.zeros(2, 1, 64, 64), [0], torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        gdr.copy_states(torch.zeros(2, 1, 64, 64))
+
+
 @pytest.mark.parametrize("op", ["recurrent", "accept"])
 def test_a_slot_named_twice_on_the_host_is_refused(op):
     x = tree_inputs()
