@@ -83,7 +83,8 @@ template <typename In, int R> struct Rows {
 
 template <typename In, int R, bool OUT> struct Token {
     Rows<In, R> k, q;
-    float v, g, beta;
+    In v;
+    float g, beta;
 };
 
 template <typename In, typename Out, int K, bool ACCEPT>
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     auto fetch = [&](Token<In, R, !ACCEPT> &t, int64_t i) {
         t.k.load(kp + row_offset(p, j, i, p.k_batch, p.k_row));
         if constexpr (!ACCEPT) t.q.load(qp + row_offset(p, j, i, p.q_batch, p.q_row));
-        t.v = to_f32(vp[row_offset(p, j, i, p.v_batch, p.v_row)]);
+        t.v = vp[row_offset(p, j, i, p.v_batch, p.v_row)];
         t.g = p.g[i * p.Hv + hv];
         t.beta = p.beta[i * p.Hv + hv];
     };
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         }
         // full-precision exponential: its error would otherwise grow with every token
         const float eg = expf(t.g);
-        const float u = t.beta * (t.v - eg * sum_columns(kh));
+        const float u = t.beta * (to_f32(t.v) - eg * sum_columns(kh));
         const f32x4 us = gather_columns(u);
 #pragma unroll
         for (int r = 0; r < R; ++r) h[r] = eg * h[r] + t.k[r] * us;
@@ -159,20 +160,21 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     fetch(now, ACCEPT ? bos + __builtin_ctzll(path) : bos);
     // with the loads in flight: a skipped sequence's are not used
     if (slot_taken(p, j, slot)) return skip();
+    // the next token's loads are in flight during this one's work.  The last token fetches itself
+    // again: a condition would end the block of instructions, and the loads be waited for there
     if constexpr (ACCEPT) {
-        for (;;) {
+        for (bool more = true; more;) {
             const int64_t i = bos + __builtin_ctzll(path);
-            path &= path - 1;
-            if (path) fetch(next, bos + __builtin_ctzll(path));
+            more = (path & (path - 1)) != 0;
+            if (more) path &= path - 1;
+            fetch(next, bos + __builtin_ctzll(path));
             step(now, i);
-            if (!path) break;
             now = next;
         }
     } else {
-        for (int64_t i = bos;;) {
-            if (i + 1 < eos) fetch(next, i + 1);
+        for (int64_t i = bos; i < eos; ++i) {
+            fetch(next, min(i + 1, eos - 1));
             step(now, i);
-            if (++i >= eos) break;
             now = next;
         }
     }
