@@ -135,25 +135,31 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         t.g = p.g[i * p.Hv + hv];
         t.beta = p.beta[i * p.Hv + hv];
     };
+    // every rounding is written out (no contraction by the compiler), so that an acceptance
+    // and the recurrent form on the same tokens agree to the bit
     auto step = [&](const Token<In, R, !ACCEPT> &t, int64_t i) {
+#pragma clang fp contract(off)
         f32x4 kh = zero4(), qh = zero4();
         float qk = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            kh += t.k[r] * h[r];
-            if constexpr (!ACCEPT) {
-                qh += t.q[r] * h[r];
-                qk += t.q[r] * t.k[r];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                kh[c] = __builtin_fmaf(t.k[r], h[r][c], kh[c]);
+                if constexpr (!ACCEPT) qh[c] = __builtin_fmaf(t.q[r], h[r][c], qh[c]);
             }
+            if constexpr (!ACCEPT) qk = __builtin_fmaf(t.q[r], t.k[r], qk);
         }
         // full-precision exponential: its error would otherwise grow with every token
         const float eg = expf(t.g);
-        const float u = t.beta * (to_f32(t.v) - eg * sum_columns(kh));
+        const float u = t.beta * __builtin_fmaf(-eg, sum_columns(kh), to_f32(t.v));
         const f32x4 us = gather_columns(u);
 #pragma unroll
-        for (int r = 0; r < R; ++r) h[r] = eg * h[r] + t.k[r] * us;
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[r][c] = __builtin_fmaf(t.k[r], us[c], eg * h[r][c]);
         if constexpr (!ACCEPT) {
-            const float y = p.scale * (eg * sum_columns(qh) + sum_all(qk) * u);
+            const float y = p.scale * __builtin_fmaf(sum_all(qk), u, eg * sum_columns(qh));
             if (writes) o[i * p.Hv * V] = (Out)y;
         }
     };
@@ -187,10 +193,15 @@ hipError_t launch(int K, int V, const PoolParams &p, hipStream_t s) {
     // a head's waves in one workgroup share its k and q rows in the L1
     const int block = 64 * (V / 32);
     const dim3 grid((uint32_t)p.n_seq * p.Hv);
+    // LDS that no kernel uses holds a compute unit to eight waves of 128 rows, the 128 KB in
+    // flight at which HBM is fastest: 256 sequences of 32 heads take 185 us, 192 with the twelve
+    // that the registers leave room for.  With 64 rows sixteen waves are (11.5 us for 4096
+    // waves, 14.5 for eight at a time), and an acceptance does not mind.
+    const uint32_t lds = ACCEPT || K == 64 ? 0 : V == 128 ? 54 << 10 : 33 << 10;
     if (K == 128)
-        launch_k(gdr_step_kernel<In, Out, 128, ACCEPT>, grid, dim3(block), 0, s, p, V);
+        launch_k(gdr_step_kernel<In, Out, 128, ACCEPT>, grid, dim3(block), lds, s, p, V);
     else
-        launch_k(gdr_step_kernel<In, Out, 64, ACCEPT>, grid, dim3(block), 0, s, p, V);
+        launch_k(gdr_step_kernel<In, Out, 64, ACCEPT>, grid, dim3(block), lds, s, p, V);
     return hipGetLastError();
 }
 
