@@ -348,7 +348,7 @@ int gdr_bwd(const gdr_bwd_args *args, hipStream_t stream);
 
 /* The recurrent form on `stream`: every sequence's tokens are taken in turn into
    its state, in place, and o gets their outputs.  For one token or a few per
-   sequence (decode); the chunked gdr_fwd is faster for long ones.  Where two
+   sequence (decode); the chunked gdr_fwd is faster from about 16 on.  Where two
    sequences with tokens name one slot, the first has it and the others are
    skipped, as if they had none.  Needs no workspace and may be captured. */
 int gdr_step(const gdr_pool_args *args, hipStream_t stream);
@@ -358,7 +358,8 @@ int gdr_step(const gdr_pool_args *args, hipStream_t stream);
    states are left as they are (sequences may share a slot).  A sequence is one tree
    of at most GDR_TREE_MAX nodes, parents before children (T above that without
    cu_seqlens is GDR_EINVAL; a longer packed sequence gets rows of NaN).  A node
-   influences its descendants only, with non-finite values too.  Needs no workspace
+   influences its descendants only, with non-finite values too (an infinity may come
+   out as NaN).  Needs no workspace
    and may be captured. */
 int gdr_tree(const gdr_pool_args *args, hipStream_t stream);
 
