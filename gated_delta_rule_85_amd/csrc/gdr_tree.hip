@@ -21,6 +21,8 @@
 // solves M's rows r from the right: M^T_c = D_c^T (P^T_c + sum over k > c of (-A_kc)^T M^T_k), D
 // the inverses of I + A's diagonal tiles.  An accumulator tile of M^T is an A operand
 // tile of M, so M goes to LDS as it stands (in the place of K and Q), in bf16 pieces.
+// fp32 rows of K and Q are split into pieces on their way to LDS: 8 trees of 64 nodes (fp32,
+// K = V = 128) take 17.2 us, 22.4 with fp32 matrix instructions, 10.8 with bf16 rows.
 //
 // Bound by HBM for large batches: 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128,
 // bf16; 214 MB) take 44 us, 4.9 TB/s, where a large copy runs at 5.0.  By latency for small
@@ -46,9 +48,10 @@ namespace {
 constexpr int LDT = 20;  // floats per row of a 16 x 16 tile in LDS (16 and padding: conflict-free rows)
 
 template <typename In, int K, int NT, int PIECES> struct TreeLds {
-    static constexpr int ROWB = K * sizeof(In) + 16;  // a row of K or Q with padding
+    // K and Q: a plane of bf16 rows (with padding) per piece, one where they are bf16
+    static constexpr int ROWB = 2 * K + 16, PLANE = 16 * NT * ROWB, PLANES = sizeof(In) == 2 ? 1 : PIECES;
     static constexpr int TILES = NT * (NT + 1) / 2, NP = (NT + 1) / 2;
-    static constexpr int k = 0, q = k + 16 * NT * ROWB, a = q + 16 * NT * ROWB, G = a + TILES * 16 * LDT * 4,
+    static constexpr int k = 0, q = k + PLANES * PLANE, a = q + PLANES * PLANE, G = a + TILES * 16 * LDT * 4,
                          mask = G + 16 * NT * 8, eg = mask + 16 * NT * 8, beta = eg + 16 * NT * 4,
                          bad = beta + 16 * NT * 4, bytes = bad + 16;
     // M, in the place of K and Q: per row tile r, pairs of column tiles, piece and lane, 16 bytes
@@ -90,44 +93,37 @@ template <int PIECES> __device__ __forceinline__ void pieces8(f32x4 x, f32x4 y, 
     for (int s = 0; s < PIECES; ++s) z[s] = __builtin_bit_cast(bf16x8, (u32x4{a[0][s], a[1][s], a[2][s], a[3][s]}));
 }
 
-// Products of rows of K or Q (8 consecutive values a lane) with rows of K or Q, and with
-// state columns in pieces, as a sequence of STEPS matrix instructions that is taken step by
-// step over several tiles, so that each waits for no other.
-template <typename In, int PIECES> struct Operands;
-template <int PIECES> struct Operands<bf16, PIECES> {
-    typedef bf16x8 Row;
-    typedef bf16x8 State[PIECES];
-    static constexpr int ROW_STEPS = 1, STATE_STEPS = PIECES;
-    static __device__ __forceinline__ void load(Row &r, const char *p) { r = *reinterpret_cast<const bf16x8 *>(p); }
-    static __device__ __forceinline__ void set(State &s, f32x4 x, f32x4 y) { pieces8<PIECES>(x, y, s); }
-    static __device__ __forceinline__ f32x4 row_step(int, const Row &a, const Row &b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-    }
-    static __device__ __forceinline__ f32x4 state_step(int s, const Row &a, const State &b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[PIECES - 1 - s], c, 0, 0, 0);  // small ones first
+// Eight consecutive values of a row of K or Q (P = 1 piece, or PIECES of fp32 values), or of
+// a state column (PIECES), and their product as a sequence of matrix instructions that is
+// taken step by step over several tiles, so that none waits for another.
+template <int P> struct Eight {
+    bf16x8 x[P];
+    // a row in planes `plane` bytes apart
+    __device__ __forceinline__ void load(const char *p, int plane) {
+#pragma unroll
+        for (int s = 0; s < P; ++s) x[s] = *reinterpret_cast<const bf16x8 *>(p + s * plane);
     }
 };
-template <int PIECES> struct Operands<float, PIECES> {
-    struct Row {
-        f32x4 x[2];
-    };
-    typedef Row State;
-    static constexpr int ROW_STEPS = 8, STATE_STEPS = 8;
-    static __device__ __forceinline__ void load(Row &r, const char *p) {
-        r.x[0] = *reinterpret_cast<const f32x4 *>(p);
-        r.x[1] = *reinterpret_cast<const f32x4 *>(p + 16);
-    }
-    static __device__ __forceinline__ void set(State &s, f32x4 x, f32x4 y) {
-        s.x[0] = x;
-        s.x[1] = y;
-    }
-    static __device__ __forceinline__ f32x4 row_step(int s, const Row &a, const Row &b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[s / 4][s % 4], b.x[s / 4][s % 4], c, 0, 0, 0);
-    }
-    static __device__ __forceinline__ f32x4 state_step(int s, const Row &a, const State &b, f32x4 c) {
-        return row_step(s, a, b, c);
-    }
-};
+// steps of a product of A and B pieces: those that `keep` pieces of accuracy need
+constexpr int steps(int A, int B, int keep) {
+    int n = 0;
+    for (int s = 0; s < A; ++s)
+        for (int z = 0; z < B; ++z) n += s + z < keep;
+    return n;
+}
+// the s-th one, small ones first
+template <int KEEP, int A, int B>
+__device__ __forceinline__ f32x4 product_step(int step, const Eight<A> &a, const Eight<B> &b, f32x4 c) {
+    int n = 0;
+#pragma unroll
+    for (int sum = KEEP - 1; sum >= 0; --sum)
+#pragma unroll
+        for (int s = 0; s < A; ++s) {
+            if (sum - s < 0 || sum - s >= B) continue;
+            if (n++ == step) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x[s], b.x[sum - s], c, 0, 0, 0);
+        }
+    return c;
+}
 
 typedef float pair __attribute__((ext_vector_type(2)));
 
@@ -151,7 +147,7 @@ template <typename In, typename Out, int K, int V, int NT>
 __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int hv, int64_t bos, int n) {
     constexpr int NTHREADS = 2 * V, NW = V / 32, PIECES = sizeof(Out) == 4 ? 3 : 2;
     using L = TreeLds<In, K, NT, PIECES>;
-    using X = Operands<In, PIECES>;
+    typedef Eight<L::PLANES> Row;
     constexpr int NP = L::NP;
     float *At = reinterpret_cast<float *>(smem + L::a);  // -A, later with D in the diagonal tiles
     double *G = reinterpret_cast<double *>(smem + L::G);
@@ -209,8 +205,22 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
 #pragma unroll
     for (int t = 0; t < TURNS; ++t)
         if (16 * NT % ROWS == 0 || t * ROWS + kq_row < 16 * NT) {
-            *reinterpret_cast<u32x4 *>(smem + L::k + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = kx[t];
-            *reinterpret_cast<u32x4 *>(smem + L::q + (t * ROWS + kq_row) * L::ROWB + 16 * kq_chunk) = qx[t];
+            char *to = smem + L::k + (t * ROWS + kq_row) * L::ROWB + 2 * PER * kq_chunk;
+            if constexpr (sizeof(In) == 2) {
+                *reinterpret_cast<u32x4 *>(to) = kx[t];
+                *reinterpret_cast<u32x4 *>(to + L::q) = qx[t];
+            } else {
+#pragma unroll
+                for (int kq = 0; kq < 2; ++kq) {
+                    const f32x4 x = __builtin_bit_cast(f32x4, kq ? qx[t] : kx[t]);
+                    uint32_t lo[PIECES], hi[PIECES];
+                    pieces2<PIECES>(x[0], x[1], lo);
+                    pieces2<PIECES>(x[2], x[3], hi);
+#pragma unroll
+                    for (int s = 0; s < PIECES; ++s)
+                        *reinterpret_cast<u32x2 *>(to + kq * L::q + s * L::PLANE) = u32x2{lo[s], hi[s]};
+                }
+            }
         }
     if (w == 0) {
         // path sums and ancestors by pointer doubling: after a round a lane has its sum
@@ -241,7 +251,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     }
     lds_barrier();
 
-    auto row = [&](int base, int i, int kb) { return smem + base + i * L::ROWB + (32 * kb + 8 * g) * (int)sizeof(In); };
+    auto load = [&](Row &x, int base, int i, int kb) { x.load(smem + base + i * L::ROWB + (32 * kb + 8 * g) * 2, L::PLANE); };
     // Rows r of A and of P, transposed: lane (c, g) has node 16 r + c against nodes
     // 16 ct + 4 g + i, whose decay D both share.  Tiles past the diagonal come out zero.
     constexpr int MINE = (NT + NW - 1) / NW;
@@ -255,17 +265,17 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         for (int ct = 0; ct < NT; ++ct) kk[ct] = mt[y][ct] = zero4();
 #pragma unroll
         for (int kb = 0; kb < K / 32; ++kb) {
-            typename X::Row kr, qr, kc[NT];
-            X::load(kr, row(L::k, 16 * r + c, kb));
-            X::load(qr, row(L::q, 16 * r + c, kb));
+            Row kr, qr, kc[NT];
+            load(kr, L::k, 16 * r + c, kb);
+            load(qr, L::q, 16 * r + c, kb);
 #pragma unroll
-            for (int ct = 0; ct < NT; ++ct) X::load(kc[ct], row(L::k, 16 * ct + c, kb));
+            for (int ct = 0; ct < NT; ++ct) load(kc[ct], L::k, 16 * ct + c, kb);
 #pragma unroll
-            for (int s = 0; s < X::ROW_STEPS; ++s)
+            for (int s = 0; s < steps(L::PLANES, L::PLANES, L::PLANES); ++s)
 #pragma unroll
                 for (int ct = 0; ct < NT; ++ct) {
-                    kk[ct] = X::row_step(s, kc[ct], kr, kk[ct]);
-                    mt[y][ct] = X::row_step(s, kc[ct], qr, mt[y][ct]);
+                    kk[ct] = product_step<L::PLANES>(s, kc[ct], kr, kk[ct]);
+                    mt[y][ct] = product_step<L::PLANES>(s, kc[ct], qr, mt[y][ct]);
                 }
             if constexpr (NT > 2) __builtin_amdgcn_sched_barrier(0);
         }
@@ -327,26 +337,26 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         for (int t = 0; t < 2; ++t) kh[rt][t] = qh[rt][t] = zero4();
 #pragma unroll
     for (int kb = 0; kb < K / 32; ++kb) {
-        typename X::State s[2];
+        Eight<PIECES> s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            X::set(s[t], f32x4{h[kb][0][t], h[kb][1][t], h[kb][2][t], h[kb][3][t]},
-                   f32x4{h[kb][4][t], h[kb][5][t], h[kb][6][t], h[kb][7][t]});
+            pieces8<PIECES>(f32x4{h[kb][0][t], h[kb][1][t], h[kb][2][t], h[kb][3][t]},
+                            f32x4{h[kb][4][t], h[kb][5][t], h[kb][6][t], h[kb][7][t]}, s[t].x);
         // K's rows, then Q's: the rows of both at once would not leave the registers for a
         // third wave per SIMD
 #pragma unroll
         for (int kq = 0; kq < 2; ++kq) {
-            typename X::Row x[NT];
+            Row x[NT];
 #pragma unroll
-            for (int rt = 0; rt < NT; ++rt) X::load(x[rt], row(kq ? L::q : L::k, 16 * rt + c, kb));
+            for (int rt = 0; rt < NT; ++rt) load(x[rt], kq ? L::q : L::k, 16 * rt + c, kb);
 #pragma unroll
-            for (int step = 0; step < X::STATE_STEPS; ++step)
+            for (int step = 0; step < steps(L::PLANES, PIECES, PIECES); ++step)
 #pragma unroll
                 for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         f32x4 &y = kq ? qh[rt][t] : kh[rt][t];
-                        y = X::state_step(step, x[rt], s[t], y);
+                        y = product_step<PIECES>(step, x[rt], s[t], y);
                     }
             if constexpr (NT > 2) __builtin_amdgcn_sched_barrier(0);
         }
