@@ -105,6 +105,79 @@ def test_recurrent_reads_slices_of_a_projection(T, dtype):
         ref.near(e["states"], s_want, T, 64, X, "states %s" % copied)
 
 
+@pytest.mark.parametrize("n", [5, 16, 37, 64])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("packed", [False, True])
+def test_trees_read_slices_of_a_projection(n, dtype, packed):
+    """Rows a projection's width apart, with NaN between the parts and behind the trees."""
+    Hq, Hv, K, V = 2, 4, 64, 128
+    x = ref.make(0, 0, Hq, Hv, K, V, dtype, [n, 3], seed=n) if packed else ref.make(2, n, Hq, Hv, K, V, dtype, seed=n)
+    gen = torch.Generator().manual_seed(n)
+    lens = [n, 3] if packed else [n, n]
+    x["parents"] = torch.tensor(sum((shape_of("random", m, gen) for m in lens), []), **I32).view(x["k"].shape[:2])
+    x["accepted"] = torch.tensor([n - 1, 2], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    s_want, X2 = ref.accept(x, x["parents"], x["accepted"])
+    d = ref.cuda(x)
+    B, T = x["k"].shape[:2]
+    wide = torch.full((B, T + 3, 3 * 128 + 512 + 40), float("nan"), dtype=dtype, device="cuda")
+    wide[:, :T, :128], wide[:, :T, 136:264], wide[:, :T, 272:784] = (d[m].flatten(2) for m in ("q", "k", "v"))
+    d["q"], d["k"] = wide[:, :T, :128].view(B, T, Hq, K), wide[:, :T, 136:264].view(B, T, Hq, K)
+    d["v"] = wide[:, :T, 272:784].view(B, T, Hv, V)
+    assert not d["k"].is_contiguous()
+    ref.near(run_tree(d), o_want, n, K, X)
+    run_accept(d)
+    ref.near(d["states"], s_want, n, K, X2)
+
+
+def test_expanded_inputs_are_read_in_place():
+    """One row for every token, and for every sequence: strides of zero."""
+    x = ref.make(3, 21, 1, 2, 128, 64, BF, seed=15)
+    for name in ("q", "k", "v"):
+        x[name] = x[name][:1, :1].expand_as(x[name])
+    x["parents"], x["accepted"] = torch.tensor([list(range(-1, 20))] * 3, **I32), torch.tensor([20] * 3, **I32)
+    o_want, s_want, X = ref.recurrent(x)
+    d = ref.cuda(x)
+    for name in ("q", "k", "v"):
+        d[name] = d[name][:1, :1].contiguous().expand_as(d[name])
+    ref.near(run_tree(d), o_want, 21, 128, X)
+    e = dict(d, states=d["states"].clone())
+    run_accept(e)
+    ref.near(run_recurrent(d), o_want, 21, 128, X)
+    ref.near(d["states"], s_want, 21, 128, X)
+    assert torch.equal(d["states"], e["states"])
+
+
+def test_calls_from_two_threads():
+    """The binding releases the interpreter's lock: two threads, a stream and a pool each."""
+    import threading
+    xs = [ref.make(3, 4, 2, 4, 64, 64, BF, seed=s) for s in (31, 32)]
+    ds, failed = [ref.cuda(x) for x in xs], []
+    torch.cuda.synchronize()
+
+    def work(d):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    state = d["states"].clone()
+                    d["o"] = run_recurrent(dict(d, states=state))
+                    d["after"] = state
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in ds]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join(60)
+    assert not failed
+    for x, d in zip(xs, ds):
+        o_want, s_want, X = ref.recurrent(x)
+        ref.near(d["o"], o_want, 4, 64, X)
+        ref.near(d["after"], s_want, 4, 64, X)
+
+
 def test_recurrent_on_a_pool_with_other_things_between_its_slots():
     x = ref.make(3, 1, 2, 4, 64, 64, BF, seed=7)
     o_want, s_want, X = ref.recurrent(x)
