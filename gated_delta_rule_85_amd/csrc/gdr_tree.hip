@@ -22,17 +22,17 @@
 // the inverses of I + A's diagonal tiles.  An accumulator tile of M^T is an A operand
 // tile of M, so M goes to LDS as it stands (in the place of K and Q), in bf16 pieces.
 // fp32 rows of K and Q are split into pieces on their way to LDS: 8 trees of 64 nodes (fp32,
-// K = V = 128) take 17.2 us, 22.4 with fp32 matrix instructions, 10.8 with bf16 rows.
+// K = V = 128) take 17.0 us, 22.4 with fp32 matrix instructions, 13.0 with bf16 rows.
 //
-// Bound by HBM for large batches: 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128,
-// bf16; 214 MB) take 44 us, 4.9 TB/s, where a large copy runs at 5.0.  By latency for small
-// ones: one tree of 13 nodes takes 6.3 us, of 64 nodes 9 us.  Of the 20,000 cycles of a lone
+// 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128, bf16; 214 MB) take 52 us, 4.1 TB/s,
+// where a large copy runs at 5.0: three workgroups per compute unit hide most of their phases
+// from each other, but not all (with two per unit 54 us).  Small batches are bound by the chain
+// of phases: one tree of 13 nodes takes 6.2 us, of 64 nodes 11.7.  Of the 20,000 cycles of a lone
 // workgroup of 64 nodes, 5,000 pass until K and Q are in LDS, the tiles of A and P take 2,900,
-// D 2,000, K h and Q h 3,300, M 2,300, R 1,200 and the output 1,900.  Three workgroups
-// per compute unit hide most of that from each other: two (registers for K's and Q's rows at
-// once) took 52 us where three took 49, and persistent workgroups with the next tree's loads in
-// flight 75.  Tiles chosen by runtime conditions, each a branch of its own, took 54.6 us
-// against 52; U by forward substitution in every wave instead of M 101 against 60.5.
+// D 2,000, K h and Q h 3,300, M 2,300, R 1,200 and the output 1,900 (these with two pieces).
+// Also with two pieces: persistent workgroups with the next tree's loads in flight took 75 us
+// where this form took 49, tiles chosen by runtime conditions, each a branch of its own, 54.6
+// against 52, U by forward substitution in every wave instead of M 101 against 60.5.
 //
 // Non-finite values.  Node j must not reach nodes that are no descendants of it,
 // though a product with a masked zero would turn its NaN or infinity into NaN there.
@@ -46,8 +46,12 @@ namespace gdr {
 namespace {
 
 constexpr int LDT = 20;  // floats per row of a 16 x 16 tile in LDS (16 and padding: conflict-free rows)
+// bf16 pieces of an fp32 value: 3 keep its 24 bits, with a bf16 output too.  There 2 (16 bits)
+// would take 44 us for the 64 packed trees above and 5.75 for one tree of 13 nodes instead of 52
+// and 6.2, but lose what is small by cancellation, which fp32 products keep
+constexpr int PIECES = 3;
 
-template <typename In, int K, int NT, int PIECES> struct TreeLds {
+template <typename In, int K, int NT> struct TreeLds {
     // K and Q: a plane of bf16 rows (with padding) per piece, one where they are bf16
     static constexpr int ROWB = 2 * K + 16, PLANE = 16 * NT * ROWB, PLANES = sizeof(In) == 2 ? 1 : PIECES;
     static constexpr int TILES = NT * (NT + 1) / 2, NP = (NT + 1) / 2;
@@ -71,8 +75,8 @@ __device__ __forceinline__ f32x4 tile_t_mul(const float *tile, f32x4 b, f32x4 c)
     return c;
 }
 
-// x as a sum of bf16 values: 3 keep 24 bits (an fp32 output), 2 keep 16 (a bf16 output has 8)
-template <int PIECES> __device__ __forceinline__ void pieces2(float a, float b, uint32_t *y) {
+// two values as sums of bf16 ones
+__device__ __forceinline__ void pieces2(float a, float b, uint32_t *y) {
 #pragma unroll
     for (int s = 0; s < PIECES; ++s) {
         y[s] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
@@ -83,12 +87,12 @@ template <int PIECES> __device__ __forceinline__ void pieces2(float a, float b, 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // eight values, an operand's, in pieces
-template <int PIECES> __device__ __forceinline__ void pieces8(f32x4 x, f32x4 y, bf16x8 *z) {
+__device__ __forceinline__ void pieces8(f32x4 x, f32x4 y, bf16x8 *z) {
     uint32_t a[4][PIECES];
-    pieces2<PIECES>(x[0], x[1], a[0]);
-    pieces2<PIECES>(x[2], x[3], a[1]);
-    pieces2<PIECES>(y[0], y[1], a[2]);
-    pieces2<PIECES>(y[2], y[3], a[3]);
+    pieces2(x[0], x[1], a[0]);
+    pieces2(x[2], x[3], a[1]);
+    pieces2(y[0], y[1], a[2]);
+    pieces2(y[2], y[3], a[3]);
 #pragma unroll
     for (int s = 0; s < PIECES; ++s) z[s] = __builtin_bit_cast(bf16x8, (u32x4{a[0][s], a[1][s], a[2][s], a[3][s]}));
 }
@@ -145,8 +149,8 @@ __device__ __forceinline__ void store2(bf16, Rsrc r, int at, pair x) {
 // One tree of n nodes, up to 16 NT, and one v head; every wave of the workgroup calls it.
 template <typename In, typename Out, int K, int V, int NT>
 __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int hv, int64_t bos, int n) {
-    constexpr int NTHREADS = 2 * V, NW = V / 32, PIECES = sizeof(Out) == 4 ? 3 : 2;
-    using L = TreeLds<In, K, NT, PIECES>;
+    constexpr int NTHREADS = 2 * V, NW = V / 32;
+    using L = TreeLds<In, K, NT>;
     typedef Eight<L::PLANES> Row;
     constexpr int NP = L::NP;
     float *At = reinterpret_cast<float *>(smem + L::a);  // -A, later with D in the diagonal tiles
@@ -214,8 +218,8 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                 for (int kq = 0; kq < 2; ++kq) {
                     const f32x4 x = __builtin_bit_cast(f32x4, kq ? qx[t] : kx[t]);
                     uint32_t lo[PIECES], hi[PIECES];
-                    pieces2<PIECES>(x[0], x[1], lo);
-                    pieces2<PIECES>(x[2], x[3], hi);
+                    pieces2(x[0], x[1], lo);
+                    pieces2(x[2], x[3], hi);
 #pragma unroll
                     for (int s = 0; s < PIECES; ++s)
                         *reinterpret_cast<u32x2 *>(to + kq * L::q + s * L::PLANE) = u32x2{lo[s], hi[s]};
@@ -340,7 +344,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         Eight<PIECES> s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            pieces8<PIECES>(f32x4{h[kb][0][t], h[kb][1][t], h[kb][2][t], h[kb][3][t]},
+            pieces8(f32x4{h[kb][0][t], h[kb][1][t], h[kb][2][t], h[kb][3][t]},
                             f32x4{h[kb][4][t], h[kb][5][t], h[kb][6][t], h[kb][7][t]}, s[t].x);
         // K's rows, then Q's: the rows of both at once would not leave the registers for a
         // third wave per SIMD
@@ -394,7 +398,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
 #pragma unroll
         for (int cp = 0; cp < NP; ++cp) {
             bf16x8 m[PIECES];
-            pieces8<PIECES>(mt[y][2 * cp], 2 * cp + 1 < NT ? mt[y][2 * cp + 1 < NT ? 2 * cp + 1 : 0] : zero4(), m);
+            pieces8(mt[y][2 * cp], 2 * cp + 1 < NT ? mt[y][2 * cp + 1 < NT ? 2 * cp + 1 : 0] : zero4(), m);
             if (2 * cp <= r)
 #pragma unroll
                 for (int s = 0; s < PIECES; ++s)
@@ -432,7 +436,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     for (int cp = 0; cp < NP; ++cp)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            pieces8<PIECES>(kh[2 * cp][t], 2 * cp + 1 < NT ? kh[2 * cp + 1 < NT ? 2 * cp + 1 : 0][t] : zero4(), rs[cp][t]);
+            pieces8(kh[2 * cp][t], 2 * cp + 1 < NT ? kh[2 * cp + 1 < NT ? 2 * cp + 1 : 0][t] : zero4(), rs[cp][t]);
     lds_barrier();
     const uint64_t rows_lost = bad[0] | (uint64_t)bad[1] << 32;
     const bool poisoned = __ballot((lost[0] | lost[1] | rows_lost) != 0) != 0;
@@ -515,7 +519,7 @@ __global__ __launch_bounds__(2 * V, (waves_per_simd<In, V, NT>())) void gdr_tree
 }
 
 template <typename In, typename Out, int K, int V, int NT> hipError_t launch(const PoolParams &p, hipStream_t s) {
-    constexpr int bytes = TreeLds<In, K, NT, sizeof(Out) == 4 ? 3 : 2>::bytes;
+    constexpr int bytes = TreeLds<In, K, NT>::bytes;
     static const hipError_t attr =
         hipFuncSetAttribute(reinterpret_cast<const void *>(&gdr_tree_kernel<In, Out, K, V, NT>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);

@@ -757,3 +757,48 @@ def test_errors_of_the_library_name_their_entry_point():
         run_tree(x)
     with pytest.raises(_lib.GdrError, match="gdr_tree_accept"):
         run_accept(dict(x, accepted=x["accepted"][0]))
+
+
+# A small difference of two values near 1, in each of a tree's products: every product and
+# partial sum below is exact in fp32, so the result is the difference to the bit, which two bf16
+# pieces of either operand (1, and 8 bits from 2^-10 on) would lose
+BASE, TINY = 1 + 2.0 ** -10, 3 * 2.0 ** -20
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [2, 20, 64])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+def test_tree_products_keep_what_is_small_by_cancellation(dtype, out, n, K, V):
+    say("cancellation", dtype, out, n, K, V)
+    x = dict(q=torch.zeros(1, n, 1, K, dtype=dtype), k=torch.zeros(1, n, 1, K, dtype=dtype),
+             v=torch.zeros(1, n, 1, V, dtype=dtype), g=torch.zeros(1, n, 1), beta=torch.zeros(1, n, 1),
+             states=torch.zeros(1, 1, K, V), slots=torch.zeros(1, **I32), cu=None)
+    x["parents"] = torch.tensor([list(range(-1, n - 1))], **I32)
+
+    def last(**change):
+        return run_tree(ref.cuda(dict(x, **change)), scale=1.0, output_dtype=out)[0, -1, 0].float().cpu()
+
+    half = x["q"].clone()
+    half[0, -1, 0, :2] = torch.tensor([0.5, -0.5])
+    states = x["states"].clone()
+    states[0, 0, 0], states[0, 0, 1] = BASE + TINY, BASE
+    # o = q h
+    assert bool((last(q=half, states=states) == TINY / 2).all())
+    # o = q h + (q . k) u, u = -k h
+    beta = x["beta"].clone()
+    beta[0, -1] = 1
+    assert bool((last(q=half, k=half, states=states, beta=beta) == TINY / 4).all())
+    if dtype is F32:
+        q, one = x["q"].clone(), torch.ones_like(states)
+        q[0, -1, 0, :2] = torch.tensor([BASE + TINY, -BASE])
+        assert bool((last(q=q, states=one) == TINY).all())
+        # o = (q . k0) u0 + (q . k1) u1 of the first two nodes, in q's values and in v's (n = 2: the
+        # last node is the second, whose own key is zero elsewhere)
+        k, v, beta = x["k"].clone(), x["v"].clone(), x["beta"].clone()
+        k[0, 0, 0, 0] = k[0, 1, 0, 1] = 1
+        beta[0, :2] = 1
+        v[0, :2] = 1
+        assert bool((last(q=q, k=k, v=v, beta=beta) == TINY).all())
+        v[0, 0], v[0, 1] = BASE + TINY, BASE
+        assert bool((last(q=half, k=k, v=v, beta=beta) == TINY / 2).all())
