@@ -24,10 +24,10 @@
 // fp32 rows of K and Q are split into pieces on their way to LDS: 8 trees of 64 nodes (fp32,
 // K = V = 128) take 17.0 us, 22.4 with fp32 matrix instructions, 13.0 with bf16 rows.
 //
-// 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128, bf16; 214 MB) take 52 us, 4.1 TB/s,
+// 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128, bf16; 214 MB) take 54.5 us, 3.9 TB/s,
 // where a large copy runs at 5.0: three workgroups per compute unit hide most of their phases
-// from each other, but not all (with two per unit 54 us).  Small batches are bound by the chain
-// of phases: one tree of 13 nodes takes 6.2 us, of 64 nodes 11.7.  Of the 20,000 cycles of a lone
+// from each other, but not all (two per unit take 2 us more).  Small batches are bound by the chain
+// of phases: one tree of 13 nodes takes 6.3 us, of 64 nodes 11.7.  Of the 20,000 cycles of a lone
 // workgroup of 64 nodes, 5,000 pass until K and Q are in LDS, the tiles of A and P take 2,900,
 // D 2,000, K h and Q h 3,300, M 2,300, R 1,200 and the output 1,900 (these with two pieces).
 // Also with two pieces: persistent workgroups with the next tree's loads in flight took 75 us
@@ -36,9 +36,10 @@
 //
 // Non-finite values.  Node j must not reach nodes that are no descendants of it,
 // though a product with a masked zero would turn its NaN or infinity into NaN there.
-// Products by rows keep to their rows; entries of A and right-hand sides that are
-// not finite are replaced by zero and remembered (by node, or by node and column),
-// and the rows of those nodes and of their descendants are written as NaN.
+// Products by rows keep to their rows; entries of A and of D (products of A's entries, which
+// may overflow where these are finite) and right-hand sides that are not finite are replaced
+// by zero and remembered (by node, or by node and column), and the rows of those nodes and of
+// their descendants are written as NaN.
 #include "gdr_lds.hpp"
 #include "gdr_pool.hpp"
 
@@ -47,8 +48,8 @@ namespace {
 
 constexpr int LDT = 20;  // floats per row of a 16 x 16 tile in LDS (16 and padding: conflict-free rows)
 // bf16 pieces of an fp32 value: 3 keep its 24 bits, with a bf16 output too.  There 2 (16 bits)
-// would take 44 us for the 64 packed trees above and 5.75 for one tree of 13 nodes instead of 52
-// and 6.2, but lose what is small by cancellation, which fp32 products keep
+// would take 8 us less for the 64 packed trees above and 0.4 less for one tree of 13 nodes,
+// but lose what is small by cancellation, which fp32 products keep
 constexpr int PIECES = 3;
 
 template <typename In, int K, int NT> struct TreeLds {
@@ -319,6 +320,12 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         if (r >= NT) break;
         float *tile = At + tile_at(r, r);
         float x[16];
+        // kept finite (med3 makes a NaN the least of the others), so that an entry past fp32's
+        // range, found below by its size, meets a zero of A as zero.  (The substitution once
+        // more in a branch of its own, without the zeros, made the registers spill: the 64 packed
+        // trees took 84 us.)
+        constexpr float MOST = __FLT_MAX__;
+        float most = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
 #pragma unroll
@@ -328,6 +335,18 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
             for (int m = 0; m <= (i - 1) / 4; ++m) a[m] = *reinterpret_cast<const f32x4 *>(tile + i * LDT + 4 * m);
 #pragma unroll
             for (int m = 0; m < i; ++m) x[i] += a[m / 4][m % 4] * x[m];
+            x[i] = __builtin_amdgcn_fmed3f(x[i], -MOST, MOST);
+            most = fmaxf(most, fabsf(x[i]));
+        }
+        if (__ballot(most >= MOST)) {
+            uint32_t over = 0;
+#pragma unroll
+            for (int i = 1; i < 16; ++i)
+                if (fabsf(x[i]) >= MOST) {
+                    over |= 1u << i;
+                    x[i] = 0.f;
+                }
+            if (over) atomicOr(&bad[r >> 1], over << 16 * (r & 1));
         }
         if (g == 0)
 #pragma unroll

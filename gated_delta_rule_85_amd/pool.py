@@ -64,9 +64,10 @@ def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seql
     with ``cu_seqlens``.  ``parents`` int32 [B,T] holds the place of a node's parent
     among its tree's nodes, which come after their parents, or -1 for a child of the
     cached state; an entry that is no earlier node counts as -1.  A node influences
-    its own row and its descendants', whatever its values (an infinity among them may
-    come out as NaN).  Several trees may name one
-    slot; a tree whose slot is negative gets rows of zeros, and a packed tree of more
+    its own row and its descendants' only, whatever its values; where a value on a node's
+    path is not finite, or a product of values on it (of keys, or of the e^g between an
+    ancestor and the node: gates that add up to more than 88) leaves fp32's range, the
+    node's row may be NaN.  Several trees may name one slot; a tree whose slot is negative gets rows of zeros, and a packed tree of more
     than 64 nodes rows of NaN.  The other arguments are those of
     :func:`recurrent_gated_delta_rule`.
     """

@@ -358,9 +358,11 @@ int gdr_step(const gdr_pool_args *args, hipStream_t stream);
    states are left as they are (sequences may share a slot).  A sequence is one tree
    of at most GDR_TREE_MAX nodes, parents before children (T above that without
    cu_seqlens is GDR_EINVAL; a longer packed sequence gets rows of NaN).  A node
-   influences its descendants only, with non-finite values too (an infinity may come
-   out as NaN).  Needs no workspace
-   and may be captured. */
+   influences its own row and its descendants' only, whatever its values.  Where a
+   value on a node's path is not finite, or a product of values on it (of keys, or of
+   the e^g of an ancestor's descendants) leaves fp32's range, the node's row may be NaN
+   where gdr_step gives an infinity or a number.  Needs no workspace and may be
+   captured. */
 int gdr_tree(const gdr_pool_args *args, hipStream_t stream);
 
 /* Acceptance on `stream`: the tokens on the path to node accepted[j] are taken into

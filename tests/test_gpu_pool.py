@@ -802,3 +802,27 @@ def test_tree_products_keep_what_is_small_by_cancellation(dtype, out, n, K, V):
         assert bool((last(q=q, k=k, v=v, beta=beta) == TINY).all())
         v[0, 0], v[0, 1] = BASE + TINY, BASE
         assert bool((last(q=half, k=k, v=v, beta=beta) == TINY / 2).all())
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, F32), (BF, BF), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("n,at", [(6, 0), (14, 7), (50, 34), (50, 14), (64, 60)])
+@pytest.mark.parametrize("size", [1e12, 1e15, 1e18])
+def test_large_finite_nodes_reach_their_descendants_only(dtype, out, n, at, size):
+    """Two large keys on one path, within a tile of 16 nodes and across two: products of their
+    scores leave fp32's range where each of them, or each of the scores, does not."""
+    say("large keys", dtype, out, n, at, size)
+    x = ref.make(1, n, 1, 2, 128, 128, dtype, seed=6)
+    parents = shape_of("random", n, torch.Generator().manual_seed(n + at))
+    for i, up in ((at + 1, at), (at + 2, at + 1), (at + 3, at + 2)):
+        parents[i] = up
+    for i in range(at + 4, n):  # the others hang on other nodes
+        if at < parents[i] < at + 4:
+            parents[i] = at if i % 2 else -1
+    x["parents"] = torch.tensor([parents], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    y = dict(x, k=x["k"].clone())
+    y["k"][0, at + 1:at + 3] *= size
+    o = run_tree(ref.cuda(y), output_dtype=out)
+    fine = [i for i in range(n) if at + 1 not in ref.path_of(parents, i)]
+    assert len(fine) == n - 3
+    ref.near(o[:, fine], o_want[:, fine], n, 128, X)
