@@ -435,21 +435,26 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kh[rt][t][i] = b4[i] * (to_f32(v[rt][i][t]) - e4[i] * kh[rt][t][i]);
-                probe += 0.f * kh[rt][t][i];
+                probe += 4.f * fabsf(kh[rt][t][i]);  // not finite from 2^126 on
             }
     }
     uint64_t lost[2] = {0, 0};  // nodes whose right-hand side in this lane's columns is not finite
-    if (__ballot(probe != probe))
+    const bool large = __ballot(!(probe < __builtin_inff())) != 0;
+    // from 2^128 - 2^119 on a finite value's first piece would be infinite, and NaN against
+    // a zero of M: the wave's columns are taken 2^8 times smaller
+    if (large)
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
                     if (!(fabsf(kh[rt][t][i]) < __builtin_inff())) {
                         lost[t] |= 1ull << (16 * rt + 4 * g + i);
                         kh[rt][t][i] = 0.f;
                     }
+                    kh[rt][t][i] *= 0x1p-8f;
+                }
     bf16x8 rs[NP][2][PIECES];
 #pragma unroll
     for (int cp = 0; cp < NP; ++cp)
@@ -462,7 +467,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     f32x4 o[NT][2];
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt) {
-        const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
+        const f32x4 e4 = (large ? 0x1p-8f : 1.f) * *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
 #pragma unroll
         for (int t = 0; t < 2; ++t) o[rt][t] = e4 * qh[rt][t];
     }
@@ -500,12 +505,13 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                 }
         }
     }
+    const float scale = p.scale * (large ? 0x1p8f : 1.f);
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             store2(Out(), out, (16 * rt + 4 * g + i) * ob + col * (int)sizeof(Out),
-                   pair{p.scale * o[rt][0][i], p.scale * o[rt][1][i]});
+                   pair{scale * o[rt][0][i], scale * o[rt][1][i]});
 }
 
 // waves per SIMD that the registers (and, where NT = 4, LDS) leave room for

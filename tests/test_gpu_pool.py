@@ -826,3 +826,29 @@ def test_large_finite_nodes_reach_their_descendants_only(dtype, out, n, at, size
     fine = [i for i in range(n) if at + 1 not in ref.path_of(parents, i)]
     assert len(fine) == n - 3
     ref.near(o[:, fine], o_want[:, fine], n, 128, X)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("n", [14, 50])
+@pytest.mark.parametrize("value", [torch.finfo(F32).min, torch.finfo(F32).max, 2.0 ** 127, float(torch.finfo(BF).min)])
+def test_values_at_the_ends_of_fp32_stay_in_their_column_and_path(out, n, value):
+    """A value next to fp32's largest, which bfloat16 rounds to an infinity, in one column of one node:
+    that column of the node and its descendants follows it, all else is as without it."""
+    say("large value", out, n, value)
+    x = ref.make(1, n, 1, 2, 128, 128, F32, seed=7)
+    parents = shape_of("random", n, torch.Generator().manual_seed(n))
+    bad, col = n // 3, 37
+    parents[bad + 1], parents[bad + 2] = bad, bad - 1
+    x["parents"] = torch.tensor([parents], **I32)
+    x["beta"][0, bad, 0] = 1.0
+    o_want, X = ref.tree(x, x["parents"])
+    y = dict(x, v=x["v"].clone())
+    y["v"][0, bad, 0, col] = value
+    o_large, X_large = ref.tree(y, x["parents"])
+    got = run_tree(ref.cuda(y), output_dtype=out)
+    hit = [i for i in range(n) if bad in ref.path_of(parents, i)]
+    assert 1 < len(hit) < n
+    ref.near(got[:, hit, 0, col], o_large[:, hit, 0, col], n, 128, X_large)
+    ok = torch.ones(1, n, 2, 128, dtype=torch.bool)
+    ok[0, hit, 0, col] = False
+    ref.near(torch.where(ok, got.cpu(), 0), torch.where(ok, o_want, 0.0), n, 128, X)
