@@ -128,6 +128,10 @@ void check_parents(const at::Tensor &parents, int64_t B, int64_t T, const at::Te
             }
     }
 }
+void check_no_gradient(const at::Tensor &t) {
+    NEED(!at::GradMode::is_enabled() || !t.requires_grad(),
+         "the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()");
+}
 // a pool's slots: each contiguous and aligned, apart from each other
 void check_slots(const at::Tensor &states, int64_t first, const char *name) {
     const int64_t n = states.size(first), H = states.size(first + 1), K = states.size(first + 2), V = states.size(first + 3);
@@ -206,10 +210,9 @@ bool run(Op op, const Call &x, at::Tensor &o) {
     }
     if (op == Op::ACCEPT) check_indices(*x.accepted, n_seq, "accepted", -1, x.cu ? GDR_TREE_MAX : T);
     const at::Tensor *floating[] = {&k, &v, x.g, x.beta, &states, x.q};
-    if (at::GradMode::is_enabled())
-        for (const at::Tensor *t : floating)
-            NEED(!t || !t->requires_grad(), "the operators on a pool of states have no gradient: use "
-                                            "chunk_gated_delta_rule, or torch.no_grad()");
+    for (const at::Tensor *t : floating)
+        if (t) check_no_gradient(*t);
+    if (x.out) check_no_gradient(*x.out);  // (a backward through it would miss that it was written)
     const at::Device dev = states.device();
     NEED(dev.is_cuda(), "inputs must be on the GPU");
     for (const at::Tensor *t : floating) NEED(!t || t->device() == dev, "all tensors must be on one GPU");
@@ -331,8 +334,8 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     NEED(n <= GDR_COPY_MAX, "at most ", GDR_COPY_MAX, " entries");
     check_indices(dst, n, "dst", -1, n_dst);
     check_indices(src, n, "src", -1, n_src);
-    NEED(!at::GradMode::is_enabled() || !(states.requires_grad() || source.requires_grad()),
-         "the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()");
+    check_no_gradient(states);
+    check_no_gradient(source);
     const at::Device dev = states.device();
     NEED(dev.is_cuda(), "inputs must be on the GPU");
     NEED(source.device() == dev, "all tensors must be on one GPU");

@@ -258,3 +258,15 @@ def test_copy_arguments_are_checked_before_any_launch(kw, code):
         setattr(a, n, v)
     assert _lib.lib.gdr_copy_states(ctypes.byref(a), None) == code
     assert _lib.lib.gdr_copy_states(None, None) == -1
+
+
+def test_an_output_that_requires_a_gradient_is_refused():
+    x = tree_inputs()
+    leaf = torch.zeros_like(x["v"], dtype=torch.float32).requires_grad_()
+    for out in (leaf, leaf * 2):
+        for op in (gdr.recurrent_gated_delta_rule, lambda *a, **kw: gdr.tree_gated_delta_rule(*a[:5], x["parents"], *a[5:], **kw)):
+            args = [x[n] for n in ("q", "k", "v", "g", "beta", "states")]
+            with pytest.raises(ValueError, match="no gradient"):
+                op(*args, slots=x["slots"], out=out)
+            with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+                op(*args, slots=x["slots"], out=out)
