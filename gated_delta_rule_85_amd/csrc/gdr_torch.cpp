@@ -10,6 +10,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -131,6 +132,9 @@ void check_parents(const at::Tensor &parents, int64_t B, int64_t T, const at::Te
 void check_no_gradient(const at::Tensor &t) {
     NEED(!at::GradMode::is_enabled() || !t.requires_grad(),
          "the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()");
+    // (torch.no_grad() leaves forward mode on)
+    NEED(!c10::AutogradState::get_tls_state().get_fw_grad_mode() || !t._fw_grad(0).defined(),
+         "the operators on a pool of states have no gradient, and no tangent in forward mode");
 }
 // a pool's slots: each contiguous and aligned, apart from each other
 void check_slots(const at::Tensor &states, int64_t first, const char *name) {

@@ -270,3 +270,39 @@ def test_an_output_that_requires_a_gradient_is_refused():
                 op(*args, slots=x["slots"], out=out)
             with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
                 op(*args, slots=x["slots"], out=out)
+
+
+@pytest.mark.parametrize("op", ["recurrent", "tree", "accept"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta", "states"])
+def test_forward_mode_tangents_are_refused(op, name):
+    import torch.autograd.forward_ad as forward
+    if (op, name) == ("accept", "q"):
+        return
+    with forward.dual_level():
+        x = tree_inputs()
+        plain = x[name]
+        for where in (torch.enable_grad, torch.no_grad):
+            x[name] = forward.make_dual(plain, torch.ones_like(plain))
+            with where(), pytest.raises(ValueError, match="tangent"):
+                call(op, x)
+        x[name] = forward.make_dual(plain, torch.ones_like(plain))[:]  # a view of it
+        with pytest.raises(ValueError, match="tangent"):
+            call(op, x)
+        x[name] = plain
+        with pytest.raises(ValueError, match="GPU"):
+            call(op, x)
+        if op == "recurrent" and name == "v":
+            out = torch.zeros_like(plain, dtype=torch.float32)
+            with pytest.raises(ValueError, match="tangent"):
+                call(op, dict(x, out=forward.make_dual(out, out.clone())))
+
+
+@pytest.mark.parametrize("dual", ["states", "source"])
+def test_copies_of_forward_mode_tangents_are_refused(dual):
+    import torch.autograd.forward_ad as forward
+    pools = dict(states=torch.zeros(2, 1, 64, 64), source=torch.zeros(2, 1, 64, 64))
+    one = torch.zeros(1, **I32)
+    with forward.dual_level():
+        pools[dual] = forward.make_dual(pools[dual], torch.ones(2, 1, 64, 64))
+        with pytest.raises(ValueError, match="tangent"):
+            gdr.copy_states(pools["states"], one, one, pools["source"])
