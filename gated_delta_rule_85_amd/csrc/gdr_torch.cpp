@@ -129,6 +129,14 @@ void check_parents(const at::Tensor &parents, int64_t B, int64_t T, const at::Te
             }
     }
 }
+void check_accepted(const at::Tensor &accepted, int64_t n_seq, int64_t T, const at::Tensor *cu) {
+    check_indices(accepted, n_seq, "accepted", -1, cu ? GDR_TREE_MAX : T);
+    if (!cu || cu->is_cuda() || accepted.is_cuda()) return;
+    const at::Tensor c = cu->contiguous(), a = accepted.contiguous();
+    const int32_t *offsets = c.const_data_ptr<int32_t>(), *nodes = a.const_data_ptr<int32_t>();
+    for (int64_t j = 0; j < n_seq; ++j)
+        NEED(nodes[j] < offsets[j + 1] - offsets[j], "accepted is -1 or a node of its tree");
+}
 void check_no_gradient(const at::Tensor &t) {
     NEED(!at::GradMode::is_enabled() || !t.requires_grad(),
          "the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()");
@@ -212,7 +220,7 @@ bool run(Op op, const Call &x, at::Tensor &o) {
     } else {
         NEED(n_slots >= n_seq, "states has ", n_slots, " slots for ", n_seq, " sequences");
     }
-    if (op == Op::ACCEPT) check_indices(*x.accepted, n_seq, "accepted", -1, x.cu ? GDR_TREE_MAX : T);
+    if (op == Op::ACCEPT) check_accepted(*x.accepted, n_seq, T, x.cu);
     const at::Tensor *floating[] = {&k, &v, x.g, x.beta, &states, x.q};
     for (const at::Tensor *t : floating)
         if (t) check_no_gradient(*t);

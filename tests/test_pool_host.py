@@ -306,3 +306,12 @@ def test_copies_of_forward_mode_tangents_are_refused(dual):
         pools[dual] = forward.make_dual(pools[dual], torch.ones(2, 1, 64, 64))
         with pytest.raises(ValueError, match="tangent"):
             gdr.copy_states(pools["states"], one, one, pools["source"])
+
+
+def test_accepted_nodes_of_packed_trees_are_checked_against_their_own_tree():
+    x = make(0, 0, 2, 4, 64, 64, lens=[2, 0, 3])
+    x["parents"] = torch.tensor([[-1, 0, -1, 0, 1]], dtype=torch.int32)
+    for accepted, message in (([1, -1, 2], "GPU"), ([2, -1, 2], "accepted"), ([1, 0, 2], "accepted"), ([1, -1, 3], "accepted")):
+        x["accepted"] = torch.tensor(accepted, dtype=torch.int32)
+        with pytest.raises(ValueError, match=message):
+            call("accept", x)
