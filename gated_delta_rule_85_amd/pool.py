@@ -21,14 +21,25 @@ import torch
 
 from . import _lib
 
-try:
-    from . import _gdr_torch
-except ImportError as e:
-    raise ImportError("_gdr_torch.so is not built (%s); run `python gated_delta_rule_85_amd/build.py` or "
-                      "__graft_entry__.build() first" % e) from e
+
+class _NotBuilt:
+    """Stands for the compiled binding where it cannot be imported: the chunked operator does
+    not need it, and the operators here raise ImportError when they are called."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("_gdr_torch.so is not built for this interpreter and torch (%s); run `python "
+                          "gated_delta_rule_85_amd/build.py` or __graft_entry__.build() first" % self._why)
+
 
 # the functions below are called once per layer and token: their checks are in csrc/gdr_torch.cpp
-_gdr_torch.connect(_lib.GdrError, torch._C._cuda_getCurrentRawStream)
+try:
+    from . import _gdr_torch
+    _gdr_torch.connect(_lib.GdrError, torch._C._cuda_getCurrentRawStream)
+except ImportError as e:
+    _gdr_torch = _NotBuilt(e)
 
 
 def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=None, *, slots=None,

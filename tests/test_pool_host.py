@@ -3,6 +3,7 @@ before anything is launched."""
 import ctypes
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -315,3 +316,43 @@ def test_accepted_nodes_of_packed_trees_are_checked_against_their_own_tree():
         x["accepted"] = torch.tensor(accepted, dtype=torch.int32)
         with pytest.raises(ValueError, match=message):
             call("accept", x)
+
+
+# ---------------------------------------------------------------- the compiled binding
+def package_without(tmp_path, *left_out):
+    """A copy of the package that lacks some files."""
+    import shutil
+    to = tmp_path / "gated_delta_rule_85_amd"
+    shutil.copytree(os.path.join(ROOT, "gated_delta_rule_85_amd"), to,
+                    ignore=shutil.ignore_patterns("__pycache__", "csrc", *left_out))
+    return to
+
+
+def in_a_process(tmp_path, code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return r.stdout
+
+
+NEEDS_BINDING = """
+import torch, gated_delta_rule_85_amd as gdr
+from gated_delta_rule_85_amd import _lib
+z, i = torch.zeros(2, 1, 64, 64), torch.zeros(1, dtype=torch.int32)
+assert gdr.num_chunks(65) == 2 and _lib.abi_version() == %d
+for call in (lambda: gdr.copy_states(z, i, i), lambda: gdr.recurrent_gated_delta_rule(z, z, z, z, z, z),
+             lambda: gdr.tree_gated_delta_rule(z, z, z, z, z, i, z), lambda: gdr.tree_gated_delta_rule_accept(z, z, z, z, i, i, z)):
+    try:
+        call()
+    except ImportError as e:
+        print(e)
+try:
+    gdr.chunk_gated_delta_rule(z, z, z, z, z)
+except ValueError as e:  # its own checks
+    print("chunked:", e)
+"""
+
+
+def test_the_chunked_operator_does_not_need_the_binding(tmp_path):
+    package_without(tmp_path, "_gdr_torch.so")
+    out = in_a_process(tmp_path, NEEDS_BINDING % _lib.ABI_VERSION).splitlines()
+    assert len(out) == 5 and all("_gdr_torch" in line for line in out[:4]) and out[4].startswith("chunked: ")
