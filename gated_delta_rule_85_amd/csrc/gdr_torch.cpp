@@ -369,6 +369,12 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
 // connect(GdrError, function from a device's index to its current stream's handle)
 PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count(n, 2)) return nullptr;
+    // the argument blocks' layouts are compiled in here
+    if (gdr_abi_version() != GDR_ABI_VERSION) {
+        PyErr_Format(PyExc_ImportError, "libgdr ABI version %d, _gdr_torch is built for %d", gdr_abi_version(),
+                     GDR_ABI_VERSION);
+        return nullptr;
+    }
     library_error = Py_NewRef(a[0]);
     current_stream = Py_NewRef(a[1]);
     Py_RETURN_NONE;

@@ -356,3 +356,23 @@ def test_the_chunked_operator_does_not_need_the_binding(tmp_path):
     package_without(tmp_path, "_gdr_torch.so")
     out = in_a_process(tmp_path, NEEDS_BINDING % _lib.ABI_VERSION).splitlines()
     assert len(out) == 5 and all("_gdr_torch" in line for line in out[:4]) and out[4].startswith("chunked: ")
+
+
+def test_the_binding_refuses_a_library_of_another_abi(tmp_path):
+    """Next to a library with the binding's symbols and another version."""
+    to = package_without(tmp_path, "libgdr.so")
+    src = tmp_path / "other.c"
+    src.write_text("int gdr_abi_version(void) { return %d; }\n" % (_lib.ABI_VERSION + 1)
+                   + "".join("int %s(const void *a, void *s) { return 0; }\n" % f for f in ENTRIES + ["gdr_copy_states"]))
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(to / "libgdr.so")], check=True)
+    out = in_a_process(tmp_path, """
+import importlib.util, torch
+spec = importlib.util.spec_from_file_location("_gdr_torch", %r)
+m = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(m)
+try:
+    m.connect(RuntimeError, len)
+except ImportError as e:
+    print(e)
+""" % str(to / "_gdr_torch.so"))
+    assert "%d" % (_lib.ABI_VERSION + 1) in out and "ABI" in out
