@@ -11,6 +11,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -77,14 +78,14 @@ def build(verbose=False):
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
         binding, torch_libs = binding.result()
-    tmp = OUT + ".tmp%d" % os.getpid()
-    subprocess.run([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs,
-                   check=True)
-    os.replace(tmp, OUT)
-    tmp = BINDING + ".tmp%d" % os.getpid()
-    subprocess.run(["g++", "-shared", "-o", tmp, binding, "-L" + PKG, "-lgdr", "-Wl,-rpath,$ORIGIN"] + torch_libs,
-                   check=True)
-    os.replace(tmp, BINDING)
+    # both are linked before either takes its place: a failure leaves the old pair
+    with tempfile.TemporaryDirectory(dir=BUILD) as tmp:
+        lib, bind = (os.path.join(tmp, os.path.basename(f)) for f in (OUT, BINDING))
+        subprocess.run([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", lib] + objs, check=True)
+        subprocess.run(["g++", "-shared", "-o", bind, binding, "-L" + tmp, "-lgdr", "-Wl,-rpath,$ORIGIN"] + torch_libs,
+                       check=True)
+        os.replace(lib, OUT)
+        os.replace(bind, BINDING)
     if verbose:
         print(OUT)
     return OUT

@@ -376,3 +376,34 @@ except ImportError as e:
     print(e)
 """ % str(to / "_gdr_torch.so"))
     assert "%d" % (_lib.ABI_VERSION + 1) in out and "ABI" in out
+
+
+@pytest.mark.parametrize("fails", ["hipcc", "g++", None])
+def test_a_build_replaces_the_library_and_its_binding_together(tmp_path, monkeypatch, fails):
+    """With the compilers' steps played: after a failed link both files are the old ones."""
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_build_script", os.path.join(ROOT, "gated_delta_rule_85_amd", "build.py"))
+    script = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(script)
+    files = {"OUT": tmp_path / "libgdr.so", "BINDING": tmp_path / "_gdr_torch.so"}
+    for name, f in files.items():
+        f.write_text("old")
+        monkeypatch.setattr(script, name, str(f))
+    monkeypatch.setattr(script, "BUILD", str(tmp_path / "objects"))
+    monkeypatch.setattr(script, "_compile", lambda src: src)
+    monkeypatch.setattr(script, "_compile_binding", lambda: ("binding.o", []))
+
+    def play(cmd, check):
+        if fails and cmd[0].endswith(fails):
+            raise subprocess.CalledProcessError(1, cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("new")
+
+    monkeypatch.setattr(script.subprocess, "run", play)
+    if fails:
+        with pytest.raises(subprocess.CalledProcessError):
+            script.build()
+    else:
+        script.build()
+    assert [f.read_text() for f in files.values()] == ["old" if fails else "new"] * 2
+    assert sorted(p.name for p in tmp_path.iterdir()) == ["_gdr_torch.so", "libgdr.so", "objects"]
