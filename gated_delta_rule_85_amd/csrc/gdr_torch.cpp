@@ -326,6 +326,27 @@ int check_pool(const at::Tensor &x, const char *name) {
     return 1;
 }
 
+// whether a state of one pool shares memory with one of the other; pools of equal strides may lie
+// between each other's slots (those of unequal strides count as overlapping where their spans do)
+bool pools_overlap(const at::Tensor &x, const at::Tensor &y, int at_slot) {
+    if (!overlap(x, y)) return false;
+    const int64_t nx = x.size(at_slot), ny = y.size(at_slot), layers = at_slot ? x.size(0) : 1;
+    const int64_t state = 4 * x.size(at_slot + 1) * x.size(at_slot + 2) * x.size(at_slot + 3);
+    const int64_t slot = 4 * (nx > 1 ? x : y).stride(at_slot), layer = layers > 1 ? 4 * x.stride(0) : 0;
+    if ((nx > 1 && ny > 1 && x.stride(at_slot) != y.stride(at_slot)) || (layers > 1 && x.stride(0) != y.stride(0)))
+        return true;
+    const int64_t apart = (const char *)x.data_ptr() - (const char *)y.data_ptr();
+    for (int64_t a = 1 - layers; a < layers; ++a) {
+        // x's state s lies `at + (s - t) slot` bytes from y's t: s - t that bring them nearest
+        const int64_t at = apart + a * layer, near = slot ? -at / slot : 0;
+        for (int64_t b = near - 1; b <= near + 1; ++b) {
+            const int64_t d = at + b * slot;
+            if (b > -ny && b < nx && d > -state && d < state) return true;
+        }
+    }
+    return false;
+}
+
 // copy(states, dst, src, source)
 PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
@@ -340,7 +361,7 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
              "states and source must hold states of one shape and as many layers");
         const bool same = source.data_ptr() == states.data_ptr() && source.sizes() == states.sizes() &&
                           source.strides() == states.strides();
-        NEED(same || !overlap(states, source), "source overlaps states");
+        NEED(same || !pools_overlap(states, source, at_slot), "source overlaps states");
     }
     const int64_t n = dst.numel(), n_dst = states.size(at_slot), n_src = source.size(at_slot);
     NEED(n <= GDR_COPY_MAX, "at most ", GDR_COPY_MAX, " entries");

@@ -112,6 +112,7 @@ def copy_states(states, dst, src, source=None):
     ``states`` and ``source``: float32 [n_slots,H_v,K,V], or [layers,n_slots,H_v,K,V]
     for the pools of several layers copied by the same list; ``dst``, ``src``: int32
     [n].  ``source`` may be another pool, such as the final states of a prefill; it
-    must not overlap ``states`` in memory, unless it is the same pool.
+    must not overlap ``states`` in memory, unless it is the same pool; the states of two
+    pools of equal strides may lie between each other's.
     """
     return _gdr_torch.copy(states, dst, src, source)

@@ -852,3 +852,18 @@ def test_values_at_the_ends_of_fp32_stay_in_their_column_and_path(out, n, value)
     ok = torch.ones(1, n, 2, 128, dtype=torch.bool)
     ok[0, hit, 0, col] = False
     ref.near(torch.where(ok, got.cpu(), 0), torch.where(ok, o_want, 0.0), n, 128, X)
+
+
+@pytest.mark.parametrize("layers", [0, 3])
+def test_copies_between_pools_that_share_an_allocation(layers):
+    """Two pools whose states lie between each other's."""
+    both = torch.randn((layers or 1), 7, 2, 2, 64, 64, generator=torch.Generator().manual_seed(4))
+    dst, src = torch.tensor([6, 0, 3, 1], **I32), torch.tensor([2, 6, -1, 2], **I32)
+    buf = both.cuda()
+    states, source = buf[:, :, 0], buf[:, :, 1]
+    want = both.clone()
+    want[:, :, 0] = copied(both[:, :, 0], dst, src, both[:, :, 1])
+    if not layers:
+        states, source = states[0], source[0]
+    gdr.copy_states(states, dst.cuda(), src.cuda(), source)
+    assert torch.equal(buf.cpu(), want)

@@ -407,3 +407,39 @@ def test_a_build_replaces_the_library_and_its_binding_together(tmp_path, monkeyp
         script.build()
     assert [f.read_text() for f in files.values()] == ["old" if fails else "new"] * 2
     assert sorted(p.name for p in tmp_path.iterdir()) == ["_gdr_torch.so", "libgdr.so", "objects"]
+
+
+def test_pools_that_lie_between_each_others_slots_do_not_overlap():
+    """Against the states' own bytes: halves of wider slots, layers of one allocation, and shifted ones."""
+    one = torch.zeros(1, **I32)
+
+    def used(x):
+        first = (x.data_ptr() - base) // 4
+        index = sum(torch.arange(n).view([-1 if j == i else 1 for j in range(x.dim())]) * s
+                    for i, (n, s) in enumerate(zip(x.shape, x.stride()))).reshape(-1) + first
+        return set(index.tolist())
+
+    buf = torch.zeros(6, 2, 1, 64, 64)
+    base = buf.data_ptr()
+    wide = buf.view(6, 2 * 4096)
+    part = lambda lo, n=6: wide[:n, lo:lo + 4096].view(n, 1, 64, 64)  # noqa: E731
+    flat = buf.view(-1)
+    strided = lambda at, n, slot: flat.as_strided((n, 1, 64, 64), (slot, 4096, 64, 1), at)  # noqa: E731
+    layered = lambda at, layers, n, layer, slot: flat.as_strided(  # noqa: E731
+        (layers, n, 1, 64, 64), (layer, slot, 4096, 64, 1), at)
+    pairs = [(buf[:, 0], buf[:, 1]), (buf[:, 1], buf[:, 0]), (part(0), part(4092)), (part(4), part(4096)), (part(0, 3), part(4096)),
+             (buf[:3, 0], buf[2:, 1]), (buf[:, 0], buf[2:3, 1]), (buf[2:3, 1], buf[:, 0]), (buf[2:3, 0], buf[:, 0]),
+             (strided(0, 3, 8192), strided(4096, 3, 8192)), (strided(0, 3, 8192), strided(8192, 3, 8192)),
+             (strided(0, 2, 16384), strided(8192, 2, 16384)), (strided(0, 2, 16384), strided(32768, 1, 16384)),
+             (layered(0, 2, 2, 24576, 8192), layered(4096, 2, 2, 24576, 8192)),
+             (layered(0, 2, 2, 24576, 8192), layered(16384, 2, 1, 24576, 8192)),
+             (layered(0, 2, 2, 8192, 16384), layered(4096, 2, 2, 8192, 16384)),
+             (layered(0, 2, 2, 8192, 16384), layered(8192, 2, 2, 8192, 16384)),
+             (layered(0, 2, 3, 4096, 8192), layered(40960, 2, 1, 4096, 8192))]
+    met = set()
+    for states, source in pairs:
+        shared = bool(used(states) & used(source))
+        met.add(shared)
+        with pytest.raises(ValueError, match="overlaps" if shared else "GPU"):
+            gdr.copy_states(states, one, one, source)
+    assert met == {False, True}
