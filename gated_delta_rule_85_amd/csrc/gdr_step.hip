@@ -81,7 +81,7 @@ template <typename In, int R> struct Rows {
     }
 };
 
-template <typename In, int R, bool OUT> struct Token {
+template <typename In, int R> struct Token {
     Rows<In, R> k, q;
     In v;
     float g, beta;
@@ -127,8 +127,8 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     const In *kp = reinterpret_cast<const In *>(p.k) + hq * K + row0;
     const In *qp = reinterpret_cast<const In *>(p.q) + hq * K + row0;
     const In *vp = reinterpret_cast<const In *>(p.v) + hv * V + mine;
-    Token<In, R, !ACCEPT> now, next;
-    auto fetch = [&](Token<In, R, !ACCEPT> &t, int64_t i) {
+    Token<In, R> now, next;
+    auto fetch = [&](Token<In, R> &t, int64_t i) {
         t.k.load(kp + row_offset(p, j, i, p.k_batch, p.k_row));
         if constexpr (!ACCEPT) t.q.load(qp + row_offset(p, j, i, p.q_batch, p.q_row));
         t.v = vp[row_offset(p, j, i, p.v_batch, p.v_row)];
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     };
     // every rounding is written out (no contraction by the compiler), so that an acceptance
     // and the recurrent form on the same tokens agree to the bit
-    auto step = [&](const Token<In, R, !ACCEPT> &t, int64_t i) {
+    auto step = [&](const Token<In, R> &t, int64_t i) {
 #pragma clang fp contract(off)
         f32x4 kh = zero4(), qh = zero4();
         float qk = 0.f;

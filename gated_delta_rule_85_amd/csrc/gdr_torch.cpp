@@ -27,7 +27,6 @@ namespace {
 PyObject *library_error = nullptr;  // GdrError(entry point, code)
 PyObject *current_stream = nullptr; // device index -> handle of its current stream
 
-#define REFUSE(...) TORCH_CHECK_VALUE(false, __VA_ARGS__)
 #define NEED(cond, ...) TORCH_CHECK_VALUE(cond, __VA_ARGS__)
 
 const at::Tensor *optional_tensor(PyObject *o, const char *name) {
