@@ -17,8 +17,8 @@
 // (K = V = 128, 1.07 GB) take 185 us, 5.8 TB/s; an in-place multiplication of 1 GB runs at
 // 6.0.  The loads and stores of the state are nontemporal and an XCD takes runs of 8 heads:
 // 205 us with cached accesses, 189 with heads dealt singly.  Waves of 16 columns (twice as
-// many) take 269 us there and gain 0.2 us at one sequence.  A token beyond the first adds
-// about 1 us to a sequence.
+// many) take 269 us there and gain 0.2 us at one sequence (both of one token).  A token beyond
+// the first adds about 1 us to a sequence: some 270 fp32 instructions of a wave.
 #include "gdr_pool.hpp"
 
 namespace gdr {

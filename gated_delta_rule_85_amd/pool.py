@@ -12,10 +12,11 @@ final states, and names a sequence's state by its slot:
 - :func:`copy_states` copies, forks, moves and clears states.
 
 They are inference operators: no gradients (the chunked operator has them), no
-workspace, no synchronisation, and all of them may be captured into a graph.
-``slots``, ``parents``, ``accepted`` and ``cu_seqlens`` are int32.  On the host
-their values are checked; on the device the library clamps or skips what is out of
-range (reading them here would synchronise the stream).
+workspace, and all of them may be captured into a graph.  ``slots``, ``parents``,
+``accepted``, ``cu_seqlens``, ``dst`` and ``src`` are int32.  On the device nothing
+waits for them: the library clamps or skips what is out of range (reading them here
+would synchronise the stream).  On the host their values are checked, and the copy to
+the device waits for the stream's earlier work and cannot be captured.
 """
 import torch
 
@@ -59,7 +60,9 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=
     ``states`` float32 [n_slots,H_v,K,V], the slots any distance apart; ``slots`` int32
     [N] names each sequence's slot (default: slot j for sequence j).  A sequence whose
     slot is negative (the padding of a batch) is skipped and its rows of ``o`` are
-    zero; so is a sequence that names a slot which an earlier one has.  ``out``: a
+    zero; so is a sequence that names a slot which an earlier one has (every sequence
+    looks through the slots before its own, which shows from about ten thousand on: 32768
+    sequences of two 64 x 64 heads take 540 us a step, 368 without ``slots``).  ``out``: a
     contiguous tensor to write; rows that belong to no sequence are left as they are.
     """
     return _gdr_torch.step(q, k, v, g, beta, states, scale, cu_seqlens, slots, output_dtype, out)

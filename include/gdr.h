@@ -350,7 +350,9 @@ int gdr_bwd(const gdr_bwd_args *args, hipStream_t stream);
    its state, in place, and o gets their outputs.  For one token or a few per
    sequence (decode); the chunked gdr_fwd is faster from about 16 on.  Where two
    sequences with tokens name one slot, the first has it and the others are
-   skipped, as if they had none.  Needs no workspace and may be captured. */
+   skipped, as if they had none.  For that every sequence looks through the slots before
+   its own, which shows from about ten thousand sequences on (not with slots NULL).
+   Needs no workspace and may be captured. */
 int gdr_step(const gdr_pool_args *args, hipStream_t stream);
 
 /* Trees of drafted tokens on `stream`: o of every node as if the recurrence had

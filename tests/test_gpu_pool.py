@@ -867,3 +867,23 @@ def test_copies_between_pools_that_share_an_allocation(layers):
         states, source = states[0], source[0]
     gdr.copy_states(states, dst.cuda(), src.cuda(), source)
     assert torch.equal(buf.cpu(), want)
+
+
+def test_indices_on_the_device_are_not_waited_for():
+    """A call returns while earlier work of its stream still runs."""
+    x = ref.make(0, 0, 1, 2, 64, 64, F32, [2, 1], seed=5)
+    x["parents"], x["accepted"] = torch.tensor([[-1, 0, -1]], **I32), torch.tensor([1, 0], **I32)
+    d = ref.cuda(x)
+    dst, src = torch.tensor([0], **I32, device="cuda"), torch.tensor([1], **I32, device="cuda")
+    calls = (lambda: run_recurrent(d), lambda: run_tree(d), lambda: run_accept(d),
+             lambda: gdr.copy_states(d["states"], dst, src))
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for call in calls:
+        torch.cuda._sleep(100_000_000)
+        before = torch.cuda.Event()
+        before.record()
+        call()
+        assert not before.query()
+        torch.cuda.synchronize()
