@@ -136,13 +136,17 @@ void check_accepted(const at::Tensor &accepted, int64_t n_seq, int64_t T, const 
     for (int64_t j = 0; j < n_seq; ++j)
         NEED(nodes[j] < offsets[j + 1] - offsets[j], "accepted is -1 or a node of its tree");
 }
-void check_no_gradient(const at::Tensor &t) {
-    NEED(!at::GradMode::is_enabled() || !t.requires_grad(),
-         "the operators on a pool of states have no gradient: use chunk_gated_delta_rule, or torch.no_grad()");
-    // (torch.no_grad() leaves forward mode on)
-    NEED(!c10::AutogradState::get_tls_state().get_fw_grad_mode() || !t._fw_grad(0).defined(),
-         "the operators on a pool of states have no gradient, and no tangent in forward mode");
-}
+// Refuses what autograd would have to follow.  (torch.no_grad() leaves forward mode on.)
+struct NoGradient {
+    const bool backward = at::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    void check(const at::Tensor &t) const {
+        if (!t.unsafeGetTensorImpl()->autograd_meta()) return;  // as on most tensors: neither of them
+        NEED(!backward || !t.requires_grad(), "the operators on a pool of states have no gradient: use "
+                                              "chunk_gated_delta_rule, or torch.no_grad()");
+        NEED(!forward || !t._fw_grad(0).defined(),
+             "the operators on a pool of states have no gradient, and no tangent in forward mode");
+    }
+};
 // a pool's slots: each contiguous and aligned, apart from each other
 void check_slots(const at::Tensor &states, int64_t first, const char *name) {
     const int64_t n = states.size(first), H = states.size(first + 1), K = states.size(first + 2), V = states.size(first + 3);
@@ -221,9 +225,10 @@ bool run(Op op, const Call &x, at::Tensor &o) {
     }
     if (op == Op::ACCEPT) check_accepted(*x.accepted, n_seq, T, x.cu);
     const at::Tensor *floating[] = {&k, &v, x.g, x.beta, &states, x.q};
+    const NoGradient gradient;
     for (const at::Tensor *t : floating)
-        if (t) check_no_gradient(*t);
-    if (x.out) check_no_gradient(*x.out);  // (a backward through it would miss that it was written)
+        if (t) gradient.check(*t);
+    if (x.out) gradient.check(*x.out);  // (a backward through it would miss that it was written)
     const at::Device dev = states.device();
     NEED(dev.is_cuda(), "inputs must be on the GPU");
     for (const at::Tensor *t : floating) NEED(!t || t->device() == dev, "all tensors must be on one GPU");
@@ -366,8 +371,9 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     NEED(n <= GDR_COPY_MAX, "at most ", GDR_COPY_MAX, " entries");
     check_indices(dst, n, "dst", -1, n_dst);
     check_indices(src, n, "src", -1, n_src);
-    check_no_gradient(states);
-    check_no_gradient(source);
+    const NoGradient gradient;
+    gradient.check(states);
+    gradient.check(source);
     const at::Device dev = states.device();
     NEED(dev.is_cuda(), "inputs must be on the GPU");
     NEED(source.device() == dev, "all tensors must be on one GPU");
