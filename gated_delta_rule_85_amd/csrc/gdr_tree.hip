@@ -20,7 +20,9 @@
 // P (from K and Q in LDS).  A wave that has P's tiles of rows r in registers, transposed,
 // solves M's rows r from the right: M^T_c = D_c^T (P^T_c + sum over k > c of (-A_kc)^T M^T_k), D
 // the inverses of I + A's diagonal tiles.  An accumulator tile of M^T is an A operand
-// tile of M, so M goes to LDS as it stands (in the place of K and Q), in bf16 pieces.
+// tile of M, so M goes to LDS as it stands (in the place of K and Q), in bf16 pieces.  The last
+// product is of 2 M and R / 2: from 2^128 - 2^119 on the first piece of a finite value of R
+// would be infinite, and NaN against the zeros of other nodes' rows of M.
 // fp32 rows of K and Q are split into pieces on their way to LDS: 8 trees of 64 nodes (fp32,
 // K = V = 128) take 17.0 us, 22.4 with fp32 matrix instructions, 13.0 with bf16 rows.
 //
@@ -157,7 +159,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     float *At = reinterpret_cast<float *>(smem + L::a);  // -A, later with D in the diagonal tiles
     double *G = reinterpret_cast<double *>(smem + L::G);
     uint64_t *mask = reinterpret_cast<uint64_t *>(smem + L::mask);
-    float *eg = reinterpret_cast<float *>(smem + L::eg), *beta = reinterpret_cast<float *>(smem + L::beta);
+    float *eg = reinterpret_cast<float *>(smem + L::eg), *half_beta = reinterpret_cast<float *>(smem + L::beta);
     unsigned *bad = reinterpret_cast<unsigned *>(smem + L::bad);  // two words of node bits
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), c = ln16(), g = lg4();
     const int col = 32 * w + 2 * c, hq = hv / (p.Hv / p.Hq);
@@ -250,14 +252,14 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
             G[l] = s;
             mask[l] = m;
             eg[l] = expf((float)s);
-            beta[l] = b;
+            half_beta[l] = 0.5f * b;
         }
         if (l < 2) bad[l] = 0;
     }
     lds_barrier();
 
     auto load = [&](Row &x, int base, int i, int kb) { x.load(smem + base + i * L::ROWB + (32 * kb + 8 * g) * 2, L::PLANE); };
-    // Rows r of A and of P, transposed: lane (c, g) has node 16 r + c against nodes
+    // Rows r of A and of 2 P, transposed: lane (c, g) has node 16 r + c against nodes
     // 16 ct + 4 g + i, whose decay D both share.  Tiles past the diagonal come out zero.
     constexpr int MINE = (NT + NW - 1) / NW;
     f32x4 mt[MINE][NT];
@@ -287,7 +289,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         const int node = 16 * r + c;
         const double Gb = G[node];
         const uint64_t above = mask[node];
-        const float minus_beta = -beta[node];
+        const float minus_beta = -2.f * half_beta[node];
         float probe = 0.f;  // becomes NaN where K's row or a row of A is not finite
 #pragma unroll
         for (int ct = 0; ct < NT; ++ct) {
@@ -299,7 +301,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                 if (self) probe += 0.f * kk[ct][i];
                 kk[ct][i] = on ? minus_beta * d * kk[ct][i] : 0.f;
                 probe += 0.f * kk[ct][i];
-                mt[y][ct][i] = on || self ? d * mt[y][ct][i] : 0.f;
+                mt[y][ct][i] = on || self ? 2.f * d * mt[y][ct][i] : 0.f;
             }
         }
         if (__ballot(probe != probe)) {
@@ -403,7 +405,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
             }
     }
     lds_barrier();
-    // M's rows r, from the right; the products with K and Q are done, M takes their place
+    // 2 M's rows r, from the right; the products with K and Q are done, M takes their place
 #pragma unroll
     for (int y = 0; y < MINE; ++y) {
         const int r = w + y * NW;
@@ -424,37 +426,32 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                     *reinterpret_cast<bf16x8 *>(smem + L::pair_at(r, cp) + 1024 * s + 16 * l) = m[s];
         }
     }
-    // R, in the place of K h
+    // R / 2, in the place of K h
     float probe = 0.f;
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt) {
         const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
-        const f32x4 b4 = *reinterpret_cast<const f32x4 *>(beta + 16 * rt + 4 * g);
+        const f32x4 b4 = *reinterpret_cast<const f32x4 *>(half_beta + 16 * rt + 4 * g);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 kh[rt][t][i] = b4[i] * (to_f32(v[rt][i][t]) - e4[i] * kh[rt][t][i]);
-                probe += 4.f * fabsf(kh[rt][t][i]);  // not finite from 2^126 on
+                probe += 2.f * fabsf(kh[rt][t][i]);
             }
     }
-    uint64_t lost[2] = {0, 0};  // nodes whose right-hand side in this lane's columns is not finite
-    const bool large = __ballot(!(probe < __builtin_inff())) != 0;
-    // from 2^128 - 2^119 on a finite value's first piece would be infinite, and NaN against
-    // a zero of M: the wave's columns are taken 2^8 times smaller
-    if (large)
+    uint64_t lost[2] = {0, 0};  // nodes whose R in this lane's columns is not finite
+    if (__ballot(!(probe < __builtin_inff())))
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!(fabsf(kh[rt][t][i]) < __builtin_inff())) {
+                for (int i = 0; i < 4; ++i)
+                    if (!(fabsf(kh[rt][t][i]) < 0x1p127f)) {
                         lost[t] |= 1ull << (16 * rt + 4 * g + i);
                         kh[rt][t][i] = 0.f;
                     }
-                    kh[rt][t][i] *= 0x1p-8f;
-                }
     bf16x8 rs[NP][2][PIECES];
 #pragma unroll
     for (int cp = 0; cp < NP; ++cp)
@@ -467,7 +464,7 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
     f32x4 o[NT][2];
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt) {
-        const f32x4 e4 = (large ? 0x1p-8f : 1.f) * *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
+        const f32x4 e4 = *reinterpret_cast<const f32x4 *>(eg + 16 * rt + 4 * g);
 #pragma unroll
         for (int t = 0; t < 2; ++t) o[rt][t] = e4 * qh[rt][t];
     }
@@ -505,13 +502,12 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
                 }
         }
     }
-    const float scale = p.scale * (large ? 0x1p8f : 1.f);
 #pragma unroll
     for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             store2(Out(), out, (16 * rt + 4 * g + i) * ob + col * (int)sizeof(Out),
-                   pair{scale * o[rt][0][i], scale * o[rt][1][i]});
+                   pair{p.scale * o[rt][0][i], p.scale * o[rt][1][i]});
 }
 
 // waves per SIMD that the registers (and, where NT = 4, LDS) leave room for
