@@ -28,13 +28,14 @@
 //
 // 64 packed trees of 37 to 64 nodes (H_v = 32, K = V = 128, bf16; 214 MB) take 54.5 us, 3.9 TB/s,
 // where a large copy runs at 5.0: three workgroups per compute unit hide most of their phases
-// from each other, but not all (two per unit take 2 us more).  Small batches are bound by the chain
-// of phases: one tree of 13 nodes takes 6.3 us, of 64 nodes 11.7.  Of the 20,000 cycles of a lone
-// workgroup of 64 nodes, 5,000 pass until K and Q are in LDS, the tiles of A and P take 2,900,
-// D 2,000, K h and Q h 3,300, M 2,300, R 1,200 and the output 1,900 (these with two pieces).
-// Also with two pieces: persistent workgroups with the next tree's loads in flight took 75 us
-// where this form took 49, tiles chosen by runtime conditions, each a branch of its own, 54.6
-// against 52, U by forward substitution in every wave instead of M 101 against 60.5.
+// from each other, but not all (two per unit take 2 us more), and the matrix units are busy for
+// 30% of it.  Small batches are bound by the chain of phases: one tree of 13 nodes takes 6.3 us,
+// of 64 nodes 11.7.  Of the 23,000 cycles of a lone workgroup of 64 nodes, 5,500 pass until K and Q
+// are in LDS, the tiles of A and P take 3,000, D 2,000, K h and Q h 5,900, M 2,600, R 1,600 and
+// the output 2,700.  With two pieces (see PIECES) persistent workgroups with the next tree's loads
+// in flight took 75 us where this form took 49, tiles chosen by runtime conditions, each a branch
+// of its own, 54.6 against 52, U by forward substitution in every wave instead of M 101 against
+// 60.5.
 //
 // Non-finite values.  Node j must not reach nodes that are no descendants of it,
 // though a product with a masked zero would turn its NaN or infinity into NaN there.
@@ -233,7 +234,9 @@ __device__ __forceinline__ void tree(const PoolParams &p, char *smem, int j, int
         // path sums and ancestors by pointer doubling: after a round a lane has its sum
         // over twice as many nodes.  The sums are in 64 bits (their differences would lose
         // a small gate next to a large one), and e^g below 2^-149 is zero, so that a floor
-        // under g keeps the differences finite where g is -inf.
+        // under g keeps the differences finite where g is -inf.  Later gates cannot lift what
+        // the floor stands for: its node is their ancestor, and from more than 88 between the
+        // two on, D is infinite and the row NaN anyway (-200 + 88 still has an e^ of zero).
         int at = up >= 0 && up < l ? up : -1;
         uint64_t m = at >= 0 ? 1ull << at : 0;
         double s = gate < -200.f ? -200.0 : (double)gate;

@@ -807,11 +807,12 @@ def test_tree_products_keep_what_is_small_by_cancellation(dtype, out, n, K, V):
 @pytest.mark.parametrize("dtype,out", [(BF, F32), (BF, BF), (F32, F32), (F32, BF)])
 @pytest.mark.parametrize("n,at", [(6, 0), (14, 7), (50, 34), (50, 14), (64, 60)])
 @pytest.mark.parametrize("size", [1e12, 1e15, 1e18])
-def test_large_finite_nodes_reach_their_descendants_only(dtype, out, n, at, size):
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_finite_nodes_reach_their_descendants_only(dtype, out, n, at, size, D):
     """Two large keys on one path, within a tile of 16 nodes and across two: products of their
     scores leave fp32's range where each of them, or each of the scores, does not."""
-    say("large keys", dtype, out, n, at, size)
-    x = ref.make(1, n, 1, 2, 128, 128, dtype, seed=6)
+    say("large keys", dtype, out, n, at, size, D)
+    x = ref.make(1, n, 1, 2, D, D, dtype, seed=6)
     parents = shape_of("random", n, torch.Generator().manual_seed(n + at))
     for i, up in ((at + 1, at), (at + 2, at + 1), (at + 3, at + 2)):
         parents[i] = up
@@ -825,7 +826,7 @@ def test_large_finite_nodes_reach_their_descendants_only(dtype, out, n, at, size
     o = run_tree(ref.cuda(y), output_dtype=out)
     fine = [i for i in range(n) if at + 1 not in ref.path_of(parents, i)]
     assert len(fine) == n - 3
-    ref.near(o[:, fine], o_want[:, fine], n, 128, X)
+    ref.near(o[:, fine], o_want[:, fine], n, D, X)
 
 
 @pytest.mark.parametrize("out", [BF, F32])
