@@ -39,7 +39,7 @@ class _NotBuilt:
 try:
     from . import _gdr_torch
     _gdr_torch.connect(_lib.GdrError, torch._C._cuda_getCurrentRawStream)
-except ImportError as e:
+except (ImportError, AttributeError) as e:  # (a torch without that function)
     _gdr_torch = _NotBuilt(e)
 
 

@@ -443,3 +443,9 @@ def test_pools_that_lie_between_each_others_slots_do_not_overlap():
         with pytest.raises(ValueError, match="overlaps" if shared else "GPU"):
             gdr.copy_states(states, one, one, source)
     assert met == {False, True}
+
+
+def test_the_chunked_operator_does_not_need_torchs_stream_handles():
+    """A torch without the function that the binding is given."""
+    out = in_a_process(ROOT, "import torch\ndel torch._C._cuda_getCurrentRawStream\n" + NEEDS_BINDING % _lib.ABI_VERSION).splitlines()
+    assert len(out) == 5 and all("_gdr_torch" in line for line in out[:4]) and out[4].startswith("chunked: ")
