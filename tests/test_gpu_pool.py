@@ -888,3 +888,46 @@ def test_indices_on_the_device_are_not_waited_for():
         call()
         assert not before.query()
         torch.cuda.synchronize()
+
+
+EXTREMES = [float("nan"), float("inf"), float("-inf"), 3.3e38, -3.38e38, 1e38, 1e30, 1e20, -1e19, 1e12, 1e-40, -1e7]
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("seed", range(12))
+def test_any_values_stay_with_their_nodes_and_columns(dtype, out, seed):
+    """Several nodes and a column of the state with values of any kind: what does not descend from
+    them is as without them."""
+    import random
+    rng = random.Random(seed)
+    K, V = rng.choice([64, 128]), rng.choice([64, 128])
+    n = rng.choice([5, 16, 17, 31, 33, 48, 50, 64])
+    say("extremes", dtype, out, seed, K, V, n)
+    x = ref.make(1, n, 1, 2, K, V, dtype, seed=seed)
+    parents = shape_of(rng.choice(["random", "binary", "star"]), n, torch.Generator().manual_seed(seed))
+    x["parents"] = torch.tensor([parents], **I32)
+    o_want, X = ref.tree(x, x["parents"])
+    y = {a: b.clone() if isinstance(b, torch.Tensor) else b for a, b in x.items()}
+    bad = set(rng.sample(range(1, n), max(1, n // 8)))
+    extremes = EXTREMES + ([torch.finfo(F32).min] if dtype is F32 else [])
+    for i in bad:
+        for name in ("q", "k", "v"):
+            how = rng.random()
+            if how < 0.3:
+                y[name][0, i] = rng.choice(extremes)
+            elif how < 0.6:
+                y[name][0, i, 0, rng.randrange(64)] = rng.choice(extremes)
+            elif how < 0.7:
+                y[name][0, i] *= rng.choice([1e10, 1e15, 1e20, 1e30])
+        if rng.random() < 0.5:
+            y["g"][0, i] = rng.choice(EXTREMES[:3] + [-3e38, 3e38, 88.0, 90.0, -250.0, 200.0])
+        if rng.random() < 0.4:
+            y["beta"][0, i] = rng.choice(EXTREMES[:3] + [1e30, -1e38, 0.0, 2.0])
+    row, col = rng.randrange(K), rng.randrange(V)
+    y["states"][int(x["slots"][0]), 0, row, col] = rng.choice(EXTREMES + [torch.finfo(F32).min])
+    o = run_tree(ref.cuda(y), output_dtype=out).cpu()
+    fine = [i for i in range(n) if not bad & set(ref.path_of(parents, i))]
+    assert fine
+    ok = torch.ones(1, len(fine), 2, V, dtype=torch.bool)
+    ok[:, :, 0, col] = False
+    ref.near(torch.where(ok, o[:, fine], 0), torch.where(ok, o_want[:, fine], 0.0), n, K, X)
