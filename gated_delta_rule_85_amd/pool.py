@@ -79,11 +79,11 @@ def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seql
     among its tree's nodes, which come after their parents, or -1 for a child of the
     cached state; an entry that is no earlier node counts as -1.  A node influences
     its own row and its descendants' only, whatever its values; where a value on a node's
-    path is not finite, or a product of values on it (of q and keys, or the e^g between an
-    ancestor and the node: gates that add up to more than 88) passes 1.6e38, the node's
-    row may be NaN (values of q, k and the state past bfloat16's 3.39e38 count as
-    infinite).  Several trees may name one slot; a tree whose slot is negative gets rows of zeros, and a packed tree of more
-    than 64 nodes rows of NaN.  The other arguments are those of
+    path is not finite, or a product of values on it (of q and keys, or the e^g from the
+    state or an ancestor to the node: gates that add up to more than 88) passes 1.6e38,
+    the node's row may be NaN (values of q, k and the state past bfloat16's 3.39e38 count
+    as infinite).  Several trees may name one slot; a tree whose slot is negative gets
+    rows of zeros, and a packed tree of more than 64 nodes rows of NaN.  The other arguments are those of
     :func:`recurrent_gated_delta_rule`.
     """
     return _gdr_torch.tree(q, k, v, g, beta, parents, states, scale, cu_seqlens, slots, output_dtype, out)

@@ -362,8 +362,8 @@ int gdr_step(const gdr_pool_args *args, hipStream_t stream);
    cu_seqlens is GDR_EINVAL; a longer packed sequence gets rows of NaN).  A node
    influences its own row and its descendants' only, whatever its values.  Where a
    value on a node's path is not finite, or a product of values on it (of q and keys, or
-   the e^g between an ancestor and the node: gates that add up to more than 88) passes
-   1.6e38, the node's row may be NaN where gdr_step gives an infinity or a number.
+   the e^g from the state or an ancestor to the node: gates that add up to more than 88)
+   passes 1.6e38, the node's row may be NaN where gdr_step gives an infinity or a number.
    Values of q, k and the state past bfloat16's range (3.39e38) count as infinite here.
    Needs no workspace and may be captured. */
 int gdr_tree(const gdr_pool_args *args, hipStream_t stream);
