@@ -8,9 +8,11 @@ step).
 """
 from .api import (SavedForBackward, chunk_bound, chunk_gated_delta_rule, chunk_gated_delta_rule_bwd,
                   chunk_gated_delta_rule_fwd, num_chunks)
+from .linear_attention import chunk_linear_attention, chunk_linear_attention_bwd, chunk_linear_attention_fwd
 from .pool import (copy_states, recurrent_gated_delta_rule, tree_gated_delta_rule,
                    tree_gated_delta_rule_accept)
 
 __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd",
            "num_chunks", "chunk_bound", "SavedForBackward", "recurrent_gated_delta_rule",
-           "tree_gated_delta_rule", "tree_gated_delta_rule_accept", "copy_states"]
+           "tree_gated_delta_rule", "tree_gated_delta_rule_accept", "copy_states", "chunk_linear_attention",
+           "chunk_linear_attention_fwd", "chunk_linear_attention_bwd"]

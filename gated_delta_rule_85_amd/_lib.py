@@ -10,7 +10,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
 
-ABI_VERSION = 8
+ABI_VERSION = 9
 CHUNK = 64
 FWD_STAGES = 3
 BWD_STAGES = 4
@@ -79,6 +79,34 @@ class CopyArgs(ctypes.Structure):
     ]
 
 
+class LaFwdArgs(ctypes.Structure):
+    """Mirror of gdr_la_fwd_args."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("H_q", _i64), ("H_v", _i64), ("K", _i64), ("V", _i64), ("n_seq", _i64),
+        ("q_row", _i64), ("k_row", _i64), ("v_row", _i64),
+        ("q_batch", _i64), ("k_batch", _i64), ("v_batch", _i64),
+        ("dtype", _i32), ("out_dtype", _i32), ("g_per_head", _i32), ("segment_chunks", _i32),
+        ("scale", ctypes.c_float),
+        ("q", _p), ("k", _p), ("v", _p), ("g", _p), ("initial_state", _p), ("cu_seqlens", _p),
+        ("o", _p), ("final_state", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class LaBwdArgs(ctypes.Structure):
+    """Mirror of gdr_la_bwd_args."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("H_q", _i64), ("H_v", _i64), ("K", _i64), ("V", _i64), ("n_seq", _i64),
+        ("q_row", _i64), ("k_row", _i64), ("v_row", _i64),
+        ("q_batch", _i64), ("k_batch", _i64), ("v_batch", _i64),
+        ("dtype", _i32), ("grad_dtype", _i32), ("g_per_head", _i32), ("segment_chunks", _i32),
+        ("scale", ctypes.c_float),
+        ("q", _p), ("k", _p), ("v", _p), ("g", _p), ("initial_state", _p), ("cu_seqlens", _p),
+        ("dout", _p), ("dht", _p),
+        ("dq", _p), ("dk", _p), ("dv", _p), ("dg", _p), ("dh0", _p),
+        ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -89,7 +117,7 @@ def _load():
     lib.gdr_abi_version.argtypes = []
     lib.gdr_strerror.restype = ctypes.c_char_p
     lib.gdr_strerror.argtypes = [ctypes.c_int]
-    for name, st in (("gdr_fwd", FwdArgs), ("gdr_bwd", BwdArgs)):
+    for name, st in (("gdr_fwd", FwdArgs), ("gdr_bwd", BwdArgs), ("gdr_la_fwd", LaFwdArgs), ("gdr_la_bwd", LaBwdArgs)):
         f = getattr(lib, name)
         f.restype = ctypes.c_int
         f.argtypes = [ctypes.POINTER(st), _p]
@@ -169,3 +197,31 @@ def bwd(args, stream):
     rc = lib.gdr_bwd(ctypes.byref(args), _p(stream))
     if rc:
         raise GdrError("gdr_bwd", rc)
+
+
+def _sized(name, args):
+    n = ctypes.c_size_t(0)
+    rc = getattr(lib, name)(ctypes.byref(args), ctypes.byref(n))
+    if rc:
+        raise GdrError(name, rc)
+    return n.value
+
+
+def la_fwd_workspace(args):
+    return _sized("gdr_la_fwd_workspace", args)
+
+
+def la_bwd_workspace(args):
+    return _sized("gdr_la_bwd_workspace", args)
+
+
+def la_fwd(args, stream):
+    rc = lib.gdr_la_fwd(ctypes.byref(args), _p(stream))
+    if rc:
+        raise GdrError("gdr_la_fwd", rc)
+
+
+def la_bwd(args, stream):
+    rc = lib.gdr_la_bwd(ctypes.byref(args), _p(stream))
+    if rc:
+        raise GdrError("gdr_la_bwd", rc)

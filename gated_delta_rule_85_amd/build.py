@@ -44,7 +44,8 @@ MAX_ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 SOURCES = {"gdr_api.hip": VGPR_FORM, "gdr_prep.hip": VGPR_FORM, "gdr_scan.hip": VGPR_FORM + ILP,
            "gdr_bwd.hip": VGPR_FORM, "gdr_bwd_scan.hip": VGPR_FORM,
            "gdr_bwd_mfma.hip": VGPR_FORM + MAX_ILP, "gdr_noalloc.hip": [],
-           "gdr_step.hip": [], "gdr_tree.hip": VGPR_FORM, "gdr_copy.hip": [], "gdr_pool_api.hip": []}
+           "gdr_step.hip": [], "gdr_tree.hip": VGPR_FORM, "gdr_copy.hip": [], "gdr_pool_api.hip": [],
+           "gdr_la_scan.hip": VGPR_FORM, "gdr_la_bwd.hip": [], "gdr_la_api.hip": []}
 
 
 def _compile(src):

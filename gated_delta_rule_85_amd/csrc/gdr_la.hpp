@@ -1,0 +1,121 @@
+// Linear attention with a decay for each head (gdr_la_fwd, gdr_la_bwd): parameter blocks,
+// launchers and the lookups its kernels share.
+#pragma once
+
+#include "gdr_kernels.hpp"
+#include "gdr_lds.hpp"
+
+namespace gdr {
+
+// The sequences, their gates, and their segments of seg_chunks chunks.  Border b of a sequence
+// (1 <= b < its segments) lies before token 64 seg_chunks b.  What is kept per segment or border
+// of all sequences is indexed by la_first() + its number; there are la_slots() such places.
+struct LaSeqs {
+    const int32_t *cu;  // [n_seq + 1] or null
+    const float *g;
+    int64_t g_tok;      // floats between the gates of two tokens (0: one gate per head)
+    int64_t T;
+    int n_seq, Hv, seg_chunks;
+};
+
+// tokens [bos, eos) of sequence j among [0, B T); offsets are clamped to [0, T], an end before
+// its start to the start
+__device__ __forceinline__ void la_bounds(const LaSeqs &s, int j, int64_t &bos, int64_t &eos) {
+    if (s.cu) {
+        bos = min(max((int64_t)s.cu[j], (int64_t)0), s.T);
+        eos = min(max((int64_t)s.cu[j + 1], bos), s.T);
+    } else {
+        bos = (int64_t)j * s.T;
+        eos = bos + s.T;
+    }
+}
+// place of a sequence's first segment: a sequence of n tokens takes n / seg_tokens + 1 places at
+// most, and the sequences' places do not meet
+__host__ __device__ __forceinline__ int la_first(int64_t bos, int j, int64_t seg_tokens) {
+    return (int)(bos / seg_tokens) + j;
+}
+__host__ __device__ __forceinline__ int64_t la_slots(int64_t tokens, int64_t n_seq, int64_t seg_tokens) {
+    return tokens / seg_tokens + n_seq;
+}
+// sequence and segment of a place (false: none)
+__device__ __forceinline__ bool la_place(const LaSeqs &s, int place, int &j, int &m) {
+    const int64_t seg_tokens = (int64_t)s.seg_chunks * CH;
+    int lo = 0, hi = s.n_seq - 1;  // the last sequence whose first place is not past it
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        int64_t bos, eos;
+        la_bounds(s, mid, bos, eos);
+        if (la_first(bos, mid, seg_tokens) <= place) lo = mid; else hi = mid - 1;
+    }
+    int64_t bos, eos;
+    la_bounds(s, lo, bos, eos);
+    j = lo;
+    m = place - la_first(bos, lo, seg_tokens);
+    return m >= 0 && (m == 0 || m * seg_tokens < eos - bos);
+}
+
+// One scan: o_t = out_scale S_t^T q_t with S_t = e^g S + in_scale k_t v_t^T over every sequence
+// and v head, S of KD x W.  The forward is one; the backward is three, with the tensors in other
+// places, two of them from the last token to the first (rev: a row's gate is then the next
+// token's).  q, k and v rows of v head hv are those of head hv / *_div.
+struct LaJob {
+    const void *q, *k, *v;
+    int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;  // elements between tokens, batch rows
+    int q_div, k_div, v_div;
+    int rev;
+    int W;                // columns of S and o, all of them
+    int trans;            // states in memory are [W][KD] in place of [KD][W]
+    float in_scale, out_scale;
+    void *o;              // [tokens][Hv][W]
+    int o_bf16;
+    const float *init;    // [n_seq][Hv] states, or null: zero
+    float *fin;           // [n_seq][Hv] last states (rev: times e^g of the first token), or null
+    float *border;        // [places][Hv] states at the borders, or null
+    float *border_fin;    // [places][Hv]: the last state at the sequence's first place, or null
+    float *decays;        // [places][Hv] the segments' whole decays (launch_la_states)
+    // dots[cb][hv][token] = sum over the block's 64 columns of o and e (rows like o's), or null
+    const void *e;
+    int64_t e_row, e_batch;
+    int e_div;
+    float *dots;
+};
+
+struct LaParams {
+    LaSeqs s;
+    LaJob job[3];
+    int n_jobs, n_cb;     // jobs and blocks of 64 columns in the grid
+    int split;            // workgroups take a segment each, from the border states
+    int64_t tokens;       // B T
+};
+
+// States at the borders, from a zero state (or init) at each segment's start; la_carry then adds
+// what comes from before.  decays: [places][Hv] a segment's whole decay
+struct LaCarry {
+    LaSeqs s;
+    float *border;
+    const float *decays;
+    int KV, rev;
+};
+
+struct LaGates {
+    LaSeqs s;
+    const float *fwd, *rev;  // states and their gradients at the borders (fwd at place 0: the last state)
+    const float *dht;        // [n_seq][Hv] or null
+    const float *a, *b;      // [n_a | n_b][Hv][tokens] dots
+    int n_a, n_b, KV;
+    int64_t tokens;
+    float *dg;               // [tokens][Hv], or per-head partial sums [places][Hv] (s.g_tok 0)
+};
+
+// fine: fp32 operands of the output in three pieces, not two (bf16 inputs; see gdr_la_scan.hip)
+hipError_t launch_la_scan(Dt dt, int KD, bool fine, const LaParams &p, int items, hipStream_t s);
+// end states of segments only, into the border after (rev: before) each, with their decays
+hipError_t launch_la_states(Dt dt, int KD, const LaParams &p, int items, hipStream_t s);
+hipError_t launch_la_carry(const LaCarry &p, hipStream_t s);
+hipError_t launch_la_gates(const LaGates &p, int items, hipStream_t s);
+// out[token][h][d] = sum over the heads of group h of x[token][H group][W] (fp32)
+hipError_t launch_la_heads(const float *x, void *out, Dt out_dt, int64_t tokens, int H, int group, int W, hipStream_t s);
+// dg[h] = sum over the places of part[place][h]
+hipError_t launch_la_sum_gates(const float *part, float *dg, int64_t places, int H, hipStream_t s);
+
+}  // namespace gdr

@@ -1,0 +1,269 @@
+// Host side of linear attention with a decay for each head (include/gdr.h): argument
+// validation, the split into segments, and the launches.
+#include <algorithm>
+
+#include "gdr_la.hpp"
+
+using namespace gdr;
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+constexpr int64_t UNITS = 256;    // compute units of an MI355X, a workgroup each
+constexpr int BORDER_CHUNKS = 16; // the backward's longest segments (gate gradients start anew at each border)
+
+// Chunks per segment, or 0: no split.  W workgroups per segment of N chunks; a split costs a scan
+// without output of all segments but the last, about half of one with output, and three launches
+// more, about eight chunks' time.
+int64_t split_chunks(int64_t N, int64_t W) {
+    int64_t best = cdiv(W, UNITS) * N, L = 0;
+    for (int64_t S = 2; S <= N && (S - 1) * W < 2 * UNITS; ++S) {
+        const int64_t l = cdiv(N, S), rounds = cdiv(W * S, UNITS), t = rounds * l + rounds * l / 2 + 8;
+        if (t < best) best = t, L = l;
+    }
+    return L;
+}
+
+template <typename Args> int check(const Args *a, int32_t out_dtype) {
+    if (!a || a->B < 0 || a->T < 0 || a->H_q < 1 || a->H_v < 1 || a->H_v % a->H_q != 0) return GDR_EINVAL;
+    const bool varlen = a->cu_seqlens != nullptr;
+    if (varlen && (a->B != 1 || a->n_seq < 0)) return GDR_EINVAL;
+    if (a->dtype != GDR_BF16 && a->dtype != GDR_F32) return GDR_ENOTSUP;
+    if (out_dtype != GDR_BF16 && out_dtype != GDR_F32) return GDR_ENOTSUP;
+    if ((a->K != 64 && a->K != 128) || (a->V != 64 && a->V != 128)) return GDR_ENOTSUP;
+    const int64_t limit = ((int64_t)1 << 31) - 64, n_seq = varlen ? a->n_seq : a->B;
+    if (a->segment_chunks < 0 || a->T >= limit || n_seq >= limit || a->H_v >= 65536) return GDR_EINVAL;
+    if (a->T > 0 && a->B >= cdiv(limit, a->T)) return GDR_EINVAL;
+    const int64_t per16 = a->dtype == GDR_BF16 ? 8 : 4;
+    for (const int64_t st : {a->q_row, a->k_row, a->v_row})
+        if (st < 0 || st % per16 != 0 || st >= 1 << 23) return GDR_EINVAL;  // 64 rows within 32-bit byte offsets
+    if (!varlen)
+        for (const int64_t st : {a->q_batch, a->k_batch, a->v_batch})
+            if (st < 0 || st % per16 != 0) return GDR_EINVAL;
+    if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->initial_state)) return GDR_EINVAL;
+    return GDR_OK;
+}
+
+// Sequences and segments, and where the borders' states lie
+struct Plan {
+    int64_t n_seq, tokens, seg_tokens, places;
+    int group, n_cb_k, n_cb_v;
+    bool split;
+    int seg_chunks;
+    size_t border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, total;
+};
+
+// scans: workgroups of a head and sequence
+template <typename Args> int plan(const Args *a, int64_t scans, bool backward, Plan &p) {
+    const bool varlen = a->cu_seqlens != nullptr;
+    p.n_seq = varlen ? a->n_seq : a->B;
+    p.tokens = p.n_seq > 0 ? a->B * a->T : 0;
+    p.group = (int)(a->H_v / a->H_q);
+    p.n_cb_k = (int)(a->K / 64), p.n_cb_v = (int)(a->V / 64);
+    // packed sequences may all but be one
+    const int64_t nct = cdiv(a->T, CH), W = (varlen ? 1 : std::max<int64_t>(p.n_seq, 1)) * a->H_v * scans;
+    int64_t L = a->segment_chunks ? a->segment_chunks : split_chunks(nct, W);
+    p.split = L > 0 && L < nct;
+    if (backward) L = L > 0 ? std::min<int64_t>(L, BORDER_CHUNKS) : BORDER_CHUNKS;
+    if (!p.split && !backward) L = std::max<int64_t>(nct, 1);
+    p.seg_chunks = (int)L;
+    p.seg_tokens = L * CH;
+    p.places = la_slots(p.tokens, p.n_seq, p.seg_tokens);
+    // 32-bit numbers of workgroups and work-items
+    if (std::max(p.places, p.n_seq) * a->H_v * std::max<int64_t>(scans, 16) >= (int64_t)1 << 23) return GDR_EINVAL;
+    p.border_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v * a->K * a->V));
+    p.decays_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v));
+    return GDR_OK;
+}
+
+int plan_fwd(const gdr_la_fwd_args *a, Plan &p) {
+    int rc = a ? check(a, a->out_dtype) : GDR_EINVAL;
+    if (rc) return rc;
+    rc = plan(a, a->V / 64, false, p);
+    if (rc) return rc;
+    p.off_fwd = 0;
+    p.off_decays_fwd = p.border_bytes;
+    p.total = p.split ? p.border_bytes + p.decays_bytes : 0;
+    return GDR_OK;
+}
+
+int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
+    int rc = a ? check(a, a->grad_dtype) : GDR_EINVAL;
+    if (rc) return rc;
+    rc = plan(a, 2 * (a->K / 64) + a->V / 64, true, p);
+    if (rc) return rc;
+    if (p.group > 1 && p.tokens * a->H_q * a->K >= (int64_t)1 << 34) return GDR_EINVAL;  // work-items of the sums
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        const size_t at = off;
+        off += up(n);
+        return at;
+    };
+    p.off_fwd = take(p.border_bytes), p.off_rev = take(p.border_bytes);
+    p.off_decays_fwd = take(p.decays_bytes), p.off_decays_rev = take(p.decays_bytes);
+    const size_t tokens = (size_t)p.tokens * a->H_v * sizeof(float);
+    p.off_dots = take(tokens * (p.n_cb_k + p.n_cb_v));
+    p.off_dq = take(p.group > 1 ? tokens * a->K : 0), p.off_dk = take(p.group > 1 ? tokens * a->K : 0);
+    p.off_gates = take(p.decays_bytes);
+    p.total = off;
+    return GDR_OK;
+}
+
+Dt type_of(int32_t t) { return t == GDR_BF16 ? Dt::BF16 : Dt::F32; }
+
+template <typename Args> LaSeqs sequences(const Args *a, const Plan &p) {
+    return {a->cu_seqlens, a->g, a->g_per_head ? 0 : a->H_v, a->T, (int)p.n_seq, (int)a->H_v, p.seg_chunks};
+}
+
+// launches bind to the timing stage open on this thread (launch_k): none is
+struct NoStage {
+    NoStage() { stage_events() = {nullptr, nullptr, false}; }
+    ~NoStage() { stage_events() = {nullptr, nullptr, false}; }
+};
+
+}  // namespace
+
+extern "C" {
+
+int gdr_la_fwd_workspace(const gdr_la_fwd_args *a, size_t *bytes) {
+    if (!bytes) return GDR_EINVAL;
+    Plan p;
+    const int rc = plan_fwd(a, p);
+    if (!rc) *bytes = p.total;
+    return rc;
+}
+
+int gdr_la_bwd_workspace(const gdr_la_bwd_args *a, size_t *bytes) {
+    if (!bytes) return GDR_EINVAL;
+    Plan p;
+    const int rc = plan_bwd(a, p);
+    if (!rc) *bytes = p.total;
+    return rc;
+}
+
+int gdr_la_fwd(const gdr_la_fwd_args *a, hipStream_t stream) {
+    Plan pl;
+    const int rc = plan_fwd(a, pl);
+    if (rc) return rc;
+    if (pl.n_seq == 0 || (pl.tokens == 0 && !a->final_state)) return GDR_OK;
+    if (pl.tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->o)) return GDR_EINVAL;
+    if (!aligned16(a->o) || !aligned16(a->final_state) || !aligned16(a->workspace)) return GDR_EINVAL;
+    if (pl.total > 0 && (!a->workspace || a->workspace_bytes < pl.total)) return GDR_EWORKSPACE;
+    const NoStage stage;
+    char *ws = static_cast<char *>(a->workspace);
+    float *border = pl.split ? reinterpret_cast<float *>(ws + pl.off_fwd) : nullptr;
+    LaParams p = {};
+    p.s = sequences(a, pl);
+    p.n_jobs = 1, p.n_cb = pl.n_cb_v, p.split = pl.split, p.tokens = pl.tokens;
+    LaJob &J = p.job[0];
+    J.q = a->q, J.k = a->k, J.v = a->v;
+    J.q_row = a->q_row, J.k_row = a->k_row, J.v_row = a->v_row;
+    J.q_batch = a->q_batch, J.k_batch = a->k_batch, J.v_batch = a->v_batch;
+    J.q_div = J.k_div = pl.group, J.v_div = 1;
+    J.W = (int)a->V, J.in_scale = 1.f, J.out_scale = a->scale;
+    J.o = a->o, J.o_bf16 = a->out_dtype == GDR_BF16;
+    J.init = a->initial_state, J.fin = a->final_state, J.border = border;
+    const Dt dt = type_of(a->dtype);
+    if (pl.split) {
+        J.decays = reinterpret_cast<float *>(ws + pl.off_decays_fwd);
+        if (launch_la_states(dt, (int)a->K, p, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
+        const LaCarry c = {p.s, border, J.decays, (int)(a->K * a->V), 0};
+        if (launch_la_carry(c, stream) != hipSuccess) return GDR_ELAUNCH;
+    }
+    const bool fine = a->out_dtype == GDR_F32;
+    return launch_la_scan(dt, (int)a->K, fine, p, (int)(pl.split ? pl.places : pl.n_seq), stream) == hipSuccess ? GDR_OK : GDR_ELAUNCH;
+}
+
+int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
+    Plan pl;
+    const int rc = plan_bwd(a, pl);
+    if (rc) return rc;
+    if (pl.n_seq == 0 && !a->g_per_head) return GDR_OK;
+    if (!a->dg || !aligned16(a->workspace)) return GDR_EINVAL;
+    if (pl.tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->dout || !a->dq || !a->dk || !a->dv)) return GDR_EINVAL;
+    for (const void *x : {(const void *)a->dout, (const void *)a->dht, (const void *)a->dq, (const void *)a->dk, (const void *)a->dv,
+                          (const void *)a->dh0})
+        if (!aligned16(x)) return GDR_EINVAL;
+    if (pl.total > 0 && (!a->workspace || a->workspace_bytes < pl.total)) return GDR_EWORKSPACE;
+    const NoStage stage;
+    char *ws = static_cast<char *>(a->workspace);
+    auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+    const Dt dt = type_of(a->dtype), gt = type_of(a->grad_dtype);
+    const int K = (int)a->K, V = (int)a->V, H = (int)a->H_v, group = pl.group, items = (int)(pl.split ? pl.places : pl.n_seq);
+    const int64_t do_row = (int64_t)H * V, do_batch = a->T * do_row;
+    float *border_fwd = at(pl.off_fwd), *border_rev = at(pl.off_rev), *decays_fwd = at(pl.off_decays_fwd), *decays_rev = at(pl.off_decays_rev);
+    float *dots_a = at(pl.off_dots), *dots_b = dots_a + (int64_t)pl.n_cb_k * H * pl.tokens;
+    const LaSeqs s = sequences(a, pl);
+
+    // the backward's scans: dq forwards over S^T, dv backwards over dS, dk backwards over dS^T
+    LaJob dq = {}, dv = {}, dk = {};
+    dq.q = a->dout, dq.q_row = do_row, dq.q_batch = do_batch, dq.q_div = 1;
+    dq.k = a->v, dq.k_row = a->v_row, dq.k_batch = a->v_batch, dq.k_div = 1;
+    dq.v = a->k, dq.v_row = a->k_row, dq.v_batch = a->k_batch, dq.v_div = group;
+    dq.e = a->q, dq.e_row = a->q_row, dq.e_batch = a->q_batch, dq.e_div = group, dq.dots = dots_a;
+    dq.W = K, dq.trans = 1, dq.in_scale = 1.f, dq.out_scale = a->scale;
+    dq.init = a->initial_state, dq.border = border_fwd, dq.border_fin = a->dht ? border_fwd : nullptr;
+
+    dv.q = a->k, dv.q_row = a->k_row, dv.q_batch = a->k_batch, dv.q_div = group;
+    dv.k = a->q, dv.k_row = a->q_row, dv.k_batch = a->q_batch, dv.k_div = group;
+    dv.v = a->dout, dv.v_row = do_row, dv.v_batch = do_batch, dv.v_div = 1;
+    dv.e = a->v, dv.e_row = a->v_row, dv.e_batch = a->v_batch, dv.e_div = 1, dv.dots = dots_b;
+    dv.W = V, dv.rev = 1, dv.in_scale = a->scale, dv.out_scale = 1.f;
+    dv.init = a->dht, dv.fin = a->dh0, dv.border = border_rev;
+    dv.o = a->dv, dv.o_bf16 = gt == Dt::BF16;
+
+    dk.q = a->v, dk.q_row = a->v_row, dk.q_batch = a->v_batch, dk.q_div = 1;
+    dk.k = a->dout, dk.k_row = do_row, dk.k_batch = do_batch, dk.k_div = 1;
+    dk.v = a->q, dk.v_row = a->q_row, dk.v_batch = a->q_batch, dk.v_div = group;
+    dk.W = K, dk.rev = 1, dk.trans = 1, dk.in_scale = a->scale, dk.out_scale = 1.f;
+    dk.init = a->dht, dk.border = pl.split ? border_rev : nullptr;
+
+    if (group > 1) {  // per v head, summed afterwards
+        dq.o = at(pl.off_dq), dk.o = at(pl.off_dk);
+    } else {
+        dq.o = a->dq, dk.o = a->dk;
+        dq.o_bf16 = dk.o_bf16 = gt == Dt::BF16;
+    }
+
+    if (pl.n_seq > 0) {
+        if (pl.split) {
+            LaParams p = {};
+            p.s = s, p.n_jobs = 2, p.n_cb = pl.n_cb_v, p.split = 1, p.tokens = pl.tokens;
+            LaJob &f = p.job[0], &r = p.job[1];
+            f.k = a->k, f.k_row = a->k_row, f.k_batch = a->k_batch, f.k_div = group;
+            f.v = a->v, f.v_row = a->v_row, f.v_batch = a->v_batch, f.v_div = 1;
+            f.q_div = f.e_div = 1;
+            f.W = V, f.in_scale = 1.f, f.init = a->initial_state, f.border = border_fwd, f.decays = decays_fwd;
+            r = dv;
+            r.decays = decays_rev;
+            if (launch_la_states(dt, K, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+            LaCarry c = {s, border_fwd, decays_fwd, K * V, 0};
+            if (launch_la_carry(c, stream) != hipSuccess) return GDR_ELAUNCH;
+            c = {s, border_rev, decays_rev, K * V, 1};
+            if (launch_la_carry(c, stream) != hipSuccess) return GDR_ELAUNCH;
+        }
+        LaParams p = {};
+        p.s = s, p.split = pl.split, p.tokens = pl.tokens;
+        p.n_jobs = 2, p.n_cb = pl.n_cb_k;
+        p.job[0] = dq, p.job[1] = dk;
+        if (launch_la_scan(dt, V, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        p.n_jobs = 1, p.n_cb = pl.n_cb_v;
+        p.job[0] = dv;
+        if (launch_la_scan(dt, K, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        if (group > 1 && pl.tokens > 0) {
+            if (launch_la_heads(static_cast<float *>(dq.o), a->dq, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
+            if (launch_la_heads(static_cast<float *>(dk.o), a->dk, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
+        }
+        LaGates g = {s, border_fwd, border_rev, a->dht, dots_a, dots_b, pl.n_cb_k, pl.n_cb_v, K * V, pl.tokens,
+                     a->g_per_head ? at(pl.off_gates) : a->dg};
+        if (launch_la_gates(g, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
+    }
+    if (a->g_per_head && launch_la_sum_gates(at(pl.off_gates), a->dg, pl.n_seq > 0 ? pl.places : 0, H, stream) != hipSuccess)
+        return GDR_ELAUNCH;
+    return GDR_OK;
+}
+
+}  // extern "C"

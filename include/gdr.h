@@ -48,7 +48,7 @@
 extern "C" {
 #endif
 
-#define GDR_ABI_VERSION 8
+#define GDR_ABI_VERSION 9
 #define GDR_CHUNK 64
 #define GDR_FWD_STAGES 3
 #define GDR_BWD_STAGES 4
@@ -252,6 +252,61 @@ typedef struct {
     const void *source;        /* states itself, or memory that does not overlap it */
 } gdr_copy_args;
 
+/* Linear attention with a decay for each head: per (sequence, v head)
+
+       S_t = exp(g_t) S_{t-1} + k_t v_t^T,    o_t = scale * S_t^T q_t,
+
+   the gated delta rule without its correction, with the same states [K,V], heads, gates and
+   packed sequences.  g is per token and v head, or one per v head.  A gate of -104 or less
+   (e^-104 is 0 in fp32), -inf among them, empties the state.  Rows are read in place as in
+   gdr_pool_args.  A value of q, k, v or a state that is not finite (in bf16's range, for bf16
+   inputs' states) may turn the rows of its own 64-token chunk of the head, and what follows in
+   the sequence, into NaN; other sequences and other heads' states do not meet it.
+   B, T and n_seq may be 0. */
+typedef struct {
+    int64_t B, T, H_q, H_v, K, V, n_seq; /* sizes as in gdr_fwd_args; B T below 2^31 - 64 */
+    /* elements between tokens' rows and between batch rows, as in gdr_pool_args */
+    int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;
+    int32_t dtype;          /* element type of q, k, v */
+    int32_t out_dtype;      /* element type of o */
+    int32_t g_per_head;     /* 0: g [B,T,H_v]; else g [H_v] */
+    int32_t segment_chunks; /* chunks of 64 tokens per segment where a long sequence is split; 0 = chosen for
+                               the device, which may be none; a large value: no split */
+    float scale;
+    const void *q, *k, *v;
+    const float *g;
+    const float *initial_state; /* [N,H_v,K,V], N = B or n_seq; NULL = zeros */
+    const int32_t *cu_seqlens;  /* [n_seq+1] token offsets (B = 1), or NULL.  On the device offsets outside
+                                   [0, T] are clamped to it, an end before its start to the start */
+    void *o;                    /* [B,T,H_v,V] out_dtype */
+    float *final_state;         /* [N,H_v,K,V]; NULL = not wanted */
+    void *workspace;
+    size_t workspace_bytes;
+} gdr_la_fwd_args;
+
+typedef struct {
+    int64_t B, T, H_q, H_v, K, V, n_seq;
+    int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;
+    int32_t dtype;          /* element type of q, k, v and dout */
+    int32_t grad_dtype;     /* element type of dq, dk, dv */
+    int32_t g_per_head;
+    int32_t segment_chunks; /* as in gdr_la_fwd_args, at most 16 here (more counts as 16: gate gradients
+                               are summed from one segment's border to the next) */
+    float scale;
+    const void *q, *k, *v;
+    const float *g;
+    const float *initial_state; /* or NULL */
+    const int32_t *cu_seqlens;  /* or NULL */
+    const void *dout;           /* [B,T,H_v,V] gradient of o, dtype */
+    const float *dht;           /* [N,H_v,K,V] gradient of final_state; NULL = zeros */
+    void *dq, *dk;              /* [B,T,H_q,K] grad_dtype, summed over the v heads of each q/k head */
+    void *dv;                   /* [B,T,H_v,V] grad_dtype */
+    float *dg;                  /* like g */
+    float *dh0;                 /* [N,H_v,K,V] gradient of initial_state; NULL = not wanted */
+    void *workspace;
+    size_t workspace_bytes;
+} gdr_la_bwd_args;
+
 /* GDR_ABI_VERSION of the loaded library. */
 int gdr_abi_version(void);
 
@@ -381,6 +436,23 @@ int gdr_tree_accept(const gdr_pool_args *args, hipStream_t stream);
    dst outside [0, n_dst) or src at or past n_src are skipped.  Needs no workspace and
    may be captured. */
 int gdr_copy_states(const gdr_copy_args *args, hipStream_t stream);
+
+/* Workspace bytes of gdr_la_fwd and gdr_la_bwd for these sizes (of the pointers, only whether
+   cu_seqlens is NULL counts).  They return GDR_OK or a validation error. */
+int gdr_la_fwd_workspace(const gdr_la_fwd_args *args, size_t *bytes);
+int gdr_la_bwd_workspace(const gdr_la_bwd_args *args, size_t *bytes);
+
+/* Chunked linear attention on `stream`: o and the final states.  Where there are fewer sequences,
+   heads and column blocks than compute units, long sequences are split into segments: the
+   segments' own end states first, carried over the segments (exactly: a segment's part is a
+   scalar decay), then all segments with their output.  May be captured. */
+int gdr_la_fwd(const gdr_la_fwd_args *args, hipStream_t stream);
+
+/* Its backward on `stream`: gradients of <dout, o> + <dht, final_state>.  Every output is
+   overwritten.  Rows of dq, dk, dv and dg that belong to no sequence are left as they are, as
+   rows of o are by the forward (where v heads share a q/k head, those of dq and dk are
+   undefined).  May be captured. */
+int gdr_la_bwd(const gdr_la_bwd_args *args, hipStream_t stream);
 
 #ifdef __cplusplus
 }
