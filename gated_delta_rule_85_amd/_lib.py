@@ -20,6 +20,7 @@ COPY_MAX = 4096  # GDR_COPY_MAX: entries of one gdr_copy_states
 OK, EINVAL, ENOTSUP, EWORKSPACE, ELAUNCH, ESCRATCH = 0, -1, -2, -3, -4, -5
 SCRATCH_BYTES = 256 << 20  # GDR_SCRATCH_BYTES: gdr_fwd_noalloc's per-device scratch
 BF16, F32 = 0, 1
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
 CP_AUTO, CP_OFF, CP_WARMUP, CP_EXACT, CP_AUTO_EXACT, CP_AUTO_PAGES = 0, 1, 2, 3, 4, 5
 
 _p = ctypes.c_void_p
@@ -65,7 +66,7 @@ class PoolArgs(ctypes.Structure):
         ("q_batch", _i64), ("k_batch", _i64), ("v_batch", _i64),
         ("dtype", _i32), ("out_dtype", _i32), ("scale", ctypes.c_float),
         ("q", _p), ("k", _p), ("v", _p), ("g", _p), ("beta", _p), ("cu_seqlens", _p), ("slots", _p),
-        ("parents", _p), ("accepted", _p), ("states", _p), ("o", _p),
+        ("parents", _p), ("accepted", _p), ("states", _p), ("o", _p), ("g_per_head", _i32),
     ]
 
 
@@ -107,6 +108,27 @@ class LaBwdArgs(ctypes.Structure):
     ]
 
 
+class NormFwdArgs(ctypes.Structure):
+    """Mirror of gdr_norm_fwd_args."""
+    _fields_ = [
+        ("M", _i64), ("C", _i64), ("groups", _i64), ("x_row", _i64), ("gate_row", _i64),
+        ("x_dtype", _i32), ("gate_dtype", _i32), ("out_dtype", _i32), ("activation", _i32), ("center", _i32),
+        ("eps", ctypes.c_float),
+        ("x", _p), ("weight", _p), ("bias", _p), ("gate", _p), ("out", _p),
+    ]
+
+
+class NormBwdArgs(ctypes.Structure):
+    """Mirror of gdr_norm_bwd_args."""
+    _fields_ = [
+        ("M", _i64), ("C", _i64), ("groups", _i64), ("x_row", _i64), ("gate_row", _i64),
+        ("x_dtype", _i32), ("gate_dtype", _i32), ("out_dtype", _i32), ("activation", _i32), ("center", _i32),
+        ("eps", ctypes.c_float),
+        ("x", _p), ("weight", _p), ("bias", _p), ("gate", _p), ("dout", _p),
+        ("dx", _p), ("dgate", _p), ("dweight", _p), ("dbias", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -128,11 +150,14 @@ def _load():
     lib.gdr_fwd_noalloc.argtypes = [ctypes.POINTER(FwdArgs), _p]
     lib.gdr_tblocks_bytes.restype = ctypes.c_int
     lib.gdr_tblocks_bytes.argtypes = [ctypes.POINTER(FwdArgs), ctypes.POINTER(ctypes.c_size_t)]
-    for name, st in (("gdr_step", PoolArgs), ("gdr_tree", PoolArgs), ("gdr_tree_accept", PoolArgs),
-                     ("gdr_copy_states", CopyArgs)):
+    for name, st in (("gdr_step", PoolArgs), ("gdr_la_step", PoolArgs), ("gdr_tree", PoolArgs), ("gdr_tree_accept", PoolArgs),
+                     ("gdr_copy_states", CopyArgs), ("gdr_group_norm", NormFwdArgs),
+                     ("gdr_group_norm_bwd", NormBwdArgs)):
         f = getattr(lib, name)
         f.restype = ctypes.c_int
         f.argtypes = [ctypes.POINTER(st), _p]
+    lib.gdr_group_norm_bwd_workspace.restype = ctypes.c_int
+    lib.gdr_group_norm_bwd_workspace.argtypes = [ctypes.POINTER(NormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]
     if lib.gdr_abi_version() != ABI_VERSION:
         raise ImportError("libgdr ABI version %d, binding expects %d"
                           % (lib.gdr_abi_version(), ABI_VERSION))
@@ -225,3 +250,13 @@ def la_bwd(args, stream):
     rc = lib.gdr_la_bwd(ctypes.byref(args), _p(stream))
     if rc:
         raise GdrError("gdr_la_bwd", rc)
+
+
+def group_norm_bwd_workspace(args):
+    return _sized("gdr_group_norm_bwd_workspace", args)
+
+
+def group_norm_bwd(args, stream):
+    rc = lib.gdr_group_norm_bwd(ctypes.byref(args), _p(stream))
+    if rc:
+        raise GdrError("gdr_group_norm_bwd", rc)

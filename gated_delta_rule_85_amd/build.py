@@ -45,7 +45,8 @@ SOURCES = {"gdr_api.hip": VGPR_FORM, "gdr_prep.hip": VGPR_FORM, "gdr_scan.hip": 
            "gdr_bwd.hip": VGPR_FORM, "gdr_bwd_scan.hip": VGPR_FORM,
            "gdr_bwd_mfma.hip": VGPR_FORM + MAX_ILP, "gdr_noalloc.hip": [],
            "gdr_step.hip": [], "gdr_tree.hip": VGPR_FORM, "gdr_copy.hip": [], "gdr_pool_api.hip": [],
-           "gdr_la_scan.hip": VGPR_FORM, "gdr_la_bwd.hip": [], "gdr_la_api.hip": []}
+           "gdr_la_scan.hip": VGPR_FORM, "gdr_la_bwd.hip": [], "gdr_la_api.hip": [],
+           "gdr_norm.hip": [], "gdr_norm_bwd.hip": [], "gdr_norm_api.hip": []}
 
 
 def _compile(src):

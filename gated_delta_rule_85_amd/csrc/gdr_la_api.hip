@@ -182,7 +182,7 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     const int rc = plan_bwd(a, pl);
     if (rc) return rc;
     if (pl.n_seq == 0 && !a->g_per_head) return GDR_OK;
-    if (!a->dg || !aligned16(a->workspace)) return GDR_EINVAL;
+    if (((pl.tokens > 0 || a->g_per_head) && !a->dg) || !aligned16(a->workspace)) return GDR_EINVAL;
     if (pl.tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->dout || !a->dq || !a->dk || !a->dv)) return GDR_EINVAL;
     for (const void *x : {(const void *)a->dout, (const void *)a->dht, (const void *)a->dq, (const void *)a->dk, (const void *)a->dv,
                           (const void *)a->dh0})

@@ -1,5 +1,5 @@
-// Operators on a pool of recurrent states (gdr_step, gdr_tree, gdr_tree_accept,
-// gdr_copy_states): parameter blocks, launchers and the lookups they share.
+// Operators on a pool of recurrent states (gdr_step, gdr_la_step, gdr_tree,
+// gdr_tree_accept, gdr_copy_states): parameter blocks, launchers and the lookups they share.
 #pragma once
 
 #include "gdr_kernels.hpp"
@@ -22,6 +22,7 @@ struct PoolParams {
     int64_t T;
     int n_seq, n_slots, Hq, Hv;
     float scale;
+    int64_t g_tok;  // floats between the gates of two tokens (launch_la_step): Hv, or 0
 };
 
 struct CopyParams {
@@ -98,6 +99,7 @@ __device__ __forceinline__ void store4_once(float *p, f32x4 x) {
 }
 
 hipError_t launch_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s);
+hipError_t launch_la_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s);
 hipError_t launch_accept(Dt dt, int K, int V, const PoolParams &p, hipStream_t s);
 // most: an upper bound on the nodes of a tree (1 .. TREE_MAX)
 hipError_t launch_tree(Dt dt, Dt out, int K, int V, int most, const PoolParams &p, hipStream_t s);

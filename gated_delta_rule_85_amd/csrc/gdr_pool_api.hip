@@ -10,7 +10,7 @@ namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-enum class Op { STEP, TREE, ACCEPT };
+enum class Op { STEP, TREE, ACCEPT, LA_STEP };
 
 // fills p; `idle`: there is nothing to launch
 int plan(const gdr_pool_args *a, Op op, PoolParams &p, bool &idle) {
@@ -24,7 +24,8 @@ int plan(const gdr_pool_args *a, Op op, PoolParams &p, bool &idle) {
     // 32-bit sequence and head numbers, and one workgroup per (sequence, v head)
     if (a->T >= limit || n_seq >= limit || a->H_v >= limit || n_seq * a->H_v > (int64_t)1 << 22) return GDR_EINVAL;
     if (a->B * a->T >= limit) return GDR_EINVAL;
-    if (op != Op::STEP && !varlen && a->T > GDR_TREE_MAX) return GDR_EINVAL;
+    const bool steps = op == Op::STEP || op == Op::LA_STEP;
+    if (!steps && !varlen && a->T > GDR_TREE_MAX) return GDR_EINVAL;
     if (a->n_slots < 1 || a->n_slots >= limit || (!a->slots && a->n_slots < n_seq)) return GDR_EINVAL;
     if (a->n_slots > 1 && (a->slot_stride % 4 != 0 || a->slot_stride < a->H_v * a->K * a->V)) return GDR_EINVAL;
     const int64_t per16 = a->dtype == GDR_BF16 ? 8 : 4;
@@ -36,15 +37,16 @@ int plan(const gdr_pool_args *a, Op op, PoolParams &p, bool &idle) {
         return GDR_EINVAL;
     idle = n_seq == 0 || a->T == 0;
     if (idle) return GDR_OK;
-    if (!a->k || !a->v || !a->g || !a->beta || !a->states) return GDR_EINVAL;
+    if (!a->k || !a->v || !a->g || (op != Op::LA_STEP && !a->beta) || !a->states) return GDR_EINVAL;
     if (op != Op::ACCEPT && (!a->q || !a->o)) return GDR_EINVAL;
-    if (op != Op::STEP && !a->parents) return GDR_EINVAL;
+    if (!steps && !a->parents) return GDR_EINVAL;
     if (op == Op::ACCEPT && !a->accepted) return GDR_EINVAL;
     if (!aligned16(a->k) || !aligned16(a->v) || !aligned16(a->states)) return GDR_EINVAL;
     if (op != Op::ACCEPT && (!aligned16(a->q) || !aligned16(a->o))) return GDR_EINVAL;
     p = {a->q, a->k, a->v, a->g, a->beta, a->cu_seqlens, a->slots, a->parents, a->accepted, a->states, a->o,
          a->n_slots > 1 ? a->slot_stride : 0, a->q_row, a->k_row, a->v_row, a->q_batch, a->k_batch, a->v_batch,
-         a->T, (int)n_seq, (int)a->n_slots, (int)a->H_q, (int)a->H_v, a->scale};
+         a->T, (int)n_seq, (int)a->n_slots, (int)a->H_q, (int)a->H_v, a->scale,
+         op == Op::LA_STEP && a->g_per_head ? 0 : a->H_v};
     return GDR_OK;
 }
 
@@ -66,6 +68,14 @@ int gdr_step(const gdr_pool_args *a, hipStream_t stream) {
     const int rc = plan(a, Op::STEP, p, idle);
     if (rc || idle) return rc;
     return done(launch_step(type_of(a->dtype), type_of(a->out_dtype), (int)a->K, (int)a->V, p, stream));
+}
+
+int gdr_la_step(const gdr_pool_args *a, hipStream_t stream) {
+    PoolParams p;
+    bool idle = false;
+    const int rc = plan(a, Op::LA_STEP, p, idle);
+    if (rc || idle) return rc;
+    return done(launch_la_step(type_of(a->dtype), type_of(a->out_dtype), (int)a->K, (int)a->V, p, stream));
 }
 
 int gdr_tree(const gdr_pool_args *a, hipStream_t stream) {

@@ -1,11 +1,12 @@
 // gdr_step: the recurrent form of the gated delta rule, a token at a time on a
-// pool of states; gdr_tree_accept: the same over the tokens of an accepted path.
+// pool of states; gdr_tree_accept: the same over the tokens of an accepted path;
+// gdr_la_step: the recurrent form of linear attention, the rule without its correction.
 //
 // Per (sequence, v head), with the state h (K x V, fp32):
 //     u = beta (v - e^g k h),   h <- e^g h + k u^T,   o = scale q h.
 // Columns of h are independent, and both products are taken of the old state:
 // q h_new = e^g q h + (q . k) u, so that one pass over the state's registers and
-// one sum over the lanes serve u and o together.
+// one sum over the lanes serve u and o together.  Without the correction u is v.
 //
 // A wave holds K rows x 32 columns of the state in registers over all of the
 // sequence's tokens: lane l has columns 4 (l & 7) .. + 3 of rows R (l >> 3) ..
@@ -87,9 +88,12 @@ template <typename In, int R> struct Token {
     float g, beta;
 };
 
-template <typename In, typename Out, int K, bool ACCEPT>
+enum class Rule { DELTA, ACCEPT, DECAY };
+
+template <typename In, typename Out, int K, Rule RULE>
 __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     constexpr int R = K / 8;
+    constexpr bool ACCEPT = RULE == Rule::ACCEPT, DECAY = RULE == Rule::DECAY;
     const int unit = xcd_runs(blockIdx.x, gridDim.x), vt = __builtin_amdgcn_readfirstlane(wave_id());
     const int j = unit / p.Hv, hv = unit - j * p.Hv, hq = hv / (p.Hv / p.Hq);
     const int l = lane_id(), col = vt * 32 + 4 * (l & 7), row0 = R * (l >> 3), mine = col + my_column(l);
@@ -132,8 +136,8 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         t.k.load(kp + row_offset(p, j, i, p.k_batch, p.k_row));
         if constexpr (!ACCEPT) t.q.load(qp + row_offset(p, j, i, p.q_batch, p.q_row));
         t.v = vp[row_offset(p, j, i, p.v_batch, p.v_row)];
-        t.g = p.g[i * p.Hv + hv];
-        t.beta = p.beta[i * p.Hv + hv];
+        t.g = p.g[(DECAY ? i * p.g_tok : i * p.Hv) + hv];
+        if constexpr (!DECAY) t.beta = p.beta[i * p.Hv + hv];
     };
     // every rounding is written out (no contraction by the compiler), so that an acceptance
     // and the recurrent form on the same tokens agree to the bit
@@ -145,14 +149,14 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
         for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                kh[c] = __builtin_fmaf(t.k[r], h[r][c], kh[c]);
+                if constexpr (!DECAY) kh[c] = __builtin_fmaf(t.k[r], h[r][c], kh[c]);
                 if constexpr (!ACCEPT) qh[c] = __builtin_fmaf(t.q[r], h[r][c], qh[c]);
             }
             if constexpr (!ACCEPT) qk = __builtin_fmaf(t.q[r], t.k[r], qk);
         }
         // full-precision exponential: its error would otherwise grow with every token
         const float eg = expf(t.g);
-        const float u = t.beta * __builtin_fmaf(-eg, sum_columns(kh), to_f32(t.v));
+        const float u = DECAY ? to_f32(t.v) : t.beta * __builtin_fmaf(-eg, sum_columns(kh), to_f32(t.v));
         const f32x4 us = gather_columns(u);
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -188,7 +192,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(PoolParams p, int V) {
     for (int r = 0; r < R; ++r) store4_once(h0 + r * V, h[r]);
 }
 
-template <typename In, typename Out, bool ACCEPT>
+template <typename In, typename Out, Rule RULE>
 hipError_t launch(int K, int V, const PoolParams &p, hipStream_t s) {
     // a head's waves in one workgroup share its k and q rows in the L1
     const int block = 64 * (V / 32);
@@ -197,24 +201,32 @@ hipError_t launch(int K, int V, const PoolParams &p, hipStream_t s) {
     // flight at which HBM is fastest: 256 sequences of 32 heads take 185 us, 192 with the twelve
     // that the registers leave room for.  With 64 rows sixteen waves are (11.5 us for 4096
     // waves, 14.5 for eight at a time), and an acceptance does not mind.
-    const uint32_t lds = ACCEPT || K == 64 ? 0 : V == 128 ? 54 << 10 : 33 << 10;
+    const uint32_t lds = RULE == Rule::ACCEPT || K == 64 ? 0 : V == 128 ? 54 << 10 : 33 << 10;
     if (K == 128)
-        launch_k(gdr_step_kernel<In, Out, 128, ACCEPT>, grid, dim3(block), lds, s, p, V);
+        launch_k(gdr_step_kernel<In, Out, 128, RULE>, grid, dim3(block), lds, s, p, V);
     else
-        launch_k(gdr_step_kernel<In, Out, 64, ACCEPT>, grid, dim3(block), lds, s, p, V);
+        launch_k(gdr_step_kernel<In, Out, 64, RULE>, grid, dim3(block), lds, s, p, V);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s) {
+template <Rule RULE> static hipError_t launch_rule(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s) {
     if (dt == Dt::BF16)
-        return out == Dt::BF16 ? launch<bf16, bf16, false>(K, V, p, s) : launch<bf16, float, false>(K, V, p, s);
-    return out == Dt::BF16 ? launch<float, bf16, false>(K, V, p, s) : launch<float, float, false>(K, V, p, s);
+        return out == Dt::BF16 ? launch<bf16, bf16, RULE>(K, V, p, s) : launch<bf16, float, RULE>(K, V, p, s);
+    return out == Dt::BF16 ? launch<float, bf16, RULE>(K, V, p, s) : launch<float, float, RULE>(K, V, p, s);
+}
+
+hipError_t launch_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s) {
+    return launch_rule<Rule::DELTA>(dt, out, K, V, p, s);
+}
+
+hipError_t launch_la_step(Dt dt, Dt out, int K, int V, const PoolParams &p, hipStream_t s) {
+    return launch_rule<Rule::DECAY>(dt, out, K, V, p, s);
 }
 
 hipError_t launch_accept(Dt dt, int K, int V, const PoolParams &p, hipStream_t s) {
-    return dt == Dt::BF16 ? launch<bf16, float, true>(K, V, p, s) : launch<float, float, true>(K, V, p, s);
+    return dt == Dt::BF16 ? launch<bf16, float, Rule::ACCEPT>(K, V, p, s) : launch<float, float, Rule::ACCEPT>(K, V, p, s);
 }
 
 }  // namespace gdr

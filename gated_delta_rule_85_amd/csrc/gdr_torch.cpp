@@ -1,5 +1,5 @@
-// Python binding of the operators on a pool of states: the argument checks of
-// pool.py's functions and the calls of libgdr.
+// Python binding of the operators on a pool of states and of the group norm: the
+// argument checks of pool.py's and norm.py's functions and the calls of libgdr.
 //
 // A decode step calls these once per layer and token, on kernels of 5 us.  A call takes the
 // host 4.3 us here, 2.4 of them the launch; with the same checks in Python it took 9.6.  The
@@ -21,6 +21,13 @@
 #include <vector>
 
 #include "gdr.h"
+
+// An older library lacks these: connect() then says which version it has, not the loader which
+// symbol is missing.
+extern "C" {
+__attribute__((weak)) int gdr_la_step(const gdr_pool_args *, hipStream_t);
+__attribute__((weak)) int gdr_group_norm(const gdr_norm_fwd_args *, hipStream_t);
+}
 
 namespace {
 
@@ -142,7 +149,7 @@ struct NoGradient {
     void check(const at::Tensor &t) const {
         if (!t.unsafeGetTensorImpl()->autograd_meta()) return;  // as on most tensors: neither of them
         NEED(!backward || !t.requires_grad(), "the operators on a pool of states have no gradient: use "
-                                              "chunk_gated_delta_rule, or torch.no_grad()");
+                                              "chunk_gated_delta_rule or chunk_linear_attention, or torch.no_grad()");
         NEED(!forward || !t._fw_grad(0).defined(),
              "the operators on a pool of states have no gradient, and no tangent in forward mode");
     }
@@ -185,7 +192,7 @@ bool launch(int (*entry)(const Args *, hipStream_t), const char *name, const Arg
     return true;
 }
 
-enum class Op { STEP, TREE, ACCEPT };
+enum class Op { STEP, TREE, ACCEPT, LA_STEP };
 
 struct Call {
     const at::Tensor *q, *k, *v, *g, *beta, *parents, *accepted, *states, *cu, *slots, *out;
@@ -202,8 +209,11 @@ bool run(Op op, const Call &x, at::Tensor &o) {
     const int dtype = element(k.scalar_type());
     NEED(dtype >= 0 && v.scalar_type() == k.scalar_type() && (!x.q || x.q->scalar_type() == k.scalar_type()),
          "q, k, v must share one dtype, bfloat16 or float32");
+    const bool steps = op == Op::STEP || op == Op::LA_STEP, g_per_head = op == Op::LA_STEP && x.g->dim() == 1;
     for (const at::Tensor *t : {x.g, x.beta})
-        NEED(t->dim() == 3 && t->size(0) == B && t->size(1) == T && t->size(2) == H_v, "g and beta must be [B,T,H_v]");
+        NEED(!t || (t == x.g && g_per_head && t->size(0) == H_v) ||
+                 (t->dim() == 3 && t->size(0) == B && t->size(1) == T && t->size(2) == H_v),
+             op == Op::LA_STEP ? "g must be [B,T,H_v] or [H_v]" : "g and beta must be [B,T,H_v]");
     int64_t n_seq = B;
     if (x.cu) {
         NEED(B == 1 && x.cu->scalar_type() == at::kInt && x.cu->dim() == 1 && x.cu->numel() >= 1,
@@ -211,7 +221,7 @@ bool run(Op op, const Call &x, at::Tensor &o) {
         if (!x.cu->is_cuda()) check_offsets(*x.cu, T);
         n_seq = x.cu->numel() - 1;
     }
-    if (op != Op::STEP) check_parents(*x.parents, B, T, x.cu);
+    if (!steps) check_parents(*x.parents, B, T, x.cu);
     NEED(states.scalar_type() == at::kFloat && states.dim() == 4 && states.size(1) == H_v && states.size(2) == K &&
              states.size(3) == V,
          "states must be float32 [n_slots,H_v,K,V]");
@@ -239,7 +249,7 @@ bool run(Op op, const Call &x, at::Tensor &o) {
             NEED(o.sizes() == v.sizes() && element(o.scalar_type()) >= 0 && o.is_contiguous() && aligned(o),
                  "out must be contiguous [B,T,H_v,V], bfloat16 or float32, 16-byte aligned");
             NEED(o.device() == dev, "all tensors must be on one GPU");
-            for (const at::Tensor *t : floating) NEED(!overlap(o, *t), "out overlaps an input");
+            for (const at::Tensor *t : floating) NEED(!t || !overlap(o, *t), "out overlaps an input");
         } else {
             NEED(THPDtype_Check(x.output_dtype) &&
                      element(reinterpret_cast<THPDtype *>(x.output_dtype)->scalar_type) >= 0,
@@ -263,14 +273,15 @@ bool run(Op op, const Call &x, at::Tensor &o) {
     a.v = vr.data, a.v_row = vr.row, a.v_batch = vr.batch;
     a.dtype = dtype;
     a.out_dtype = o.defined() ? element(o.scalar_type()) : GDR_F32;
-    a.g = floats(*x.g, held), a.beta = floats(*x.beta, held);
+    a.g = floats(*x.g, held), a.beta = x.beta ? floats(*x.beta, held) : nullptr, a.g_per_head = g_per_head;
     a.cu_seqlens = indices(x.cu, dev, held), a.slots = indices(x.slots, dev, held);
-    if (op != Op::STEP) a.parents = indices(x.parents, dev, held);
+    if (!steps) a.parents = indices(x.parents, dev, held);
     if (op == Op::ACCEPT) a.accepted = indices(x.accepted, dev, held);
     a.states = static_cast<float *>(states.data_ptr());
     a.o = o.defined() ? o.data_ptr() : nullptr;
     if (op == Op::TREE) return launch(gdr_tree, "gdr_tree", a, dev, {x.out});
     if (op == Op::ACCEPT) return launch(gdr_tree_accept, "gdr_tree_accept", a, dev, {&states});
+    if (op == Op::LA_STEP) return launch(gdr_la_step, "gdr_la_step", a, dev, {&states, x.out});
     return launch(gdr_step, "gdr_step", a, dev, {&states, x.out});
 }
 
@@ -288,6 +299,18 @@ PyObject *step(PyObject *, PyObject *const *a, Py_ssize_t n) {
                     optional_tensor(a[8], "slots"), optional_tensor(a[10], "out"), a[6], a[9]};
     at::Tensor o;
     return run(Op::STEP, x, o) ? THPVariable_Wrap(o) : nullptr;
+    END_HANDLE_TH_ERRORS
+}
+
+// la_step(q, k, v, g, states, scale, cu_seqlens, slots, output_dtype, out)
+PyObject *la_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 10)) return nullptr;
+    const Call x = {&tensor(a[0], "q"), &tensor(a[1], "k"), &tensor(a[2], "v"), &tensor(a[3], "g"), nullptr, nullptr, nullptr,
+                    &tensor(a[4], "states"), optional_tensor(a[6], "cu_seqlens"), optional_tensor(a[7], "slots"),
+                    optional_tensor(a[9], "out"), a[5], a[8]};
+    at::Tensor o;
+    return run(Op::LA_STEP, x, o) ? THPVariable_Wrap(o) : nullptr;
     END_HANDLE_TH_ERRORS
 }
 
@@ -392,6 +415,76 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
+// x [..., C] as rows of C, with the elements between them; copied where it is no such rows
+struct Matrix {
+    const void *data;
+    int64_t row;
+};
+Matrix matrix(const at::Tensor &x, int64_t M, int64_t C, Held &held) {
+    if (M > 0 && x.stride(-1) != 1 && C > 1) return {held.keep(x.contiguous()).data_ptr(), C};
+    // rows a fixed distance apart, over all dimensions but the last
+    int64_t row = 0, next = 0;  // the stride that the next dimension outwards has to have
+    for (int64_t d = x.dim() - 2; d >= 0; --d) {
+        if (x.size(d) == 1) continue;
+        if (next == 0)
+            row = x.stride(d);
+        else if (x.stride(d) != next)
+            return {held.keep(x.contiguous()).data_ptr(), C};
+        next = x.stride(d) * x.size(d);
+        if (next == 0 && d > 0) return {held.keep(x.contiguous()).data_ptr(), C};  // an expanded row
+    }
+    return {x.data_ptr(), row};
+}
+
+// norm(x, groups, weight, bias, gate, eps, activation, center, output_dtype)
+PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 9)) return nullptr;
+    const at::Tensor &x = tensor(a[0], "x"), *weight = optional_tensor(a[2], "weight"), *bias = optional_tensor(a[3], "bias"),
+                     *gate = optional_tensor(a[4], "gate");
+    gdr_norm_fwd_args p = {};
+    p.groups = PyLong_AsLongLong(a[1]);
+    if (p.groups == -1 && PyErr_Occurred()) return nullptr;
+    p.eps = (float)PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    p.activation = (int32_t)PyLong_AsLong(a[6]);
+    p.center = PyObject_IsTrue(a[7]);
+    if (PyErr_Occurred()) return nullptr;
+    NEED(x.dim() >= 1 && element(x.scalar_type()) >= 0, "x must be [..., C], bfloat16 or float32");
+    p.C = x.size(-1);
+    NEED(p.groups >= 1 && p.C >= 1 && p.C % p.groups == 0, "the channels of x must be a multiple of num_groups");
+    p.M = x.numel() / p.C;
+    for (const at::Tensor *t : {weight, bias})
+        NEED(!t || (t->dim() == 1 && t->size(0) == p.C && t->is_floating_point()), "weight and bias must be [C]");
+    NEED(!gate || (gate->sizes() == x.sizes() && element(gate->scalar_type()) >= 0),
+         "gate must be like x, bfloat16 or float32");
+    const at::ScalarType type = a[8] == Py_None               ? (gate ? gate : &x)->scalar_type()
+                                : THPDtype_Check(a[8]) ? reinterpret_cast<THPDtype *>(a[8])->scalar_type
+                                                       : at::ScalarType::Undefined;
+    NEED(element(type) >= 0, "output_dtype must be bfloat16 or float32");
+    const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    const at::Device dev = x.device();
+    NEED(dev.is_cuda(), "inputs must be on the GPU");
+    for (const at::Tensor *t : {&x, weight, bias, gate}) {
+        if (!t) continue;
+        NEED(t->device() == dev, "all tensors must be on one GPU");
+        NEED(!forward || !t->unsafeGetTensorImpl()->autograd_meta() || !t->_fw_grad(0).defined(),
+             "group_norm has no tangent in forward mode");
+    }
+    const c10::DeviceGuard guard(dev);
+    at::Tensor out = at::empty(x.sizes(), x.options().dtype(type));
+    Held held;
+    const Matrix xm = matrix(x, p.M, p.C, held), zm = gate ? matrix(*gate, p.M, p.C, held) : Matrix{nullptr, 0};
+    p.x = xm.data, p.x_row = xm.row, p.gate = zm.data, p.gate_row = zm.row;
+    p.x_dtype = element(x.scalar_type()), p.out_dtype = element(type);
+    p.gate_dtype = gate ? element(gate->scalar_type()) : p.x_dtype;
+    p.weight = weight ? floats(*weight, held) : nullptr, p.bias = bias ? floats(*bias, held) : nullptr;
+    p.out = out.data_ptr();
+    if (!launch(gdr_group_norm, "gdr_group_norm", p, dev, {})) return nullptr;
+    return THPVariable_Wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
 // connect(GdrError, function from a device's index to its current stream's handle)
 PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count(n, 2)) return nullptr;
@@ -408,8 +501,10 @@ PyObject *connect(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 PyMethodDef methods[] = {{"connect", (PyCFunction)(void (*)(void))connect, METH_FASTCALL, nullptr},
                          {"step", (PyCFunction)(void (*)(void))step, METH_FASTCALL, nullptr},
+                         {"la_step", (PyCFunction)(void (*)(void))la_step, METH_FASTCALL, nullptr},
                          {"tree", (PyCFunction)(void (*)(void))tree, METH_FASTCALL, nullptr},
                          {"accept", (PyCFunction)(void (*)(void))accept, METH_FASTCALL, nullptr},
+                         {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, nullptr},
                          {"copy", (PyCFunction)(void (*)(void))copy, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdr_torch", "Checked calls of libgdr's operators on a pool of states.", -1,

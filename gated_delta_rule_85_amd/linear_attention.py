@@ -12,6 +12,7 @@ each v head, [H_v].  The recurrent form on a pool of states is
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from .api import _DT, _c, _ptr, check_offsets
@@ -185,7 +186,8 @@ def chunk_linear_attention(q, k, v, g, scale=None, initial_state=None, output_fi
     arguments are those of :func:`chunk_gated_delta_rule` without beta, and
     :func:`chunk_linear_attention_fwd` says more of them.  All five inputs have gradients
     (:func:`chunk_linear_attention_bwd`)."""
-    if torch.is_grad_enabled() and any(x is not None and x.requires_grad for x in (q, k, v, g, initial_state)):
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and any(
+            x is not None and x.requires_grad for x in (q, k, v, g, initial_state)):  # (forward mode is refused there)
         return _ChunkLA.apply(q, k, v, g, scale, initial_state, output_final_state, cu_seqlens, output_dtype)
     return chunk_linear_attention_fwd(q, k, v, g, scale, initial_state, cu_seqlens, output_final_state,
                                       output_dtype=output_dtype)

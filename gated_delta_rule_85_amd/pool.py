@@ -1,4 +1,4 @@
-"""Serving operators of the gated delta rule on a pool of recurrent states.
+"""Serving operators of the gated delta rule and of linear attention on a pool of recurrent states.
 
 A serving program keeps one K x V state (fp32) per (sequence, v head) in a pool
 ``states [n_slots, H_v, K, V]``, the layout of the chunked operator's initial and
@@ -9,6 +9,8 @@ final states, and names a sequence's state by its slot:
 - :func:`tree_gated_delta_rule` evaluates trees of drafted tokens against the
   states, which stay as they are, and :func:`tree_gated_delta_rule_accept` takes the
   accepted path into them;
+- :func:`recurrent_linear_attention` is the first of these for linear attention with a
+  decay for each head;
 - :func:`copy_states` copies, forks, moves and clears states.
 
 They are inference operators: no gradients (the chunked operator has them), no
@@ -66,6 +68,18 @@ def recurrent_gated_delta_rule(q, k, v, g, beta, states, scale=None, cu_seqlens=
     contiguous tensor to write; rows that belong to no sequence are left as they are.
     """
     return _gdr_torch.step(q, k, v, g, beta, states, scale, cu_seqlens, slots, output_dtype, out)
+
+
+def recurrent_linear_attention(q, k, v, g, states, scale=None, cu_seqlens=None, *, slots=None,
+                               output_dtype=torch.float32, out=None):
+    """The recurrent form of :func:`chunk_linear_attention`: every sequence's tokens are taken
+    into its state, in place.  Returns ``o`` [B,T,H_v,V].
+
+    g is [B,T,H_v] or, fixed for each v head, [H_v]; there is no beta.  The other arguments,
+    and what happens to sequences without a slot, are those of
+    :func:`recurrent_gated_delta_rule`.
+    """
+    return _gdr_torch.la_step(q, k, v, g, states, scale, cu_seqlens, slots, output_dtype, out)
 
 
 def tree_gated_delta_rule(q, k, v, g, beta, parents, states, scale=None, cu_seqlens=None, *, slots=None,

@@ -201,7 +201,7 @@ typedef struct {
 } gdr_bwd_args;
 
 /* A pool of recurrent states and the tokens that meet it (gdr_step, gdr_tree,
-   gdr_tree_accept).  The pool holds one state h = S^T (K x V, fp32) per (slot, v
+   gdr_tree_accept, gdr_la_step).  The pool holds one state h = S^T (K x V, fp32) per (slot, v
    head); slots[j] is the slot of sequence j.  Index arrays are device data that
    the host cannot check without a synchronisation: an entry of slots outside
    [0, n_slots) means that the sequence has no state (it is skipped, and its rows
@@ -225,7 +225,7 @@ typedef struct {
     float scale;
     const void *q;             /* H_q x K per token; not read by gdr_tree_accept */
     const void *k, *v;         /* H_q x K and H_v x V per token */
-    const float *g, *beta;     /* [B,T,H_v] */
+    const float *g, *beta;     /* [B,T,H_v]; beta is not read by gdr_la_step */
     const int32_t *cu_seqlens; /* [n_seq+1] token offsets (B = 1), or NULL */
     const int32_t *slots;      /* [n_seq]; NULL: sequence j has slot j (n_slots >= n_seq) */
     const int32_t *parents;    /* [B,T]: a node's parent, counted from its tree's first node; -1, and
@@ -235,6 +235,7 @@ typedef struct {
                                   -1, or any entry that is no node, accepts nothing */
     float *states;             /* [n_slots][H_v,K,V], slot_stride apart; gdr_tree only reads it */
     void *o;                   /* [B,T,H_v,V] out_dtype; not written by gdr_tree_accept */
+    int32_t g_per_head;        /* gdr_la_step only: nonzero where g is [H_v] */
 } gdr_pool_args;
 
 /* Copies of states between slots (gdr_copy_states); bytes throughout. */
@@ -306,6 +307,52 @@ typedef struct {
     void *workspace;
     size_t workspace_bytes;
 } gdr_la_bwd_args;
+
+/* activations of gdr_group_norm: none, z sigmoid(z), sigmoid(z) */
+#define GDR_ACT_NONE 0
+#define GDR_ACT_SILU 1
+#define GDR_ACT_SIGMOID 2
+
+/* Group norm of every token's channels, channels last: a token's C channels are `groups` groups
+   of C / groups (at most 8192), each normalised by itself,
+
+       n = (x - mean) / sqrt(mean((x - mean)^2) + eps),   or   x / sqrt(mean(x^2) + eps)
+       y = n * weight + bias,   out = y * act(gate),   or   act(y) without a gate.
+
+   With one group per head it is the norm on the operators' output.  Rows of out, dout, dx and
+   dgate are contiguous; base pointers at multiples of 16 bytes and rows at multiples of 8 elements
+   are read and written in pieces of 16 bytes where the group width is a multiple of 8, others
+   channel by channel.  out may be x or gate where their types and rows are alike. */
+typedef struct {
+    int64_t M, C, groups;
+    int64_t x_row, gate_row; /* elements between tokens */
+    int32_t x_dtype, gate_dtype, out_dtype;
+    int32_t activation;      /* GDR_ACT_* */
+    int32_t center;          /* nonzero: the mean is subtracted */
+    float eps;
+    const void *x;
+    const float *weight, *bias; /* [C] each, or NULL */
+    const void *gate;           /* or NULL */
+    void *out;                  /* [M,C] out_dtype */
+} gdr_norm_fwd_args;
+
+typedef struct {
+    int64_t M, C, groups;
+    int64_t x_row, gate_row;
+    int32_t x_dtype, gate_dtype;
+    int32_t out_dtype;       /* element type of dout */
+    int32_t activation, center;
+    float eps;
+    const void *x;
+    const float *weight, *bias;
+    const void *gate;
+    const void *dout;        /* [M,C] out_dtype */
+    void *dx;                /* [M,C] x_dtype */
+    void *dgate;             /* [M,C] gate_dtype; not written without a gate */
+    float *dweight, *dbias;  /* [C]; NULL = not wanted */
+    void *workspace;
+    size_t workspace_bytes;
+} gdr_norm_bwd_args;
 
 /* GDR_ABI_VERSION of the loaded library. */
 int gdr_abi_version(void);
@@ -410,6 +457,10 @@ int gdr_bwd(const gdr_bwd_args *args, hipStream_t stream);
    Needs no workspace and may be captured. */
 int gdr_step(const gdr_pool_args *args, hipStream_t stream);
 
+/* The recurrent form of linear attention (see gdr_la_fwd_args) on `stream`: as gdr_step, of
+   S_t = exp(g_t) S_{t-1} + k_t v_t^T. */
+int gdr_la_step(const gdr_pool_args *args, hipStream_t stream);
+
 /* Trees of drafted tokens on `stream`: o of every node as if the recurrence had
    been run from the sequence's state over the node's ancestors and the node; the
    states are left as they are (sequences may share a slot).  A sequence is one tree
@@ -453,6 +504,14 @@ int gdr_la_fwd(const gdr_la_fwd_args *args, hipStream_t stream);
    rows of o are by the forward (where v heads share a q/k head, those of dq and dk are
    undefined).  May be captured. */
 int gdr_la_bwd(const gdr_la_bwd_args *args, hipStream_t stream);
+
+/* Group norm with its activation on `stream`.  Needs no workspace and may be captured. */
+int gdr_group_norm(const gdr_norm_fwd_args *args, hipStream_t stream);
+
+/* Its backward on `stream`, and the workspace it needs (for the sums of dweight and dbias over the
+   tokens; of the pointers none is read).  May be captured. */
+int gdr_group_norm_bwd_workspace(const gdr_norm_bwd_args *args, size_t *bytes);
+int gdr_group_norm_bwd(const gdr_norm_bwd_args *args, hipStream_t stream);
 
 #ifdef __cplusplus
 }
