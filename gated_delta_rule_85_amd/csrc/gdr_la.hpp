@@ -67,7 +67,6 @@ struct LaJob {
     int trans;            // states in memory are [W][KD] in place of [KD][W]
     float in_scale, out_scale;
     void *o;              // [tokens][Hv][W]
-    int o_bf16;
     const float *init;    // [n_seq][Hv] states, or null: zero
     float *fin;           // [n_seq][Hv] last states (rev: times e^g of the first token), or null
     float *border;        // [places][Hv] states at the borders, or null
@@ -107,8 +106,8 @@ struct LaGates {
     float *dg;               // [tokens][Hv], or per-head partial sums [places][Hv] (s.g_tok 0)
 };
 
-// fine: fp32 operands of the output in three pieces, not two (bf16 inputs; see gdr_la_scan.hip)
-hipError_t launch_la_scan(Dt dt, int KD, bool fine, const LaParams &p, int items, hipStream_t s);
+// out: type of the jobs' o; dots: whether they sum dots
+hipError_t launch_la_scan(Dt dt, Dt out, int KD, bool dots, const LaParams &p, int items, hipStream_t s);
 // end states of segments only, into the border after (rev: before) each, with their decays
 hipError_t launch_la_states(Dt dt, int KD, const LaParams &p, int items, hipStream_t s);
 hipError_t launch_la_carry(const LaCarry &p, hipStream_t s);

@@ -50,7 +50,7 @@ template <typename Args> int check(const Args *a, int32_t out_dtype) {
 // Sequences and segments, and where the borders' states lie
 struct Plan {
     int64_t n_seq, tokens, seg_tokens, places;
-    int group, n_cb_k, n_cb_v;
+    int group, n_cb_k, n_cb_v;  // blocks of columns, where K or V columns are scanned
     bool split;
     int seg_chunks;
     size_t border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, total;
@@ -62,7 +62,6 @@ template <typename Args> int plan(const Args *a, int64_t scans, bool backward, P
     p.n_seq = varlen ? a->n_seq : a->B;
     p.tokens = p.n_seq > 0 ? a->B * a->T : 0;
     p.group = (int)(a->H_v / a->H_q);
-    p.n_cb_k = (int)(a->K / 64), p.n_cb_v = (int)(a->V / 64);
     // packed sequences may all but be one
     const int64_t nct = cdiv(a->T, CH), W = (varlen ? 1 : std::max<int64_t>(p.n_seq, 1)) * a->H_v * scans;
     int64_t L = a->segment_chunks ? a->segment_chunks : split_chunks(nct, W);
@@ -74,6 +73,9 @@ template <typename Args> int plan(const Args *a, int64_t scans, bool backward, P
     p.places = la_slots(p.tokens, p.n_seq, p.seg_tokens);
     // 32-bit numbers of workgroups and work-items
     if (std::max(p.places, p.n_seq) * a->H_v * std::max<int64_t>(scans, 16) >= (int64_t)1 << 23) return GDR_EINVAL;
+    // 128 columns a workgroup where that leaves one for every compute unit (gdr_la_scan.hip)
+    const bool wide = (p.split ? p.places : p.n_seq) * a->H_v >= UNITS;
+    p.n_cb_k = a->K == 128 && !wide ? 2 : 1, p.n_cb_v = a->V == 128 && !wide ? 2 : 1;
     p.border_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v * a->K * a->V));
     p.decays_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v));
     return GDR_OK;
@@ -164,17 +166,19 @@ int gdr_la_fwd(const gdr_la_fwd_args *a, hipStream_t stream) {
     J.q_batch = a->q_batch, J.k_batch = a->k_batch, J.v_batch = a->v_batch;
     J.q_div = J.k_div = pl.group, J.v_div = 1;
     J.W = (int)a->V, J.in_scale = 1.f, J.out_scale = a->scale;
-    J.o = a->o, J.o_bf16 = a->out_dtype == GDR_BF16;
+    J.o = a->o;
     J.init = a->initial_state, J.fin = a->final_state, J.border = border;
     const Dt dt = type_of(a->dtype);
     if (pl.split) {
         J.decays = reinterpret_cast<float *>(ws + pl.off_decays_fwd);
+        p.n_cb = (int)(a->V / 64);
         if (launch_la_states(dt, (int)a->K, p, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
         const LaCarry c = {p.s, border, J.decays, (int)(a->K * a->V), 0};
         if (launch_la_carry(c, stream) != hipSuccess) return GDR_ELAUNCH;
+        p.n_cb = pl.n_cb_v;
     }
-    const bool fine = a->out_dtype == GDR_F32;
-    return launch_la_scan(dt, (int)a->K, fine, p, (int)(pl.split ? pl.places : pl.n_seq), stream) == hipSuccess ? GDR_OK : GDR_ELAUNCH;
+    const int items = (int)(pl.split ? pl.places : pl.n_seq);
+    return launch_la_scan(dt, type_of(a->out_dtype), (int)a->K, false, p, items, stream) == hipSuccess ? GDR_OK : GDR_ELAUNCH;
 }
 
 int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
@@ -213,7 +217,7 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     dv.e = a->v, dv.e_row = a->v_row, dv.e_batch = a->v_batch, dv.e_div = 1, dv.dots = dots_b;
     dv.W = V, dv.rev = 1, dv.in_scale = a->scale, dv.out_scale = 1.f;
     dv.init = a->dht, dv.fin = a->dh0, dv.border = border_rev;
-    dv.o = a->dv, dv.o_bf16 = gt == Dt::BF16;
+    dv.o = a->dv;
 
     dk.q = a->v, dk.q_row = a->v_row, dk.q_batch = a->v_batch, dk.q_div = 1;
     dk.k = a->dout, dk.k_row = do_row, dk.k_batch = do_batch, dk.k_div = 1;
@@ -221,17 +225,14 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     dk.W = K, dk.rev = 1, dk.trans = 1, dk.in_scale = a->scale, dk.out_scale = 1.f;
     dk.init = a->dht, dk.border = pl.split ? border_rev : nullptr;
 
-    if (group > 1) {  // per v head, summed afterwards
-        dq.o = at(pl.off_dq), dk.o = at(pl.off_dk);
-    } else {
-        dq.o = a->dq, dk.o = a->dk;
-        dq.o_bf16 = dk.o_bf16 = gt == Dt::BF16;
-    }
+    // of several v heads: per head, summed afterwards
+    const Dt qt = group > 1 ? Dt::F32 : gt;
+    dq.o = group > 1 ? at(pl.off_dq) : a->dq, dk.o = group > 1 ? at(pl.off_dk) : a->dk;
 
     if (pl.n_seq > 0) {
         if (pl.split) {
             LaParams p = {};
-            p.s = s, p.n_jobs = 2, p.n_cb = pl.n_cb_v, p.split = 1, p.tokens = pl.tokens;
+            p.s = s, p.n_jobs = 2, p.n_cb = V / 64, p.split = 1, p.tokens = pl.tokens;
             LaJob &f = p.job[0], &r = p.job[1];
             f.k = a->k, f.k_row = a->k_row, f.k_batch = a->k_batch, f.k_div = group;
             f.v = a->v, f.v_row = a->v_row, f.v_batch = a->v_batch, f.v_div = 1;
@@ -247,12 +248,14 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
         }
         LaParams p = {};
         p.s = s, p.split = pl.split, p.tokens = pl.tokens;
-        p.n_jobs = 2, p.n_cb = pl.n_cb_k;
-        p.job[0] = dq, p.job[1] = dk;
-        if (launch_la_scan(dt, V, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
-        p.n_jobs = 1, p.n_cb = pl.n_cb_v;
+        p.n_jobs = 1, p.n_cb = pl.n_cb_k;
+        p.job[0] = dq;
+        if (launch_la_scan(dt, qt, V, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        p.job[0] = dk;
+        if (launch_la_scan(dt, qt, V, false, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        p.n_cb = pl.n_cb_v;
         p.job[0] = dv;
-        if (launch_la_scan(dt, K, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        if (launch_la_scan(dt, gt, K, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
         if (group > 1 && pl.tokens > 0) {
             if (launch_la_heads(static_cast<float *>(dq.o), a->dq, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
             if (launch_la_heads(static_cast<float *>(dk.o), a->dk, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;

@@ -6,13 +6,13 @@
 //     O  = e^{gam_r} Q h + P V,   P = (Q K^T) in_scale e^{gam_r - gam_i} where i <= r,
 //     h' = e^{gam_last} h + K^T diag(in_scale e^{gam_last - gam}) V.
 //
-// One workgroup of eight waves owns 64 columns of S for a whole sequence (or segment) and keeps
-// them in registers: wave w has columns 16 (w & 3) .. + 15 of rows KD/2 (w >> 2) .. .  The two
-// waves of a column block add their halves of Q h through LDS, where the output is staged for
-// rows of whole 128-byte lines.  The ten 16 x 16 tiles of P on and below the diagonal are spread
-// over the waves and shared through LDS.  K, Q and V of the next chunk are copied global -> LDS
-// meanwhile (bf16: two buffers).  Two barriers a chunk: P complete; output staged and the next
-// chunk landed.
+// A workgroup of NW waves owns 16 NW columns of S for a whole sequence (or segment), 16 a wave, in
+// registers; columns are independent, so the waves share only what is made of K and Q alone: the ten
+// 16 x 16 tiles of P on and below the diagonal, through LDS.  A chunk's P V is taken with the next
+// chunk's work, so that one barrier a chunk orders everything: in turn c a wave stores O of chunk
+// c - 1 with its P V, makes its tiles of P of chunk c and its columns of Q h, then h', while K, Q, V
+// and the gates of chunk c + 1 are copied global -> LDS (bf16: two buffers).  NW is 8 (128 columns:
+// half of the tiles of P a column) where that leaves a workgroup for every compute unit, else 4.
 //
 // rev: row r of a chunk is its r-th token from the end, and a row's gate is the next token's, so
 // that the same code scans from the last token to the first.
@@ -27,12 +27,32 @@
 namespace gdr {
 namespace {
 
-constexpr int NT = 512;   // threads
-constexpr int BW = 64;    // columns of a workgroup
 
 // A gate below this empties the state like this one: e^-104 is 0 in fp32.  (Sums of gates stay
 // finite, and -inf may be given.)
 constexpr float LOWEST_GATE = -104.f;
+
+// memory that is not LDS: a pointer out of a parameter block would be taken for either
+template <typename T> using Glb = __attribute__((address_space(1))) T;
+template <typename T> __device__ __forceinline__ Glb<T> *glb(T *p) { return (Glb<T> *)p; }
+
+// Wave-wide copies of 64 x 16 (or 4) bytes global -> LDS, lane l's to 16 l (4 l) past `to`.  As
+// instructions of their own: before any read of LDS the compiler waits for every copy that it knows to
+// be in flight, whichever buffer is read, and with it for the latency of memory in every chunk.
+// Nothing else here uses m0; wait_copies() and a barrier come before what is copied is read.
+__device__ __forceinline__ void copy16(const char *base, uint32_t off, const char *to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(const char *base, uint32_t off, const char *to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 
 // ------------------------------------------------------- operands in pieces
 template <typename In, int NP> struct Pieces {
@@ -74,49 +94,73 @@ template <typename In, int NP> __device__ __forceinline__ Pieces<In, NP> pieces8
     }
     return r;
 }
-// small pieces first
-template <int NP> __device__ __forceinline__ f32x4 mma(f32x4 c, const Pieces<bf16, NP> &a, const OpX &b) {
+// c[i] += a b[i] (a[i] b): a piece of all of them before the next, small pieces first, so that a product
+// does not wait for the one before it
+template <int N, int NP> __device__ __forceinline__ void mma_each(f32x4 *c, const Pieces<bf16, NP> &a, const OpX (&b)[N]) {
 #pragma unroll
-    for (int i = NP - 1; i >= 0; --i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], cat(b.b0, b.b1), c, 0, 0, 0);
-    return c;
-}
-template <int NP> __device__ __forceinline__ f32x4 mma(f32x4 c, const OpX &a, const Pieces<bf16, NP> &b) {
+    for (int k = NP - 1; k >= 0; --k)
 #pragma unroll
-    for (int i = NP - 1; i >= 0; --i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cat(a.b0, a.b1), b.p[i], c, 0, 0, 0);
-    return c;
+        for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[k], cat(b[i].b0, b[i].b1), c[i], 0, 0, 0);
 }
-template <int NP> __device__ __forceinline__ f32x4 mma(f32x4 c, const Pieces<float, NP> &a, const OpF &b) {
-    return mma(c, a.x, b);
+template <int N, int NP> __device__ __forceinline__ void mma_each(f32x4 *c, const OpX (&a)[N], const Pieces<bf16, NP> &b) {
+#pragma unroll
+    for (int k = NP - 1; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cat(a[i].b0, a[i].b1), b.p[k], c[i], 0, 0, 0);
 }
-template <int NP> __device__ __forceinline__ f32x4 mma(f32x4 c, const OpF &a, const Pieces<float, NP> &b) {
-    return mma(c, a, b.x);
+template <int N, int NP> __device__ __forceinline__ void mma_each(f32x4 *c, const Pieces<float, NP> &a, const OpF (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = mma(c[i], a.x, b[i]);
+}
+template <int N, int NP> __device__ __forceinline__ void mma_each(f32x4 *c, const OpF (&a)[N], const Pieces<float, NP> &b) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = mma(c[i], a[i], b.x);
+}
+// c[i] += a b[i], b in pieces
+template <int N, int NP> __device__ __forceinline__ void mma_pieces(f32x4 *c, const OpX &a, const Pieces<bf16, NP> *b) {
+#pragma unroll
+    for (int k = NP - 1; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cat(a.b0, a.b1), b[i].p[k], c[i], 0, 0, 0);
+}
+template <int N, int NP> __device__ __forceinline__ void mma_pieces(f32x4 *c, const OpF &a, const Pieces<float, NP> *b) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = mma(c[i], a, b[i].x);
 }
 
 // ------------------------------------------------------------ LDS layout
-template <typename In, int KD, int NP, bool OUT> struct Lay {
+template <typename In, int KD, int NP, int NW, bool OUT> struct Lay {
     static constexpr bool BF = sizeof(In) == 2;
-    static constexpr int ES = sizeof(In), NB = BF ? 2 : 1;
+    static constexpr int ES = sizeof(In), NB = BF ? 2 : 1, BW = 16 * NW;
     static constexpr int KROW = KD * ES, VROW = BW * ES, PROW = CH * ES;
     static constexpr int KT = CH * KROW, VT = CH * VROW;
     static constexpr int OFF_K = 0, OFF_V = KT, OFF_Q = KT + VT, BUF = KT + VT + (OUT ? KT : 0);
-    static constexpr int PPLANE = CH * PROW, NPL = BF ? NP : 1;
-    static constexpr int OPLANE = CH * BW * 4;
-    static constexpr int OFF_P = NB * BUF, OFF_O = OFF_P + (OUT ? NPL * PPLANE : 0), OFF_G = OFF_O + (OUT ? 2 * OPLANE : 0);
-    static constexpr int GT = 7 * CH;  // floats of a chunk's gate table
-    static constexpr int BYTES = OFF_G + 2 * GT * 4;
+    static constexpr int PPLANE = CH * PROW, PT = (BF ? NP : 1) * PPLANE;  // planes of P
+    static constexpr int OFF_P = NB * BUF;                           // P of two chunks
+    static constexpr int OFF_S = OFF_P + (OUT ? 2 * PT : 0);         // dots of two chunks: [wave][token]
+    static constexpr int OFF_T = OFF_S + (OUT ? 2 * NW * CH * 4 : 0);  // gate tables of two chunks
+    static constexpr int GT = 8 * CH;                                // floats of one
+    static constexpr int OFF_G = OFF_T + 2 * GT * 4;                 // gates of four chunks
+    static constexpr int BYTES = OFF_G + 4 * CH * 4;
     static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
     using SK = Swz<KROW, KeyKQ>;
-    using SV = Swz<VROW, KeyVP>;
+    using SV = Swz<VROW, typename std::conditional<VROW == 128, KeyVP, KeyKQ>::type>;
     using SP = Swz<PROW, typename std::conditional<BF, KeyP, KeyVP>::type>;
-    using SO = Swz<BW * 4>;
 };
-// gate table: running sums within a tile of 16 rows and their exponentials, decays from the
-// chunk's start, to the chunk's end, and to the end of the tile 1, 2 or 3 tiles on
-enum { G_LOC = 0, G_A = CH, G_START = 2 * CH, G_END = 3 * CH, G_TO = 4 * CH };
+// A chunk's table of gates: decays from its start to a row (as the output's factor, too) and from a
+// row to its end; and base-2 logarithms of the decay between a key and a row, as a sum of the row's
+// part (from the start of its tile of 16 rows) and the key's (to the end of its tile and of d - 1
+// tiles more, for a row tile d tiles on; negative of its row's part for the same tile).  The parts
+// are sums over a tile or three, so that their rounding is small against them however strong the
+// decay before.
+enum { G_START = 0, G_OUT = CH, G_END = 2 * CH, G_ROW = 3 * CH, G_KEY = 4 * CH };
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// one row's gate per lane -> the table; rows past n do not decay (their gate is 0) and add nothing
-__device__ __forceinline__ void gate_table(float x, int n, float in_scale, float *t) {
+// one row's gate per lane (0 past the chunk's n rows and before its sequence's first gate) -> the table;
+// rows past n add nothing
+__device__ __forceinline__ void gate_table(float x, int n, float in_scale, float out_scale, float *t) {
     const int l = lane_id(), tile = l >> 4;
+    x = (x < LOWEST_GATE ? LOWEST_GATE : x) * 1.4426950408889634f;  // log2 e
     x += dpp_mov<0x111>(x);  // row_shr 1, 2, 4, 8: running sums within 16 lanes
     x += dpp_mov<0x112>(x);
     x += dpp_mov<0x114>(x);
@@ -128,355 +172,602 @@ __device__ __forceinline__ void gate_table(float x, int n, float in_scale, float
     const float next = tile == 0 ? t1 : tile == 1 ? t2 : t3, next2 = tile == 0 ? t2 : t3;
     const float rest = mine - x;  // to the end of the tile
     const float after = tile == 0 ? t1 + t2 + t3 : tile == 1 ? t2 + t3 : tile == 2 ? t3 : 0.f;
-    t[G_LOC + l] = x;
-    t[G_A + l] = fast_exp(x);
-    t[G_START + l] = fast_exp(before + x);
-    t[G_END + l] = l < n ? in_scale * fast_exp(rest + after) : 0.f;
-    t[G_TO + l] = in_scale * fast_exp(rest);
-    t[G_TO + CH + l] = in_scale * fast_exp(rest + next);
-    t[G_TO + 2 * CH + l] = in_scale * fast_exp(rest + (next + next2));
+    const float start = exp2_fast(before + x);
+    t[G_START + l] = start;
+    t[G_OUT + l] = out_scale * start;
+    t[G_END + l] = l < n ? in_scale * exp2_fast(rest + after) : 0.f;
+    t[G_ROW + l] = x;
+    t[G_KEY + l] = -x;
+    t[G_KEY + CH + l] = rest;
+    t[G_KEY + 2 * CH + l] = rest + next;
+    t[G_KEY + 3 * CH + l] = rest + (next + next2);
 }
 
-__device__ __forceinline__ float sum8(float v) {  // over 8 lanes
-    v += dpp_mov<0xB1>(v);
-    v += dpp_mov<0x4E>(v);
-    v += dpp_mov<0x141>(v);
-    return v;
+// Sums of four values over the lanes with the same l & 15: of value [0, 2, 1, 3][l >> 4]
+__device__ __forceinline__ float sum_rows(f32x4 x) {
+    auto add = [](auto r) {
+        const uint32_t a = r[0], b = r[1];
+        return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+    };
+    auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    const float a = add(__builtin_amdgcn_permlane32_swap(bits(x[0]), bits(x[1]), false, false));
+    const float b = add(__builtin_amdgcn_permlane32_swap(bits(x[2]), bits(x[3]), false, false));
+    return add(__builtin_amdgcn_permlane16_swap(bits(a), bits(b), false, false));
 }
 
-// OUT: with the output; else the end states of segments alone
-template <typename In, int KD, int NP, bool OUT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void gdr_la_scan_kernel(const LaParams p) {
-    using Y = Lay<In, KD, NP, OUT>;
+// ------------------------------------------------------- a workgroup's part
+// Out: void for the end states of segments alone; DOTS: LaJob's sums with e
+template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct Scan {
+    static constexpr bool OUT = !std::is_void<Out>::value;
+    using Y = Lay<In, KD, NP, NW, OUT>;
     using SK = typename Y::SK;
     using SV = typename Y::SV;
     using SP = typename Y::SP;
-    using SO = typename Y::SO;
-    using O = Ops<In>;
-    using X = typename O::X;
-    constexpr int ES = Y::ES, RT = KD / 32, U = KD / 64;  // 16-row tiles of a wave, pairs of them
-    __shared__ __attribute__((aligned(16))) char lds[Y::BYTES];
+    using X = typename Ops<In>::X;
+    static constexpr int ES = Y::ES, BW = Y::BW, RT = KD / 16, U = KD / 32;  // tiles of 16 and of 32 rows of h
 
-    // ---------------------------------------------------------------- work item
-    int id = xcd_remap(blockIdx.x, gridDim.x);
-    const int cb = id % p.n_cb;
-    id /= p.n_cb;
-    const LaJob &J = p.job[id % p.n_jobs];
-    id /= p.n_jobs;
-    const int hv = id % p.s.Hv, item = id / p.s.Hv;
-    int j = item, m = 0;
-    if (p.split && !la_place(p.s, item, j, m)) return;
-    int64_t bos, eos;
-    la_bounds(p.s, j, bos, eos);
-    const int len = (int)(eos - bos), nc = (len + CH - 1) / CH, rev = J.rev;
-    const int first_place = p.s.seg_chunks ? la_first(bos, j, (int64_t)p.s.seg_chunks * CH) : 0;
-    const int n_seg = p.split ? max(1, (nc + p.s.seg_chunks - 1) / p.s.seg_chunks) : 1;
-    const int c_lo = p.split ? m * p.s.seg_chunks : 0, c_hi = p.split ? min(nc, c_lo + p.s.seg_chunks) : nc;
-    const bool starts = m == (rev ? n_seg - 1 : 0), ends = m == (rev ? 0 : n_seg - 1);
-    if (!OUT && ends) return;  // (no border after it)
+    const LaParams &p;
+    const LaJob &J;
+    char *const lds;
+    int cb, hv, j, m, len, nc, n_it, c_first, first_place;
+    int64_t bos;
+    bool rev, starts, ends;
+    int l, n16, g, w;
 
-    const int tid = threadIdx.x, l = lane_id(), n16 = ln16(), g = lg4();
-    const int w = __builtin_amdgcn_readfirstlane(wave_id()), c4 = w & 3, half = w >> 2;
-    const int64_t row0 = p.s.cu ? bos : 0, b0 = p.s.cu ? 0 : j;  // first token's row, batch row
-    const char *kp = reinterpret_cast<const char *>(J.k) + (b0 * J.k_batch + row0 * J.k_row + (int64_t)(hv / J.k_div) * KD) * ES;
-    const char *qp = reinterpret_cast<const char *>(J.q) + (b0 * J.q_batch + row0 * J.q_row + (int64_t)(hv / J.q_div) * KD) * ES;
-    const char *vp = reinterpret_cast<const char *>(J.v) + (b0 * J.v_batch + row0 * J.v_row + (int64_t)(hv / J.v_div) * J.W + cb * BW) * ES;
-    const float *gp = p.s.g + bos * p.s.g_tok + hv;
+    __device__ __forceinline__ Scan(const LaParams &p_, int job, char *lds_) : p(p_), J(p_.job[job]), lds(lds_) {}
 
-    // ------------------------------------------------------------------- states
-    f32x4 h[RT];  // h[t][i]: row slot_base(half RT + t, g) + i, column 16 c4 + n16 of the block
-    const int64_t KV = (int64_t)KD * J.W;
-    const int col = cb * BW + 16 * c4 + n16;
-    auto load_state = [&](const float *s) {
+    // false: nothing to do
+    __device__ __forceinline__ bool place(int item) {
+        j = item, m = 0;
+        if (p.split && !la_place(p.s, item, j, m)) return false;
+        int64_t eos;
+        la_bounds(p.s, j, bos, eos);
+        rev = J.rev;
+        len = (int)(eos - bos), nc = (len + CH - 1) / CH;
+        first_place = la_first(bos, j, (int64_t)p.s.seg_chunks * CH);
+        const int n_seg = p.split ? max(1, (nc + p.s.seg_chunks - 1) / p.s.seg_chunks) : 1;
+        const int c_lo = p.split ? m * p.s.seg_chunks : 0, c_hi = p.split ? min(nc, c_lo + p.s.seg_chunks) : nc;
+        n_it = c_hi - c_lo, c_first = rev ? c_hi - 1 : c_lo;
+        starts = m == (rev ? n_seg - 1 : 0), ends = m == (rev ? 0 : n_seg - 1);
+        l = lane_id(), n16 = ln16(), g = lg4();
+        w = __builtin_amdgcn_readfirstlane(wave_id());
+        return true;
+    }
+    __device__ __forceinline__ int chunk_of(int it) const { return rev ? c_first - it : c_first + it; }
+    __device__ __forceinline__ int rows_of(int c) const { return min(CH, len - c * CH); }
+    // row r of a chunk of n rows -> its token counted from the chunk's first
+    __device__ __forceinline__ int token_of(int r, int n) const { return rev ? n - 1 - r : r; }
+    // element offset of the sequence's first token in a tensor
+    __device__ __forceinline__ int64_t first_row(int64_t row, int64_t batch) const { return p.s.cu ? bos * row : (int64_t)j * batch; }
+
+    // ----------------------------------------------------------------- states
+    // h[t][i]: row slot_base(t, g) + i, column 16 w + n16 of the block
+    __device__ __forceinline__ void load_state(const float *s, f32x4 (&h)[RT]) const {
+        const int col = cb * BW + 16 * w + n16;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const int r = slot_base(half * RT + t, g);
+            const int r = slot_base(t, g);
             if (J.trans) {
-                h[t] = *reinterpret_cast<const f32x4 *>(s + (int64_t)col * KD + r);
+                h[t] = *glb(reinterpret_cast<const f32x4 *>(s + (int64_t)col * KD + r));
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[t][i] = s[(r + i) * J.W + col];
+                for (int i = 0; i < 4; ++i) h[t][i] = glb(s)[(r + i) * J.W + col];
             }
         }
-    };
-    auto store_state = [&](float *s, float f) {
+    }
+    __device__ __forceinline__ void store_state(float *s, const f32x4 (&h)[RT], float f) const {
+        const int col = cb * BW + 16 * w + n16;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const int r = slot_base(half * RT + t, g);
+            const int r = slot_base(t, g);
             if (J.trans) {
-                *reinterpret_cast<f32x4 *>(s + (int64_t)col * KD + r) = f * h[t];
+                *glb(reinterpret_cast<f32x4 *>(s + (int64_t)col * KD + r)) = f * h[t];
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[(r + i) * J.W + col] = f * h[t][i];
+                for (int i = 0; i < 4; ++i) glb(s)[(r + i) * J.W + col] = f * h[t][i];
             }
         }
-    };
-    auto at_place = [&](float *s, int place) { return s + ((int64_t)place * p.s.Hv + hv) * KV; };
-    const int64_t unit = (int64_t)j * p.s.Hv + hv;
-    if (starts ? J.init != nullptr : OUT) {
-        load_state(starts ? J.init + unit * KV : at_place(J.border, first_place + (rev ? m + 1 : m)));
-    } else {
+    }
+    __device__ __forceinline__ float *at_place(float *s, int at) const { return s + ((int64_t)at * p.s.Hv + hv) * KD * J.W; }
+    __device__ __forceinline__ int64_t unit() const { return (int64_t)j * p.s.Hv + hv; }
+    __device__ __forceinline__ void start_state(f32x4 (&h)[RT]) const {
+        if (starts ? J.init != nullptr : OUT) {
+            load_state(starts ? J.init + unit() * KD * J.W : at_place(J.border, first_place + (rev ? m + 1 : m)), h);
+        } else {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) h[t] = zero4();
+            for (int t = 0; t < RT; ++t) h[t] = zero4();
+        }
+    }
+    __device__ __forceinline__ void end_state(const f32x4 (&h)[RT]) const {
+        if (ends && J.fin) {
+            float f = 1.f;
+            if (rev && len > 0) f = fast_exp(p.s.g[bos * p.s.g_tok + hv]);
+            store_state(J.fin + unit() * KD * J.W, h, f);
+        }
+        if (ends && J.border_fin) store_state(at_place(J.border_fin, first_place), h, 1.f);
     }
 
-    // ---------------------------------------------------------- a chunk's copies
-    const int n_it = c_hi - c_lo;
-    auto chunk_of = [&](int it) { return rev ? c_hi - 1 - it : c_lo + it; };
-    auto copy_tile = [&](auto swz, const char *src, int64_t row, int nm1, char *dst, auto bytes) {
-        using S = decltype(swz);
-        constexpr int ROWB = S::CPR * 16, PIECES = decltype(bytes)::value / 1024;
-        static_assert(PIECES % 8 == 0, "pieces spread over the waves");
+    // ----------------------------------------------------------------- copies
+    // Pieces of 1 KB in turn on the waves, and the gates.  The offsets of a lane's rows and 16-byte
+    // columns are the same in every whole chunk; rows past the end of a shorter one repeat its last row.
+    static constexpr int NK = Y::KT / 1024 / NW, NV = Y::VT / 1024 / NW;
+    static_assert(NK * 1024 * NW == Y::KT && NV * 1024 * NW == Y::VT, "pieces spread over the waves");
+    struct Copies {
+        const char *k, *q, *v;    // first row of the chunk to copy next
+        int64_t k_step, q_step, v_step;
+        uint32_t ko[NK], qo[OUT ? NK : 1], vo[NV];
+        int at;                   // that chunk's first token
+    };
+    template <typename S> __device__ __forceinline__ uint32_t copy_offset(int i, uint32_t row, int n) const {
+        constexpr int ROWB = S::CPR * 16;
+        const int b = (NW * i + w) * 1024 + 16 * l, r = b / ROWB, pc = (b % ROWB) / 16;
+        return (uint32_t)token_of(min(r, n - 1), n) * row + 16 * S::chunk(r, pc);
+    }
+    __device__ __forceinline__ Copies copies() const {
+        Copies x;
+        x.at = c_first * CH;
+        auto from = [&](const void *t, int64_t row, int64_t batch, int head, int64_t &step) {
+            step = (rev ? -CH : CH) * row * ES;
+            return reinterpret_cast<const char *>(t) + (first_row(row, batch) + x.at * row + head) * ES;
+        };
+        x.k = from(J.k, J.k_row, J.k_batch, (hv / J.k_div) * KD, x.k_step);
+        x.v = from(J.v, J.v_row, J.v_batch, (hv / J.v_div) * J.W + cb * BW, x.v_step);
+        x.q = OUT ? from(J.q, J.q_row, J.q_batch, (hv / J.q_div) * KD, x.q_step) : nullptr;
 #pragma unroll
-        for (int i = 0; i < PIECES / 8; ++i) {
-            const int piece = 8 * i + w, b = piece * 1024 + 16 * l, r = b / ROWB, pc = (b % ROWB) / 16;
-            const int rr = min(r, nm1), tok = rev ? nm1 - rr : rr;  // rows past the end repeat the last one
-            dma16(src + (uint32_t)(tok * (uint32_t)(row * ES) + 16 * S::chunk(r, pc)), dst + piece * 1024);
+        for (int i = 0; i < NK; ++i) {
+            x.ko[i] = copy_offset<SK>(i, (uint32_t)(J.k_row * ES), CH);
+            if constexpr (OUT) x.qo[i] = copy_offset<SK>(i, (uint32_t)(J.q_row * ES), CH);
         }
-    };
-    auto issue = [&](int c, char *b) {
-        const int64_t t0 = (int64_t)c * CH;
-        const int nm1 = min(CH, len - (int)t0) - 1;
-        copy_tile(SK{}, kp + t0 * J.k_row * ES, J.k_row, nm1, b + Y::OFF_K, std::integral_constant<int, Y::KT>{});
-        copy_tile(SV{}, vp + t0 * J.v_row * ES, J.v_row, nm1, b + Y::OFF_V, std::integral_constant<int, Y::VT>{});
-        if constexpr (OUT)
-            copy_tile(SK{}, qp + t0 * J.q_row * ES, J.q_row, nm1, b + Y::OFF_Q, std::integral_constant<int, Y::KT>{});
-    };
-    // this lane's row's gate
-    auto gate = [&](int c) {
-        const int n = min(CH, len - c * CH), t = c * CH + (rev ? n - l : l);
-        float x = 0.f;
-        if (l < n && t < len) x = gp[(int64_t)t * p.s.g_tok];
-        return x < LOWEST_GATE ? LOWEST_GATE : x;
-    };
-    float *gates = reinterpret_cast<float *>(lds + Y::OFF_G);
-    constexpr int GW = 2;  // the wave that makes the gate tables (it has no score tile)
-    float g_next = 0.f, whole = 1.f;
-
-    // ------------------------------------------------------------------- output
-    typedef typename Vec16<In>::type vec16;
-    constexpr int EVN = 8 / Vec16<In>::n;
-    vec16 ev[EVN];  // this thread's part of e for the chunk that is staged
-    const int orow = tid >> 3, ocol = 8 * (tid & 7);
-    auto row_token = [&](int c) {  // token of the staged row this thread stores, or -1
-        const int n = min(CH, len - c * CH);
-        return orow < n ? c * CH + (rev ? n - 1 - orow : orow) : -1;
-    };
-    auto fetch_e = [&](int c) {
-        const int t = row_token(c);
-        const In *e = reinterpret_cast<const In *>(J.e) + b0 * J.e_batch + row0 * J.e_row + (int64_t)(hv / J.e_div) * J.W +
-                      cb * BW + ocol + (int64_t)max(t, 0) * J.e_row;
 #pragma unroll
-        for (int i = 0; i < EVN; ++i) ev[i] = *reinterpret_cast<const vec16 *>(e + i * Vec16<In>::n);
-    };
-    auto store_out = [&](int c) {
-        const char *o0 = lds + Y::OFF_O, *o1 = o0 + Y::OPLANE;
-        f32x4 y[2];
+        for (int i = 0; i < NV; ++i) x.vo[i] = copy_offset<SV>(i, (uint32_t)(J.v_row * ES), CH);
+        return x;
+    }
+    // the next chunk -> buffer buf
+    __device__ __forceinline__ void issue(Copies &x, int buf) const {
+        char *b = buffer(buf);
+        const int n = min(CH, len - x.at);
+        if (__builtin_expect(n == CH, 1)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int off = SO::off(orow, 4 * (ocol + 4 * i));
-            y[i] = J.out_scale * (*reinterpret_cast<const f32x4 *>(o0 + off) + *reinterpret_cast<const f32x4 *>(o1 + off));
-        }
-        const int t = row_token(c);
-        if (J.dots) {
-            float d = 0.f;
+            for (int i = 0; i < NK; ++i) {
+                copy16(x.k, x.ko[i], b + Y::OFF_K + (NW * i + w) * 1024);
+                if constexpr (OUT) copy16(x.q, x.qo[i], b + Y::OFF_Q + (NW * i + w) * 1024);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d = fmaf(y[i >> 2][i & 3], to_f32(ev[i / Vec16<In>::n][i % Vec16<In>::n]), d);
-            d = sum8(d);
-            if ((tid & 7) == 0 && t >= 0) J.dots[((int64_t)cb * p.s.Hv + hv) * p.tokens + bos + t] = d;
-        }
-        if (t < 0) return;
-        const int64_t off = ((bos + t) * p.s.Hv + hv) * J.W + cb * BW + ocol;
-        if (J.o_bf16) {
-            __builtin_nontemporal_store(cat(narrow(y[0]), narrow(y[1])),
-                                        reinterpret_cast<bf16x8 *>(reinterpret_cast<bf16 *>(J.o) + off));
+            for (int i = 0; i < NV; ++i) copy16(x.v, x.vo[i], b + Y::OFF_V + (NW * i + w) * 1024);
         } else {
-            float *o = reinterpret_cast<float *>(J.o) + off;
-            __builtin_nontemporal_store(y[0], reinterpret_cast<f32x4 *>(o));
-            __builtin_nontemporal_store(y[1], reinterpret_cast<f32x4 *>(o + 4));
+#pragma unroll 1
+            for (int i = 0; i < NK; ++i) {
+                copy16(x.k, copy_offset<SK>(i, (uint32_t)(J.k_row * ES), n), b + Y::OFF_K + (NW * i + w) * 1024);
+                if constexpr (OUT) copy16(x.q, copy_offset<SK>(i, (uint32_t)(J.q_row * ES), n), b + Y::OFF_Q + (NW * i + w) * 1024);
+            }
+#pragma unroll 1
+            for (int i = 0; i < NV; ++i) copy16(x.v, copy_offset<SV>(i, (uint32_t)(J.v_row * ES), n), b + Y::OFF_V + (NW * i + w) * 1024);
         }
-    };
+        x.k += x.k_step, x.v += x.v_step, x.at += rev ? -CH : CH;
+        if constexpr (OUT) x.q += x.q_step;
+    }
+    __device__ __forceinline__ char *buffer(int buf) const { return lds + (Y::NB == 2 ? buf * Y::BUF : 0); }
 
-    // ----------------------------------------------------------------- prologue
-    char *pplane = lds + Y::OFF_P;
-    if (n_it > 0) {
-        issue(chunk_of(0), lds);
-        if (w == GW) {
-            gate_table(gate(chunk_of(0)), min(CH, len - chunk_of(0) * CH), J.in_scale, gates);
-            if (n_it > 1) g_next = gate(chunk_of(1));
+    // Gates: copied two chunks ahead into one of four places, made into a table one chunk ahead.  One
+    // wave does both.
+    __device__ __forceinline__ void issue_gates(int it) const {
+        const int c = chunk_of(it), n = rows_of(c), t = c * CH + min(max(rev ? n - l : l, 0), min(CH, len - c * CH - 1));
+        const char *from = reinterpret_cast<const char *>(p.s.g + (bos + c * (int64_t)CH) * p.s.g_tok + hv);
+        copy4(from, (uint32_t)(t - c * CH) * (uint32_t)(4 * p.s.g_tok), lds + Y::OFF_G + (it & 3) * CH * 4);
+    }
+    __device__ __forceinline__ void make_table(int it) const {
+        const int c = chunk_of(it), n = rows_of(c), t = c * CH + (rev ? n - l : l);
+        const float x = reinterpret_cast<const float *>(lds + Y::OFF_G)[(it & 3) * CH + l];
+        gate_table(l < n && t < len ? x : 0.f, n, J.in_scale, OUT ? J.out_scale : 1.f, table(it & 1));
+    }
+    __device__ __forceinline__ float *table(int buf) const { return reinterpret_cast<float *>(lds + Y::OFF_T) + buf * Y::GT; }
+
+    // --------------------------------------------------------------- products
+    // The reads of LDS that a product needs, and the product, apart: run() reads for one step during
+    // the step before, and stage() keeps the compiler from moving the reads to where they are used.
+    static __device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+
+    // V^T of this wave's columns and keys 32 ip ..
+    __device__ __forceinline__ X values(const char *b, int ip) const { return kt8<In, SV>(b + Y::OFF_V, 32 * ip, 16 * w, 4); }
+    // those, decayed to the chunk's end
+    struct Ends {
+        f32x4 e[2][2];
+    };
+    __device__ __forceinline__ Ends ends_of(const float *gt) const {
+        Ends x;
+#pragma unroll
+        for (int ip = 0; ip < 2; ++ip)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x.e[ip][i] = *reinterpret_cast<const f32x4 *>(gt + G_END + 32 * ip + 8 * g + 4 * i);
+        return x;
+    }
+    __device__ __forceinline__ Pieces<In, 3> decayed(const X &v, const f32x4 (&e)[2]) const {
+        if constexpr (Y::BF)
+            return pieces8<In, 3>(widen(v.b0) * e[0], widen(v.b1) * e[1]);
+        else
+            return pieces8<In, 3>(v.b0 * e[0], v.b1 * e[1]);
+    }
+    // K^T of tiles T .. T + N - 1, keys 32 ip ..
+    static constexpr int N4 = RT < 4 ? RT : 4;
+    struct Keys {
+        X k[N4];
+    };
+    __device__ __forceinline__ Keys keys(const char *b, int ip, int first) const {
+        Keys x;
+#pragma unroll
+        for (int i = 0; i < N4; ++i) {
+            const int t = first + i;
+            x.k[i] = kt8<In, SK>(b + Y::OFF_K, 32 * ip, 32 * (t >> 1) + 4 * (t & 1), 8);
         }
-        if constexpr (OUT) {
-            // the tiles of P right of the diagonal that a 32-deep product reads: zero, never written
-            constexpr int per = 16 * 16 * 2;  // elements of a plane
-            for (int i = tid; i < per * Y::NPL; i += NT) {
-                const int e = i % per, t = e >> 8, r = 32 * t + ((e >> 4) & 15), k = 32 * t + 16 + (e & 15);
-                *reinterpret_cast<In *>(pplane + (i / per) * Y::PPLANE + SP::off(r, k * ES)) = In(0.f);
+        return x;
+    }
+    __device__ __forceinline__ void add_keys(const Keys &k, const Pieces<In, 3> &d, int first, f32x4 (&h)[RT]) const {
+        mma_each<N4>(h + first, k.k, d);
+    }
+    // h to the chunk's end; the first keys have been read
+    __device__ __forceinline__ void add_chunk(const char *b, const float *gt, const X (&v)[2], const Ends &e, Keys k, f32x4 (&h)[RT]) const {
+        const float all = gt[G_START + CH - 1];
+        const Pieces<In, 3> d0 = decayed(v[0], e.e[0]);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) h[t] *= all;
+        Pieces<In, 3> d1;
+#pragma unroll
+        for (int i = 0; i < 2 * RT / N4; ++i) {
+            const int ip = i / (RT / N4), first = i % (RT / N4) * N4, j = i + 1;
+            stage();
+            Keys next;
+            if (j < 2 * RT / N4) next = keys(b, j / (RT / N4), j % (RT / N4) * N4);
+            add_keys(k, ip ? d1 : d0, first, h);
+            if (i == 0) d1 = decayed(v[1], e.e[1]);
+            k = next;
+        }
+        stage();
+    }
+    __device__ __forceinline__ X query(const char *b, int rt, int u) const {
+        return frag8<In, SK>(b + Y::OFF_Q, 16 * rt + n16, (32 * u + 8 * g) * ES);
+    }
+    __device__ __forceinline__ X key(const char *b, int kt, int u) const {
+        return frag8<In, SK>(b + Y::OFF_K, 16 * kt + n16, (32 * u + 8 * g) * ES);
+    }
+    // N tiles of P of one row tile
+    template <int N> struct Scores {
+        X k[N][U], q[U];
+        f32x4 key[N];
+        float row;
+    };
+    template <int N> __device__ __forceinline__ Scores<N> score_operands(const char *b, const float *gt, int rt, int kt) const {
+        Scores<N> x;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x.q[u] = query(b, rt, u);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x.k[i][u] = key(b, kt + i, u);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) x.key[i] = *reinterpret_cast<const f32x4 *>(gt + G_KEY + (rt - kt - i) * CH + 16 * (kt + i) + 4 * g);
+        x.row = gt[G_ROW + 16 * rt + n16];
+        return x;
+    }
+    template <int N> __device__ __forceinline__ void score(const Scores<N> &x, char *P, int rt, int kt) const {
+        f32x4 s[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = zero4();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = mma(s[i], x.k[i][u], x.q[u]);
+        const float scale = J.in_scale * J.out_scale;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {  // s[i][k]: row 16 rt + n16, key 16 (kt + i) + 4g + k
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s[i][k] = rt != kt + i || 4 * g + k <= n16 ? s[i][k] * (scale * exp2_fast(x.row + x.key[i][k])) : 0.f;
+            char *to = P + SP::off(16 * rt + n16, (16 * (kt + i) + 4 * g) * ES);
+            if constexpr (Y::BF) {
+                bf16x4 y[NP];
+                pieces4<NP>(s[i], y);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) *reinterpret_cast<bf16x4 *>(to + k * Y::PPLANE) = y[k];
+            } else {
+                *reinterpret_cast<f32x4 *>(to) = s[i];
             }
         }
-        wait_dma();
+    }
+    // P of row tile r, keys 32 ip ..
+    struct Weights {
+        Pieces<In, NP> p[6];
+    };
+    __device__ __forceinline__ Weights weights(const char *P) const {
+        Weights x;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const int r = i < 4 ? i : i - 2, ip = i / 4, off = SP::off(16 * r + n16, (32 * ip + 8 * g) * ES);
+            if constexpr (Y::BF) {
+#pragma unroll
+                for (int k = 0; k < NP; ++k) x.p[i].p[k] = *reinterpret_cast<const bf16x8 *>(P + k * Y::PPLANE + off);
+            } else {
+                x.p[i].x.b0 = *reinterpret_cast<const f32x4 *>(P + off);
+                x.p[i].x.b1 = *reinterpret_cast<const f32x4 *>(P + SP::off(16 * r + n16, (32 * ip + 8 * g) * ES + 16));
+            }
+        }
+        return x;
+    }
+
+    // --------------------------------------------------------------- the waves
+    // Two chunks a turn, so that a buffer's addresses are the same in every turn
+    template <typename F> __device__ __forceinline__ void each_chunk(F step) const {
+        for (int it = 0; it < n_it; it += 2) {
+            step(it, std::integral_constant<int, 0>{});
+            if (it + 1 < n_it) step(it + 1, std::integral_constant<int, 1>{});
+        }
+    }
+    __device__ __forceinline__ void first_copies(Copies &x, bool with_gates) const {
+        if (n_it > 0) {
+            issue(x, 0);
+            if (with_gates) {
+                issue_gates(0);
+                if (n_it > 1) issue_gates(1);
+                wait_copies();
+                make_table(0);  // (this wave's own copy)
+            }
+        }
+        wait_copies();
         lds_barrier();
     }
 
-    // score tiles (row tile, key tile) of this wave: the waves whose half of P V is the shorter
-    // one take two each
-    constexpr int none = -1;
-    const int tile0 = w == 4 ? 0x30 : w == 5 ? 0x32 : w == 6 ? 0x20 : w == 7 ? 0x22 : w == 0 ? 0x00 : w == 1 ? 0x11 : none;
-    const int tile1 = w == 4 ? 0x31 : w == 5 ? 0x33 : w == 6 ? 0x21 : w == 7 ? 0x10 : none;
-
-    for (int it = 0; it < n_it; ++it) {
-        const int c = chunk_of(it);
-        char *b = lds + (Y::NB == 2 ? (it & 1) * Y::BUF : 0);
-        const char *Ks = b + Y::OFF_K, *Vs = b + Y::OFF_V, *Qs = b + Y::OFF_Q;
-        const float *gt = gates + (it & 1) * Y::GT;
-        if (Y::NB == 2 && it + 1 < n_it) issue(chunk_of(it + 1), lds + ((it + 1) & 1) * Y::BUF);
-        if constexpr (OUT) {
-            if (it > 0) store_out(chunk_of(it - 1));
-            if (J.dots) fetch_e(c);
+    __device__ __forceinline__ void run() {
+        Copies from = copies();
+        f32x4 h[RT];
+        start_state(h);
+        int to_border = !J.border || p.split ? -1 : rev ? c_first % p.s.seg_chunks + 1 : p.s.seg_chunks;  // chunks
+        // the tiles of P right of the diagonal that a 32-deep product reads: zero, never written
+        constexpr int per = 16 * 16 * 2;  // elements of a plane
+        for (int i = threadIdx.x; i < 2 * (Y::PT / Y::PPLANE) * per; i += 64 * NW) {
+            const int e = i % per, t = e >> 8, r = 32 * t + ((e >> 4) & 15), k = 32 * t + 16 + (e & 15);
+            *reinterpret_cast<In *>(lds + Y::OFF_P + (i / per) * Y::PPLANE + SP::off(r, k * ES)) = In(0.f);
         }
+        typedef In in4 __attribute__((ext_vector_type(4)));
+        typedef Out out4 __attribute__((ext_vector_type(4)));
+        // a row's place: token 16 r + n16 of the chunk, columns 4g .. of this wave's.  Offsets within a
+        // whole chunk; a shorter one's rows lie that much lower where rows run backwards
+        const int64_t orow = (int64_t)p.s.Hv * J.W, at = c_first * (int64_t)CH;
+        const int in_block = cb * BW + 16 * w + 4 * g;
+        Out *o0 = reinterpret_cast<Out *>(J.o) + (bos + at) * orow + (int64_t)hv * J.W + in_block;
+        const int64_t o_step = (rev ? -CH : CH) * orow;
+        const In *e0 = nullptr;
+        float *d0 = nullptr;
+        uint32_t oo[4], eo[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tok = token_of(16 * r + n16, CH);
+            oo[r] = (uint32_t)tok * (uint32_t)orow;
+            if constexpr (DOTS) eo[r] = (uint32_t)tok * (uint32_t)J.e_row;
+        }
+        if constexpr (DOTS) {
+            e0 = reinterpret_cast<const In *>(J.e) + first_row(J.e_row, J.e_batch) + at * J.e_row + (hv / J.e_div) * J.W + in_block;
+            d0 = J.dots + ((int64_t)cb * p.s.Hv + hv) * p.tokens + bos;
+        }
+        auto dots_at = [&](int buf) { return reinterpret_cast<float *>(lds + Y::OFF_S) + buf * NW * CH; };
+        auto store_dots = [&](int it, int buf) {  // one wave, a row per lane
+            const int c = chunk_of(it), n = rows_of(c);
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) d += dots_at(buf)[i * CH + l];
+            if (l < n) glb(d0)[c * CH + token_of(l, n)] = d;
+        };
+        // of the chunk before: its Q h, V and part of e
         f32x4 o[4];
-        X vo[2];
+        X v[2];
+        in4 e[4];
+        auto place_of_scores = [&](int buf) { return lds + Y::OFF_P + buf * Y::PT; };
+        auto finish = [&](int it, int buf, const Weights &x) {  // chunk `it`, P in place buf
+            const int n = rows_of(chunk_of(it));
+            mma_pieces<4>(o, v[0], x.p);
+            mma_pieces<2>(o + 2, v[1], x.p + 4);
+            if constexpr (DOTS) {
+                f32x4 d;
 #pragma unroll
-        for (int ip = 0; ip < 2; ++ip) vo[ip] = kt8<In, SV>(Vs, 32 * ip, 16 * c4, 4);
-        if constexpr (OUT) {
-            // P tiles
-            auto score = [&](int tile) {
-                const int rt = tile >> 4, kt = tile & 15;
-                f32x4 s = zero4();
+                for (int r = 0; r < 4; ++r) {
+                    d[r] = o[r][0] * to_f32(e[r][0]);
 #pragma unroll
-                for (int u = 0; u < KD / 32; ++u)
-                    s = mma(s, frag8<In, SK>(Ks, 16 * kt + n16, (32 * u + 8 * g) * ES),
-                            frag8<In, SK>(Qs, 16 * rt + n16, (32 * u + 8 * g) * ES));
-                const int r = 16 * rt + n16, k0 = 16 * kt + 4 * g;  // s[i]: row r, key k0 + i
-                if (rt == kt) {
-                    const f32x4 gk = *reinterpret_cast<const f32x4 *>(gt + G_LOC + k0);
-                    const float gr = gt[G_LOC + r];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = 4 * g + i <= n16 ? s[i] * (J.in_scale * fast_exp(gr - gk[i])) : 0.f;
-                } else {
-                    s *= *reinterpret_cast<const f32x4 *>(gt + G_TO + (rt - kt - 1) * CH + k0) * gt[G_A + r];
+                    for (int i = 1; i < 4; ++i) d[r] = fmaf(o[r][i], to_f32(e[r][i]), d[r]);
                 }
-                const int off = SP::off(r, k0 * ES);
-                if constexpr (Y::BF) {
-                    bf16x4 x[NP];
-                    pieces4<NP>(s, x);
+                const int tile = (l >> 5 & 1) | (l >> 3 & 2);
+                dots_at(buf)[w * CH + 16 * tile + n16] = sum_rows(d);
+            }
+            Out *oc = o0 + (rev && n < CH ? (n - CH) * orow : 0);
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) *reinterpret_cast<bf16x4 *>(pplane + i * Y::PPLANE + off) = x[i];
-                } else {
-                    *reinterpret_cast<f32x4 *>(pplane + off) = s;
-                }
-            };
-            if (tile0 != none) score(tile0);
-            if (tile1 != none) score(tile1);
-            // this half's part of (Q h)^T: lane (token n16 of tile r, columns 4g ..)
+            for (int r = 0; r < 4; ++r)
+                if (16 * r + n16 < n) *glb(reinterpret_cast<out4 *>(oc + oo[r])) = __builtin_convertvector(o[r], out4);
+            o0 += o_step;
+        };
+        // this wave's tiles of P: NT of one row tile and, for two waves, one more
+        constexpr int NT = NW == 8 ? 1 : 2;
+        const int rt = NW == 8 ? (w < 4 ? 3 : w == 5 ? 1 : w == 7 ? 0 : 2) : w < 2 ? 3 : 4 - w;
+        const int kt = NW == 8 ? (w < 4 ? w : w == 6 ? 2 : 0) : w == 1 ? 2 : 0;
+        const int more_rt = NW == 8 ? (w == 4 ? 2 : w == 5 ? 1 : -1) : w == 2 ? 2 : w == 3 ? 0 : -1;
+        const int more_kt = NW == 8 ? 1 : w == 2 ? 2 : 0;
+        first_copies(from, w == 0);
+        each_chunk([&](int it, auto B) {
+            constexpr int buf = decltype(B)::value;
+            const int c = chunk_of(it), n = rows_of(c);
+            const char *b = buffer(buf);
+            const float *gt = table(buf);
+            char *P = place_of_scores(buf);
+            if (Y::NB == 2 && it + 1 < n_it) issue(from, buf ^ 1);
+            stage();
+            // the last chunk's P V (in the first turn of zeros), with the reads for the tiles of P
+            const Weights pw = weights(place_of_scores(buf ^ 1));
+            stage();
+            const Scores<NT> sc = score_operands<NT>(b, gt, rt, kt);
+            if (it > 0) finish(it - 1, buf ^ 1, pw);
+            if constexpr (DOTS) {
+                if (w == 1 && it > 1) store_dots(it - 2, buf);
+                const In *ec = e0 + (rev && n < CH ? (n - CH) * J.e_row : 0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (16 * r + n16 < n) e[r] = *glb(reinterpret_cast<const in4 *>(ec + eo[r]));
+                e0 += (rev ? -CH : CH) * J.e_row;
+            }
+            stage();
+            X q[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) q[r] = query(b, r, 0);
+            score<NT>(sc, P, rt, kt);
+            stage();
+            // (Q h)^T: lane (token n16 of tile r, columns 4g ..)
+            float out[4];
+            Ends ends_here;
+            Keys k0;
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = zero4();
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const Pieces<In, NP> hp = pieces8<In, NP>(h[2 * u], h[2 * u + 1]);
+                X next[4];
+                if (u + 1 < U) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    o[r] = mma(o[r], hp, frag8<In, SK>(Qs, 16 * r + n16, (half * (KD / 2) + 32 * u + 8 * g) * ES));
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] *= gt[G_START + 16 * r + n16];
-        }
-        // the state at the chunk's end
-        const float all = gt[G_START + CH - 1];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) h[t] *= all;
-        if (!OUT) whole *= all;
-#pragma unroll
-        for (int ip = 0; ip < 2; ++ip) {
-            const f32x4 *e = reinterpret_cast<const f32x4 *>(gt + G_END + 32 * ip + 8 * g);
-            f32x4 x0, x1;
-            if constexpr (Y::BF) {
-                x0 = widen(vo[ip].b0), x1 = widen(vo[ip].b1);
-            } else {
-                x0 = vo[ip].b0, x1 = vo[ip].b1;
-            }
-            const Pieces<In, 3> vd = pieces8<In, 3>(x0 * e[0], x1 * e[1]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const int tt = half * RT + t;
-                h[t] = mma(h[t], kt8<In, SK>(Ks, 32 * ip, 32 * (tt >> 1) + 4 * (tt & 1), 8), vd);
-            }
-        }
-        if (w == GW && it + 1 < n_it) {
-            const int cn = chunk_of(it + 1);
-            gate_table(g_next, min(CH, len - cn * CH), J.in_scale, gates + ((it + 1) & 1) * Y::GT);
-            if (it + 2 < n_it) g_next = gate(chunk_of(it + 2));
-        }
-        if constexpr (OUT) {
-            lds_barrier();  // P complete, the staged output stored
-            // P V: a half of the keys each
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (r < 2 && half == 1) continue;
-                const int off0 = SP::off(16 * r + n16, (32 * half + 8 * g) * ES);
-                const X v = half ? vo[1] : vo[0];
-                if constexpr (Y::BF) {
-#pragma unroll
-                    for (int i = NP - 1; i >= 0; --i)
-                        o[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            cat(v.b0, v.b1), *reinterpret_cast<const bf16x8 *>(pplane + i * Y::PPLANE + off0), o[r], 0, 0, 0);
+                    for (int r = 0; r < 4; ++r) next[r] = query(b, r, u + 1);
                 } else {
-                    const int off1 = SP::off(16 * r + n16, (32 * half + 8 * g) * ES + 16);
-                    o[r] = mma(o[r], v, OpF{*reinterpret_cast<const f32x4 *>(pplane + off0),
-                                            *reinterpret_cast<const f32x4 *>(pplane + off1)});
-                }
-            }
-            char *op = lds + Y::OFF_O + half * Y::OPLANE;
+                    v[0] = values(b, 0), v[1] = values(b, 1), ends_here = ends_of(gt), k0 = keys(b, 0, 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) *reinterpret_cast<f32x4 *>(op + SO::off(16 * r + n16, 4 * (16 * c4 + 4 * g))) = o[r];
-            // a border inside the scan
-            if (J.border && !p.split) {
-                const int after = rev ? c : c + 1;
-                if (after % p.s.seg_chunks == 0 && after > 0 && after < nc)
-                    store_state(at_place(J.border, first_place + after / p.s.seg_chunks), 1.f);
+                    for (int r = 0; r < 4; ++r) out[r] = gt[G_OUT + 16 * r + n16];
+                }
+                const Pieces<In, NP> hp = pieces8<In, NP>(h[2 * u], h[2 * u + 1]);
+                mma_each<4>(o, hp, q);
+                stage();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) q[r] = next[r];
             }
-        }
-        wait_dma();
-        lds_barrier();  // output staged, this buffer free, the next chunk landed
-        if (Y::NB == 1 && it + 1 < n_it) {
-            issue(chunk_of(it + 1), lds);
-            wait_dma();
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] *= out[r];
+            add_chunk(b, gt, v, ends_here, k0, h);
+            if (more_rt >= 0) score<1>(score_operands<1>(b, gt, more_rt, more_kt), P, more_rt, more_kt);
+            if (w == 0) {
+                if (it + 1 < n_it) make_table(it + 1);
+                if (it + 2 < n_it) issue_gates(it + 2);
+            }
+            if (--to_border == 0) {
+                to_border = p.s.seg_chunks;
+                const int after = rev ? c : c + 1;  // chunks before the border
+                if (after > 0 && after < nc) store_state(at_place(J.border, first_place + after / p.s.seg_chunks), h, 1.f);
+            }
+            wait_copies();
             lds_barrier();
-        }
-    }
-    if constexpr (OUT) {
-        if (n_it > 0) store_out(chunk_of(n_it - 1));
-        if (ends && J.fin) {
-            float f = 1.f;
-            if (rev && len > 0) {
-                const float x = gp[0];
-                f = fast_exp(x < LOWEST_GATE ? LOWEST_GATE : x);
+            if (Y::NB == 1 && it + 1 < n_it) {
+                issue(from, 0);
+                wait_copies();
+                lds_barrier();
             }
-            store_state(J.fin + unit * KV, f);
+        });
+        if (n_it > 0) {
+            finish(n_it - 1, (n_it - 1) & 1, weights(place_of_scores((n_it - 1) & 1)));
+            if constexpr (DOTS) {
+                lds_barrier();
+                if (w == 1 && n_it > 1) store_dots(n_it - 2, n_it & 1);
+                if (w == 1) store_dots(n_it - 1, (n_it - 1) & 1);
+            }
         }
-        if (ends && J.border_fin) store_state(at_place(J.border_fin, first_place), 1.f);
-    } else {
-        store_state(at_place(J.border, first_place + (rev ? m : m + 1)), 1.f);
-        if (cb == 0 && tid == 0) J.decays[(int64_t)(first_place + m) * p.s.Hv + hv] = whole;
+        end_state(h);
     }
+
+    // The end state of a segment alone
+    __device__ __forceinline__ void run_segment() {
+        Copies from = copies();
+        f32x4 h[RT];
+        start_state(h);
+        float whole = 1.f;
+        first_copies(from, w == 0);
+        each_chunk([&](int it, auto B) {
+            constexpr int buf = decltype(B)::value;
+            const char *b = buffer(buf);
+            if (Y::NB == 2 && it + 1 < n_it) issue(from, buf ^ 1);
+            const X v[2] = {values(b, 0), values(b, 1)};
+            const Ends e = ends_of(table(buf));
+            const Keys k0 = keys(b, 0, 0);
+            if (w == 0) {
+                if (it + 1 < n_it) make_table(it + 1);
+                if (it + 2 < n_it) issue_gates(it + 2);
+            }
+            add_chunk(b, table(buf), v, e, k0, h);
+            whole *= table(buf)[G_START + CH - 1];
+            wait_copies();
+            lds_barrier();
+            if (Y::NB == 1 && it + 1 < n_it) {
+                issue(from, 0);
+                wait_copies();
+                lds_barrier();
+            }
+        });
+        store_state(at_place(J.border, first_place + (rev ? m : m + 1)), h, 1.f);
+        if (cb == 0 && threadIdx.x == 0) J.decays[(int64_t)(first_place + m) * p.s.Hv + hv] = whole;
+    }
+};
+
+template <typename In, typename Out, int KD, int NP, int NW, bool DOTS>
+__global__ __launch_bounds__(64 * NW)
+    __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void gdr_la_scan_kernel(const LaParams p) {
+    using S = Scan<In, Out, KD, NP, NW, DOTS>;
+    __shared__ __attribute__((aligned(16))) char lds[S::Y::BYTES];
+    int id = xcd_remap(blockIdx.x, gridDim.x);
+    const int cb = id % p.n_cb;
+    id /= p.n_cb;
+    S s(p, id % p.n_jobs, lds);
+    id /= p.n_jobs;
+    s.cb = cb, s.hv = id % p.s.Hv;
+    if (!s.place(id / p.s.Hv)) return;
+    s.run();
+}
+// end states of segments
+template <typename In, int KD>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void gdr_la_states_kernel(const LaParams p) {
+    using S = Scan<In, void, KD, 1, 4, false>;
+    __shared__ __attribute__((aligned(16))) char lds[S::Y::BYTES];
+    int id = xcd_remap(blockIdx.x, gridDim.x);
+    const int cb = id % p.n_cb;
+    id /= p.n_cb;
+    S s(p, id % p.n_jobs, lds);
+    id /= p.n_jobs;
+    s.cb = cb, s.hv = id % p.s.Hv;
+    if (s.place(id / p.s.Hv) && !s.ends) s.run_segment();  // (a border lies after it)
 }
 
-template <typename In, int KD, int NP, bool OUT>
-hipError_t launch(const LaParams &p, int items, hipStream_t s) {
-    launch_k(gdr_la_scan_kernel<In, KD, NP, OUT>, dim3((uint32_t)items * p.s.Hv * p.n_jobs * p.n_cb), dim3(NT), 0, s, p);
+template <typename In, typename Out, int NP, bool DOTS>
+hipError_t launch(int KD, const LaParams &p, int items, hipStream_t s) {
+    const dim3 grid((uint32_t)items * p.s.Hv * p.n_jobs * p.n_cb);
+    const bool wide = p.job[0].W == 128 * p.n_cb;
+    if (KD == 128 && wide)
+        launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
+    else if (KD == 128)
+        launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 4, DOTS>, grid, dim3(256), 0, s, p);
+    else if (wide)
+        launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
+    else
+        launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 4, DOTS>, grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_la_scan(Dt dt, int KD, bool fine, const LaParams &p, int items, hipStream_t s) {
-    if (dt == Dt::F32) return KD == 128 ? launch<float, 128, 1, true>(p, items, s) : launch<float, 64, 1, true>(p, items, s);
-    if (fine) return KD == 128 ? launch<bf16, 128, 3, true>(p, items, s) : launch<bf16, 64, 3, true>(p, items, s);
-    return KD == 128 ? launch<bf16, 128, 2, true>(p, items, s) : launch<bf16, 64, 2, true>(p, items, s);
+hipError_t launch_la_scan(Dt dt, Dt out, int KD, bool dots, const LaParams &p, int items, hipStream_t s) {
+    if (dt == Dt::F32) {
+        if (out == Dt::F32) return dots ? launch<float, float, 1, true>(KD, p, items, s) : launch<float, float, 1, false>(KD, p, items, s);
+        return dots ? launch<float, bf16, 1, true>(KD, p, items, s) : launch<float, bf16, 1, false>(KD, p, items, s);
+    }
+    if (out == Dt::F32) return dots ? launch<bf16, float, 3, true>(KD, p, items, s) : launch<bf16, float, 3, false>(KD, p, items, s);
+    return dots ? launch<bf16, bf16, 3, true>(KD, p, items, s) : launch<bf16, bf16, 2, false>(KD, p, items, s);
 }
 
 hipError_t launch_la_states(Dt dt, int KD, const LaParams &p, int items, hipStream_t s) {
-    if (dt == Dt::F32) return KD == 128 ? launch<float, 128, 1, false>(p, items, s) : launch<float, 64, 1, false>(p, items, s);
-    return KD == 128 ? launch<bf16, 128, 1, false>(p, items, s) : launch<bf16, 64, 1, false>(p, items, s);
+    const dim3 grid((uint32_t)items * p.s.Hv * p.n_jobs * p.n_cb);
+    if (dt == Dt::F32 && KD == 128)
+        launch_k(gdr_la_states_kernel<float, 128>, grid, dim3(256), 0, s, p);
+    else if (dt == Dt::F32)
+        launch_k(gdr_la_states_kernel<float, 64>, grid, dim3(256), 0, s, p);
+    else if (KD == 128)
+        launch_k(gdr_la_states_kernel<bf16, 128>, grid, dim3(256), 0, s, p);
+    else
+        launch_k(gdr_la_states_kernel<bf16, 64>, grid, dim3(256), 0, s, p);
+    return hipGetLastError();
 }
 
 }  // namespace gdr

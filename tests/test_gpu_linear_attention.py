@@ -88,7 +88,7 @@ def exact(x, do=None, dht=None, scale=None):
         return out
     heads = lambda y: y.view(B, T, Hq, G, K).sum(3)  # noqa: E731
     dg = dg.sum(0) if x["g"].dim() == 1 else dg.view(B, T, Hv)
-    terms = (q * dq).sum(-1).norm().item() * (math.sqrt(B * T) if x["g"].dim() == 1 else 1)
+    terms = max((q * dq).sum(-1).norm().item(), (k * dk).sum(-1).norm().item()) * (math.sqrt(B * T) if x["g"].dim() == 1 else 1)
     return out + (heads(dq), heads(dk), dv.view(B, T, Hv, V), dg, None if x["initial_state"] is None else dh0, terms)
 
 
@@ -128,7 +128,7 @@ def test_backward(gdr, T, dtype, K, V):
                                              grad_dtype=grad)
         for name, a, b in zip(("dq", "dk", "dv"), got, want):
             check(a, b, TOL[grad], name)
-        check(got[3], want[3], TOL_GATES, "dg")
+        check(got[3], want[3], TOL_GATES, "dg", want[5])
         if want[4] is not None:
             check(got[4], want[4], TOL[F32], "dh0")
 
@@ -146,7 +146,7 @@ def test_packed(gdr, lens, K, V, dtype):
     check(last, hT, TOL[F32], "final_state")
     grads = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, x["initial_state"], x["cu_seqlens"])
     for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "dh0"), grads, want, [TOL[dtype]] * 3 + [TOL_GATES, TOL[F32]]):
-        check(a, b, tol, name)
+        check(a, b, tol, name, want[5] if name == "dg" else 0.0)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -164,7 +164,7 @@ def test_segments(gdr, segment, dtype):
     grads = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, x["initial_state"],
                                            x["cu_seqlens"], segment_chunks=segment)
     for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "dh0"), grads, want, [TOL[dtype]] * 3 + [TOL_GATES, TOL[F32]]):
-        check(a, b, tol, name)
+        check(a, b, tol, name, want[5] if name == "dg" else 0.0)
 
 
 @pytest.mark.parametrize("N", [1, 3, 40])
@@ -176,9 +176,9 @@ def test_heads(gdr, N, group):
         o, hT, *want = exact(x, do)
         got, _ = gdr.chunk_linear_attention_fwd(**x, output_dtype=BF)
         check(got, o, TOL[BF], "o")
-        for a, b, tol in zip(gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do), want,
-                             [TOL[BF]] * 3 + [TOL_GATES]):
-            check(a, b, tol, "gradient")
+        for a, b, tol, terms in zip(gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do), want,
+                                    [TOL[BF]] * 3 + [TOL_GATES], [0, 0, 0, want[5]]):
+            check(a, b, tol, "gradient", terms)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -243,22 +243,22 @@ def test_autograd(gdr):
         detached = {n: t if t is None or n == "cu_seqlens" else t.detach() for n, t in x.items()}
         want = exact(detached, do, dht)
         check(o.detach(), want[0], TOL[out], "o")
-        for a, b, leaf, tol in zip(torch.autograd.grad([o, hT], leaves, [do, dht]), want[2:], leaves,
-                                   [TOL[dtype]] * 3 + [TOL_GATES, TOL[F32]]):
+        tols, terms = [TOL[dtype]] * 3 + [TOL_GATES, TOL[F32]], lambda w: [0, 0, 0, w[-1], 0]  # noqa: E731
+        for a, b, leaf, tol, t in zip(torch.autograd.grad([o, hT], leaves, [do, dht]), want[2:], leaves, tols, terms(want)):
             assert a.dtype == leaf.dtype
-            check(a, b, tol, "gradient")
+            check(a, b, tol, "gradient", t)
         # of the final state alone, and an expanded gradient of o
         o, hT = gdr.chunk_linear_attention(**x, output_final_state=True, output_dtype=out)
         want = exact(detached, None, dht)[2:]
         grads = torch.autograd.grad(hT, leaves, dht, allow_unused=True)
-        for a, b, tol in zip(grads[1:], want[1:], [TOL[dtype]] * 2 + [TOL_GATES, TOL[F32]]):
-            check(a, b, tol, "gradient")
+        for a, b, tol, t in zip(grads[1:], want[1:], tols[1:], terms(want)[1:]):
+            check(a, b, tol, "gradient", t)
         assert not grads[0].any()
         o, none = gdr.chunk_linear_attention(**x, output_dtype=out)
         assert none is None
         want = exact(detached, torch.ones(o.shape, device="cuda"))[2:]
-        for a, b, tol in zip(torch.autograd.grad(o.sum(), leaves), want, [TOL[dtype]] * 3 + [TOL_GATES, TOL[F32]]):
-            check(a, b, tol, "gradient")
+        for a, b, tol, t in zip(torch.autograd.grad(o.sum(), leaves), want, tols, terms(want)):
+            check(a, b, tol, "gradient", t)
 
 
 def test_gradients_are_differences(gdr):
