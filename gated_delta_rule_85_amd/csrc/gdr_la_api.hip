@@ -15,13 +15,27 @@ size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int64_t UNITS = 256;    // compute units of an MI355X, a workgroup each
 constexpr int BORDER_CHUNKS = 16; // the backward's longest segments (gate gradients start anew at each border)
 
-// Chunks per segment, or 0: no split.  W workgroups per segment of N chunks; a split costs a scan
-// without output of all segments but the last, about half of one with output, and three launches
-// more, about eight chunks' time.
-int64_t split_chunks(int64_t N, int64_t W) {
-    int64_t best = cdiv(W, UNITS) * N, L = 0;
-    for (int64_t S = 2; S <= N && (S - 1) * W < 2 * UNITS; ++S) {
-        const int64_t l = cdiv(N, S), rounds = cdiv(W * S, UNITS), t = rounds * l + rounds * l / 2 + 8;
+// 128 columns a workgroup (bf16) where that leaves one for every compute unit (gdr_la_scan.hip): fewer
+// tiles of P a column, against all compute units busy.  `units`: sequences (or segments) and heads
+bool wide(int32_t dtype, int64_t units) { return dtype == GDR_BF16 && units >= UNITS; }
+
+// Chunks per segment, or 0: no split.  N chunks a sequence, `units` sequences and heads of `blocks` times
+// 64 columns, `scans` scans and `states` scans without output.  In the time of a chunk of 128 columns on every
+// compute unit (4.4 us): a chunk of 64 columns takes 0.6, one without output 0.5 of a workgroup that
+// shares its compute unit; a workgroup's start 1 to 3, the launches and the carry between the two
+// 3 and what the segments' states take.  Prefill of one sequence of 4096 tokens (32 heads of 128 columns):
+// 177 us unsplit, 144 / 109 / 107 with segments of 32 / 8 / 4; of 1024 tokens 50 unsplit, 58 with 4
+int64_t split_chunks(int32_t dtype, int64_t N, int64_t units, int64_t blocks, int64_t scans, int64_t states) {
+    auto scan = [&](int64_t u, int64_t L) {
+        return blocks == 2 && wide(dtype, u) ? (double)cdiv(u, UNITS) * (L + 1) : 0.6 * (double)cdiv(u * blocks, UNITS) * (L + 1);
+    };
+    double best = scans * scan(units, N);
+    int64_t L = 0;
+    for (int64_t S = 2; S <= N && (S - 1) * units < 4 * UNITS; ++S) {
+        const int64_t l = cdiv(N, S);
+        if (cdiv(N, l) != S) continue;  // the segments of a smaller S
+        const double t = scans * scan(S * units, l) + 0.5 * (double)cdiv(states * (S - 1) * units * blocks, 2 * UNITS) * (l + 3) +
+                         3 + S / 16.0;
         if (t < best) best = t, L = l;
     }
     return L;
@@ -56,15 +70,15 @@ struct Plan {
     size_t border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, total;
 };
 
-// scans: workgroups of a head and sequence
-template <typename Args> int plan(const Args *a, int64_t scans, bool backward, Plan &p) {
+template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
     const bool varlen = a->cu_seqlens != nullptr;
     p.n_seq = varlen ? a->n_seq : a->B;
     p.tokens = p.n_seq > 0 ? a->B * a->T : 0;
     p.group = (int)(a->H_v / a->H_q);
     // packed sequences may all but be one
-    const int64_t nct = cdiv(a->T, CH), W = (varlen ? 1 : std::max<int64_t>(p.n_seq, 1)) * a->H_v * scans;
-    int64_t L = a->segment_chunks ? a->segment_chunks : split_chunks(nct, W);
+    const int64_t nct = cdiv(a->T, CH), units = (varlen ? 1 : std::max<int64_t>(p.n_seq, 1)) * a->H_v;
+    int64_t L = a->segment_chunks ? a->segment_chunks
+                                  : split_chunks(a->dtype, nct, units, std::max(a->V, backward ? a->K : 0) / 64, backward ? 3 : 1, backward ? 2 : 1);
     p.split = L > 0 && L < nct;
     if (backward) L = L > 0 ? std::min<int64_t>(L, BORDER_CHUNKS) : BORDER_CHUNKS;
     if (!p.split && !backward) L = std::max<int64_t>(nct, 1);
@@ -72,10 +86,9 @@ template <typename Args> int plan(const Args *a, int64_t scans, bool backward, P
     p.seg_tokens = L * CH;
     p.places = la_slots(p.tokens, p.n_seq, p.seg_tokens);
     // 32-bit numbers of workgroups and work-items
-    if (std::max(p.places, p.n_seq) * a->H_v * std::max<int64_t>(scans, 16) >= (int64_t)1 << 23) return GDR_EINVAL;
-    // 128 columns a workgroup where that leaves one for every compute unit (gdr_la_scan.hip)
-    const bool wide = (p.split ? p.places : p.n_seq) * a->H_v >= UNITS;
-    p.n_cb_k = a->K == 128 && !wide ? 2 : 1, p.n_cb_v = a->V == 128 && !wide ? 2 : 1;
+    if (std::max(p.places, p.n_seq) * a->H_v * 16 >= (int64_t)1 << 23) return GDR_EINVAL;
+    const bool whole = wide(a->dtype, (p.split ? p.places : p.n_seq) * a->H_v);
+    p.n_cb_k = a->K == 128 && !whole ? 2 : 1, p.n_cb_v = a->V == 128 && !whole ? 2 : 1;
     p.border_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v * a->K * a->V));
     p.decays_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v));
     return GDR_OK;
@@ -84,7 +97,7 @@ template <typename Args> int plan(const Args *a, int64_t scans, bool backward, P
 int plan_fwd(const gdr_la_fwd_args *a, Plan &p) {
     int rc = a ? check(a, a->out_dtype) : GDR_EINVAL;
     if (rc) return rc;
-    rc = plan(a, a->V / 64, false, p);
+    rc = plan(a, false, p);
     if (rc) return rc;
     p.off_fwd = 0;
     p.off_decays_fwd = p.border_bytes;
@@ -95,7 +108,7 @@ int plan_fwd(const gdr_la_fwd_args *a, Plan &p) {
 int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
     int rc = a ? check(a, a->grad_dtype) : GDR_EINVAL;
     if (rc) return rc;
-    rc = plan(a, 2 * (a->K / 64) + a->V / 64, true, p);
+    rc = plan(a, true, p);
     if (rc) return rc;
     if (p.group > 1 && p.tokens * a->H_q * a->K >= (int64_t)1 << 34) return GDR_EINVAL;  // work-items of the sums
     size_t off = 0;

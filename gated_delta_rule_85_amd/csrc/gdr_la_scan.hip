@@ -12,7 +12,7 @@
 // chunk's work, so that one barrier a chunk orders everything: in turn c a wave stores O of chunk
 // c - 1 with its P V, makes its tiles of P of chunk c and its columns of Q h, then h', while K, Q, V
 // and the gates of chunk c + 1 are copied global -> LDS (bf16: two buffers).  NW is 8 (128 columns:
-// half of the tiles of P a column) where that leaves a workgroup for every compute unit, else 4.
+// half of the tiles of P a column) for bf16 inputs where that leaves a workgroup for every compute unit, else 4.
 //
 // rev: row r of a chunk is its r-th token from the end, and a row's gate is the next token's, so
 // that the same code scans from the last token to the first.
@@ -52,7 +52,9 @@ __device__ __forceinline__ void copy4(const char *base, uint32_t off, const char
                  : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(off), "s"(base)
                  : "memory");
 }
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+// until no more than the last N instructions that touch memory are under way: they end in order, and any
+// others than copies among them make the wait longer, never shorter
+template <int N = 0> __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 // ------------------------------------------------------- operands in pieces
 template <typename In, int NP> struct Pieces {
@@ -131,16 +133,17 @@ template <int N, int NP> __device__ __forceinline__ void mma_pieces(f32x4 *c, co
 // ------------------------------------------------------------ LDS layout
 template <typename In, int KD, int NP, int NW, bool OUT> struct Lay {
     static constexpr bool BF = sizeof(In) == 2;
-    static constexpr int ES = sizeof(In), NB = BF ? 2 : 1, BW = 16 * NW;
+    // buffers: as many as the two workgroups of a compute unit without output, or the one with it, have room for
+    static constexpr int ES = sizeof(In), NB = !BF ? 1 : OUT ? 2 : 3, BW = 16 * NW;
     static constexpr int KROW = KD * ES, VROW = BW * ES, PROW = CH * ES;
     static constexpr int KT = CH * KROW, VT = CH * VROW;
     static constexpr int OFF_K = 0, OFF_V = KT, OFF_Q = KT + VT, BUF = KT + VT + (OUT ? KT : 0);
     static constexpr int PPLANE = CH * PROW, PT = (BF ? NP : 1) * PPLANE;  // planes of P
     static constexpr int OFF_P = NB * BUF;                           // P of two chunks
     static constexpr int OFF_S = OFF_P + (OUT ? 2 * PT : 0);         // dots of two chunks: [wave][token]
-    static constexpr int OFF_T = OFF_S + (OUT ? 2 * NW * CH * 4 : 0);  // gate tables of two chunks
-    static constexpr int GT = 8 * CH;                                // floats of one
-    static constexpr int OFF_G = OFF_T + 2 * GT * 4;                 // gates of four chunks
+    static constexpr int OFF_T = OFF_S + (OUT ? 2 * NW * CH * 4 : 0);  // gate tables of two chunks (without output: of each wave)
+    static constexpr int GT = (OUT ? 8 : 3) * CH;                    // floats of one
+    static constexpr int OFF_G = OFF_T + (OUT ? 2 : NW) * GT * 4;    // gates of four chunks
     static constexpr int BYTES = OFF_G + 4 * CH * 4;
     static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
     using SK = Swz<KROW, KeyKQ>;
@@ -157,8 +160,8 @@ enum { G_START = 0, G_OUT = CH, G_END = 2 * CH, G_ROW = 3 * CH, G_KEY = 4 * CH }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // one row's gate per lane (0 past the chunk's n rows and before its sequence's first gate) -> the table;
-// rows past n add nothing
-__device__ __forceinline__ void gate_table(float x, int n, float in_scale, float out_scale, float *t) {
+// rows past n add nothing.  PAIRS: with the decays between keys and rows
+template <bool PAIRS> __device__ __forceinline__ void gate_table(float x, int n, float in_scale, float out_scale, float *t) {
     const int l = lane_id(), tile = l >> 4;
     x = (x < LOWEST_GATE ? LOWEST_GATE : x) * 1.4426950408889634f;  // log2 e
     x += dpp_mov<0x111>(x);  // row_shr 1, 2, 4, 8: running sums within 16 lanes
@@ -176,6 +179,7 @@ __device__ __forceinline__ void gate_table(float x, int n, float in_scale, float
     t[G_START + l] = start;
     t[G_OUT + l] = out_scale * start;
     t[G_END + l] = l < n ? in_scale * exp2_fast(rest + after) : 0.f;
+    if (!PAIRS) return;
     t[G_ROW + l] = x;
     t[G_KEY + l] = -x;
     t[G_KEY + CH + l] = rest;
@@ -346,7 +350,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         x.k += x.k_step, x.v += x.v_step, x.at += rev ? -CH : CH;
         if constexpr (OUT) x.q += x.q_step;
     }
-    __device__ __forceinline__ char *buffer(int buf) const { return lds + (Y::NB == 2 ? buf * Y::BUF : 0); }
+    __device__ __forceinline__ char *buffer(int buf) const { return lds + (Y::NB > 1 ? buf * Y::BUF : 0); }
 
     // Gates: copied two chunks ahead into one of four places, made into a table one chunk ahead.  One
     // wave does both.
@@ -355,10 +359,10 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         const char *from = reinterpret_cast<const char *>(p.s.g + (bos + c * (int64_t)CH) * p.s.g_tok + hv);
         copy4(from, (uint32_t)(t - c * CH) * (uint32_t)(4 * p.s.g_tok), lds + Y::OFF_G + (it & 3) * CH * 4);
     }
-    __device__ __forceinline__ void make_table(int it) const {
+    __device__ __forceinline__ void make_table(int it, float *to) const {
         const int c = chunk_of(it), n = rows_of(c), t = c * CH + (rev ? n - l : l);
         const float x = reinterpret_cast<const float *>(lds + Y::OFF_G)[(it & 3) * CH + l];
-        gate_table(l < n && t < len ? x : 0.f, n, J.in_scale, OUT ? J.out_scale : 1.f, table(it & 1));
+        gate_table<OUT>(l < n && t < len ? x : 0.f, n, J.in_scale, OUT ? J.out_scale : 1.f, to);
     }
     __device__ __forceinline__ float *table(int buf) const { return reinterpret_cast<float *>(lds + Y::OFF_T) + buf * Y::GT; }
 
@@ -388,7 +392,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             return pieces8<In, 3>(v.b0 * e[0], v.b1 * e[1]);
     }
     // K^T of tiles T .. T + N - 1, keys 32 ip ..
-    static constexpr int N4 = RT < 4 ? RT : 4;
+    static constexpr int N4 = !Y::BF ? 2 : RT < 4 ? RT : 4;  // (fp32: registers)
     struct Keys {
         X k[N4];
     };
@@ -473,21 +477,21 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             }
         }
     }
-    // P of row tile r, keys 32 ip ..
-    struct Weights {
-        Pieces<In, NP> p[6];
+    // P of N row tiles from the first on, keys 32 ip ..
+    template <int N> struct Weights {
+        Pieces<In, NP> p[N];
     };
-    __device__ __forceinline__ Weights weights(const char *P) const {
-        Weights x;
+    template <int N> __device__ __forceinline__ Weights<N> weights(const char *P, int first, int ip) const {
+        Weights<N> x;
 #pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            const int r = i < 4 ? i : i - 2, ip = i / 4, off = SP::off(16 * r + n16, (32 * ip + 8 * g) * ES);
+        for (int i = 0; i < N; ++i) {
+            const int row = 16 * (first + i) + n16, off = SP::off(row, (32 * ip + 8 * g) * ES);
             if constexpr (Y::BF) {
 #pragma unroll
                 for (int k = 0; k < NP; ++k) x.p[i].p[k] = *reinterpret_cast<const bf16x8 *>(P + k * Y::PPLANE + off);
             } else {
                 x.p[i].x.b0 = *reinterpret_cast<const f32x4 *>(P + off);
-                x.p[i].x.b1 = *reinterpret_cast<const f32x4 *>(P + SP::off(16 * r + n16, (32 * ip + 8 * g) * ES + 16));
+                x.p[i].x.b1 = *reinterpret_cast<const f32x4 *>(P + SP::off(row, (32 * ip + 8 * g) * ES + 16));
             }
         }
         return x;
@@ -508,7 +512,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
                 issue_gates(0);
                 if (n_it > 1) issue_gates(1);
                 wait_copies();
-                make_table(0);  // (this wave's own copy)
+                make_table(0, table(0));  // (this wave's own copy)
             }
         }
         wait_copies();
@@ -556,14 +560,16 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             if (l < n) glb(d0)[c * CH + token_of(l, n)] = d;
         };
         // of the chunk before: its Q h, V and part of e
-        f32x4 o[4];
+        f32x4 o[4] = {zero4(), zero4(), zero4(), zero4()};
         X v[2];
+        v[0] = v[1] = X{};
         in4 e[4];
         auto place_of_scores = [&](int buf) { return lds + Y::OFF_P + buf * Y::PT; };
-        auto finish = [&](int it, int buf, const Weights &x) {  // chunk `it`, P in place buf
+        // + P V
+        auto add_first = [&](const Weights<4> &x) { mma_pieces<4>(o, v[0], x.p); };   // keys 0 .. 31 of all rows
+        auto add_rest = [&](const Weights<2> &x) { mma_pieces<2>(o + 2, v[1], x.p); };  // the others
+        auto finish = [&](int it, int buf) {  // chunk `it`, its dots in place buf
             const int n = rows_of(chunk_of(it));
-            mma_pieces<4>(o, v[0], x.p);
-            mma_pieces<2>(o + 2, v[1], x.p + 4);
             if constexpr (DOTS) {
                 f32x4 d;
 #pragma unroll
@@ -581,6 +587,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
                 if (16 * r + n16 < n) *glb(reinterpret_cast<out4 *>(oc + oo[r])) = __builtin_convertvector(o[r], out4);
             o0 += o_step;
         };
+        constexpr bool TIGHT = NP == 3 || !Y::BF;  // registers for a step less of P
         // this wave's tiles of P: NT of one row tile and, for two waves, one more
         constexpr int NT = NW == 8 ? 1 : 2;
         const int rt = NW == 8 ? (w < 4 ? 3 : w == 5 ? 1 : w == 7 ? 0 : 2) : w < 2 ? 3 : 4 - w;
@@ -597,10 +604,20 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             if (Y::NB == 2 && it + 1 < n_it) issue(from, buf ^ 1);
             stage();
             // the last chunk's P V (in the first turn of zeros), with the reads for the tiles of P
-            const Weights pw = weights(place_of_scores(buf ^ 1));
+            const char *last = place_of_scores(buf ^ 1);
+            const Weights<4> p0 = weights<4>(last, 0, 0);
+            Weights<2> p1;
+            if (!TIGHT) p1 = weights<2>(last, 2, 1);
             stage();
+            if (TIGHT) {
+                p1 = weights<2>(last, 2, 1);
+                add_first(p0);
+                stage();
+            }
             const Scores<NT> sc = score_operands<NT>(b, gt, rt, kt);
-            if (it > 0) finish(it - 1, buf ^ 1, pw);
+            if (!TIGHT) add_first(p0);
+            add_rest(p1);
+            if (it > 0) finish(it - 1, buf ^ 1);
             if constexpr (DOTS) {
                 if (w == 1 && it > 1) store_dots(it - 2, buf);
                 const In *ec = e0 + (rev && n < CH ? (n - CH) * J.e_row : 0);
@@ -611,8 +628,9 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             }
             stage();
             X q[4];
+            if (Y::BF)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) q[r] = query(b, r, 0);
+                for (int r = 0; r < 4; ++r) q[r] = query(b, r, 0);
             score<NT>(sc, P, rt, kt);
             stage();
             // (Q h)^T: lane (token n16 of tile r, columns 4g ..)
@@ -624,7 +642,11 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 X next[4];
+                if (!Y::BF)  // (registers)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) q[r] = query(b, r, u);
                 if (u + 1 < U) {
+                    if (Y::BF)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) next[r] = query(b, r, u + 1);
                 } else {
@@ -635,15 +657,16 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
                 const Pieces<In, NP> hp = pieces8<In, NP>(h[2 * u], h[2 * u + 1]);
                 mma_each<4>(o, hp, q);
                 stage();
+                if (Y::BF)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) q[r] = next[r];
+                    for (int r = 0; r < 4; ++r) q[r] = next[r];
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] *= out[r];
             add_chunk(b, gt, v, ends_here, k0, h);
             if (more_rt >= 0) score<1>(score_operands<1>(b, gt, more_rt, more_kt), P, more_rt, more_kt);
             if (w == 0) {
-                if (it + 1 < n_it) make_table(it + 1);
+                if (it + 1 < n_it) make_table(it + 1, table(buf ^ 1));
                 if (it + 2 < n_it) issue_gates(it + 2);
             }
             if (--to_border == 0) {
@@ -660,7 +683,10 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             }
         });
         if (n_it > 0) {
-            finish(n_it - 1, (n_it - 1) & 1, weights(place_of_scores((n_it - 1) & 1)));
+            const char *last = place_of_scores((n_it - 1) & 1);
+            add_first(weights<4>(last, 0, 0));
+            add_rest(weights<2>(last, 2, 1));
+            finish(n_it - 1, (n_it - 1) & 1);
             if constexpr (DOTS) {
                 lds_barrier();
                 if (w == 1 && n_it > 1) store_dots(n_it - 2, n_it & 1);
@@ -670,34 +696,46 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         end_state(h);
     }
 
-    // The end state of a segment alone
+    // The end state of a segment alone.  Its chunks take less time than memory's latency, so that two
+    // (bf16) are copied ahead; every wave copies the gates, so that all have as many copies under way.
     __device__ __forceinline__ void run_segment() {
+        constexpr int AHEAD = Y::NB == 3 ? 2 : 1, EACH = NK + NV + 1;
+        static_assert(NK * NW * 1024 == Y::KT && NV * NW * 1024 == Y::VT, "as many copies on every wave");
         Copies from = copies();
         f32x4 h[RT];
         start_state(h);
         float whole = 1.f;
-        first_copies(from, w == 0);
-        each_chunk([&](int it, auto B) {
-            constexpr int buf = decltype(B)::value;
-            const char *b = buffer(buf);
-            if (Y::NB == 2 && it + 1 < n_it) issue(from, buf ^ 1);
-            const X v[2] = {values(b, 0), values(b, 1)};
-            const Ends e = ends_of(table(buf));
-            const Keys k0 = keys(b, 0, 0);
-            if (w == 0) {
-                if (it + 1 < n_it) make_table(it + 1);
-                if (it + 2 < n_it) issue_gates(it + 2);
-            }
-            add_chunk(b, table(buf), v, e, k0, h);
-            whole *= table(buf)[G_START + CH - 1];
-            wait_copies();
-            lds_barrier();
-            if (Y::NB == 1 && it + 1 < n_it) {
-                issue(from, 0);
+        auto fetch = [&](int it, int buf) {
+            issue(from, buf);
+            issue_gates(it);
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < n_it) fetch(i, i);
+        int buf = 0;
+        for (int it = 0; it < n_it; ++it) {
+            // chunk it landed, the buffer of it - 1 free
+            if (AHEAD == 2 && it + 1 < n_it)
+                wait_copies<EACH>();
+            else
                 wait_copies();
+            lds_barrier();
+            const char *b = buffer(buf);
+            const int next = buf == 0 ? AHEAD : buf - 1;  // of chunk it + AHEAD
+            if (Y::NB > 1 && it + AHEAD < n_it) fetch(it + AHEAD, next);
+            const X v[2] = {values(b, 0), values(b, 1)};
+            const Keys k0 = keys(b, 0, 0);
+            make_table(it, table(w));  // a table of its own for each wave
+            const float *gt = table(w);
+            const Ends e = ends_of(gt);
+            add_chunk(b, gt, v, e, k0, h);
+            whole *= gt[G_START + CH - 1];
+            if (Y::NB == 1) {
                 lds_barrier();
+                if (it + 1 < n_it) fetch(it + 1, 0);
             }
-        });
+            buf = buf + 1 == Y::NB ? 0 : buf + 1;
+        }
         store_state(at_place(J.border, first_place + (rev ? m : m + 1)), h, 1.f);
         if (cb == 0 && threadIdx.x == 0) J.decays[(int64_t)(first_place + m) * p.s.Hv + hv] = whole;
     }
@@ -734,13 +772,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void g
 template <typename In, typename Out, int NP, bool DOTS>
 hipError_t launch(int KD, const LaParams &p, int items, hipStream_t s) {
     const dim3 grid((uint32_t)items * p.s.Hv * p.n_jobs * p.n_cb);
-    const bool wide = p.job[0].W == 128 * p.n_cb;
-    if (KD == 128 && wide)
-        launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
-    else if (KD == 128)
+    if constexpr (sizeof(In) == 2) {  // (fp32: a wave of 8 would not have the registers)
+        if (p.job[0].W == 128 * p.n_cb) {
+            if (KD == 128)
+                launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
+            else
+                launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
+            return hipGetLastError();
+        }
+    }
+    if (KD == 128)
         launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 4, DOTS>, grid, dim3(256), 0, s, p);
-    else if (wide)
-        launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
     else
         launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 4, DOTS>, grid, dim3(256), 0, s, p);
     return hipGetLastError();
