@@ -224,39 +224,7 @@ def bwd(args, stream):
         raise GdrError("gdr_bwd", rc)
 
 
-def _sized(name, args):
-    n = ctypes.c_size_t(0)
-    rc = getattr(lib, name)(ctypes.byref(args), ctypes.byref(n))
-    if rc:
-        raise GdrError(name, rc)
-    return n.value
-
-
-def la_fwd_workspace(args):
-    return _sized("gdr_la_fwd_workspace", args)
-
-
-def la_bwd_workspace(args):
-    return _sized("gdr_la_bwd_workspace", args)
-
-
 def la_fwd(args, stream):
     rc = lib.gdr_la_fwd(ctypes.byref(args), _p(stream))
     if rc:
         raise GdrError("gdr_la_fwd", rc)
-
-
-def la_bwd(args, stream):
-    rc = lib.gdr_la_bwd(ctypes.byref(args), _p(stream))
-    if rc:
-        raise GdrError("gdr_la_bwd", rc)
-
-
-def group_norm_bwd_workspace(args):
-    return _sized("gdr_group_norm_bwd_workspace", args)
-
-
-def group_norm_bwd(args, stream):
-    rc = lib.gdr_group_norm_bwd(ctypes.byref(args), _p(stream))
-    if rc:
-        raise GdrError("gdr_group_norm_bwd", rc)

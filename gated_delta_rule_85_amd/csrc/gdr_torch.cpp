@@ -1,5 +1,6 @@
-// Python binding of the operators on a pool of states and of the group norm: the
-// argument checks of pool.py's and norm.py's functions and the calls of libgdr.
+// Python binding of the operators on a pool of states, of linear attention and of the group
+// norm: the argument checks of pool.py's, linear_attention.py's and norm.py's functions and the
+// calls of libgdr.
 //
 // A decode step calls these once per layer and token, on kernels of 5 us.  A call takes the
 // host 4.3 us here, 2.4 of them the launch; with the same checks in Python it took 9.6.  The
@@ -27,6 +28,12 @@
 extern "C" {
 __attribute__((weak)) int gdr_la_step(const gdr_pool_args *, hipStream_t);
 __attribute__((weak)) int gdr_group_norm(const gdr_norm_fwd_args *, hipStream_t);
+__attribute__((weak)) int gdr_group_norm_bwd_workspace(const gdr_norm_bwd_args *, size_t *);
+__attribute__((weak)) int gdr_group_norm_bwd(const gdr_norm_bwd_args *, hipStream_t);
+__attribute__((weak)) int gdr_la_fwd_workspace(const gdr_la_fwd_args *, size_t *);
+__attribute__((weak)) int gdr_la_fwd(const gdr_la_fwd_args *, hipStream_t);
+__attribute__((weak)) int gdr_la_bwd_workspace(const gdr_la_bwd_args *, size_t *);
+__attribute__((weak)) int gdr_la_bwd(const gdr_la_bwd_args *, hipStream_t);
 }
 
 namespace {
@@ -61,7 +68,7 @@ bool overlap(const at::Tensor &a, const at::Tensor &b) {
 
 // A tensor as the kernels read it, kept alive by `held` where it had to be made
 struct Held {
-    at::Tensor made[9];  // at most: q, k, v, g, beta and four index arrays
+    at::Tensor made[12];  // at most: q, k, v, g, beta and four index arrays; or those of linear attention's backward
     int n = 0;
     const at::Tensor &keep(at::Tensor t) { return made[n++] = std::move(t); }
 };
@@ -163,6 +170,24 @@ void check_slots(const at::Tensor &states, int64_t first, const char *name) {
          "a slot of ", name, " must be contiguous and 16-byte aligned");
 }
 
+bool failed(const char *name, int rc) {
+    PyObject *e = PyObject_CallFunction(library_error, "si", name, rc);
+    if (e) PyErr_SetObject(library_error, e);
+    Py_XDECREF(e);
+    return false;
+}
+
+// The workspace that an entry point asks for; the allocator keeps it for the stream.  False: a Python error is set
+template <typename Args>
+bool workspace(int (*sizes)(const Args *, size_t *), const char *name, Args &args, const at::Tensor &like, at::Tensor &ws) {
+    size_t bytes = 0;
+    const int rc = sizes(&args, &bytes);
+    if (rc) return failed(name, rc);
+    if (bytes) ws = at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+    args.workspace = bytes ? ws.data_ptr() : nullptr, args.workspace_bytes = bytes;
+    return true;
+}
+
 // Runs an entry point on the device's current stream.  What the kernels write in place is
 // `written`: autograd is told, so that a backward that has saved it raises an error instead of
 // using the new values.  False: a Python error is set.
@@ -181,12 +206,7 @@ bool launch(int (*entry)(const Args *, hipStream_t), const char *name, const Arg
     Py_BEGIN_ALLOW_THREADS
     rc = entry(&args, (hipStream_t)stream);
     Py_END_ALLOW_THREADS
-    if (rc) {
-        PyObject *e = PyObject_CallFunction(library_error, "si", name, rc);
-        if (e) PyErr_SetObject(library_error, e);
-        Py_XDECREF(e);
-        return false;
-    }
+    if (rc) return failed(name, rc);
     for (const at::Tensor *t : written)
         if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
     return true;
@@ -415,6 +435,152 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
+// None, or a dtype that the kernels write
+at::ScalarType dtype_of(PyObject *o, at::ScalarType none, const char *name) {
+    const at::ScalarType t = o == Py_None ? none
+                             : THPDtype_Check(o) ? reinterpret_cast<THPDtype *>(o)->scalar_type
+                                                 : at::ScalarType::Undefined;
+    NEED(element(t) >= 0, name, " must be bfloat16 or float32");
+    return t;
+}
+PyObject *wrap(const at::Tensor &t) {
+    if (t.defined()) return THPVariable_Wrap(t);
+    Py_RETURN_NONE;
+}
+PyObject *wrap_all(std::initializer_list<const at::Tensor *> all) {
+    PyObject *r = PyTuple_New((Py_ssize_t)all.size());
+    Py_ssize_t i = 0;
+    for (const at::Tensor *t : all)
+        if (r) PyTuple_SET_ITEM(r, i++, wrap(*t));
+    return r;
+}
+// floats, 16-byte aligned
+const float *states_of(const at::Tensor *x, Held &held) {
+    if (!x) return nullptr;
+    const float *p = floats(*x, held);
+    return ((uintptr_t)p & 15) == 0 ? p : held.keep(x->to(at::kFloat).clone(at::MemoryFormat::Contiguous)).const_data_ptr<float>();
+}
+// x contiguous and 16-byte aligned
+const void *packed(const at::Tensor &x, Held &held) {
+    if (x.is_contiguous() && aligned(x)) return x.data_ptr();
+    return held.keep(x.clone(at::MemoryFormat::Contiguous)).data_ptr();
+}
+
+// Chunked linear attention: what both directions check, and the arguments they share
+struct Linear {
+    const at::Tensor *q, *k, *v, *g, *h0, *cu;
+    PyObject *scale, *segment_chunks;
+    int64_t B, T, H_q, K, H_v, V, n_seq;
+    void check(std::initializer_list<const at::Tensor *> others) {
+        NEED(q->dim() == 4 && v->dim() == 4 && k->sizes() == q->sizes() && v->size(0) == q->size(0) && v->size(1) == q->size(1),
+             "expected q, k [B,T,H_q,K] and v [B,T,H_v,V]");
+        NEED(element(q->scalar_type()) >= 0 && k->scalar_type() == q->scalar_type() && v->scalar_type() == q->scalar_type(),
+             "q, k, v must share one dtype, bfloat16 or float32");
+        B = q->size(0), T = q->size(1), H_q = q->size(2), K = q->size(3), H_v = v->size(2), V = v->size(3);
+        NEED((g->dim() == 1 && g->size(0) == H_v) || (g->dim() == 3 && g->size(0) == B && g->size(1) == T && g->size(2) == H_v),
+             "g must be [B,T,H_v] or [H_v]");
+        NEED(g->is_floating_point(), "g must be floating point");
+        n_seq = B;
+        if (cu) {
+            NEED(B == 1 && cu->scalar_type() == at::kInt && cu->dim() == 1 && cu->numel() >= 1,
+                 "cu_seqlens must be int32 [N+1] with B == 1");
+            if (!cu->is_cuda()) check_offsets(*cu, T);
+            n_seq = cu->numel() - 1;
+        }
+        check_states(h0, "initial_state");
+        const at::Device dev = q->device();
+        NEED(dev.is_cuda(), "inputs must be on the GPU");
+        for (const at::Tensor *t : {k, v, g, h0}) NEED(!t || t->device() == dev, "all tensors must be on one GPU");
+        for (const at::Tensor *t : others) NEED(!t || t->device() == dev, "all tensors must be on one GPU");
+        NEED(!cu || !cu->is_cuda() || cu->device() == dev, "all tensors must be on one GPU");
+    }
+    void check_states(const at::Tensor *x, const char *name) const {
+        NEED(!x || (x->dim() == 4 && x->size(0) == n_seq && x->size(1) == H_v && x->size(2) == K && x->size(3) == V &&
+                    x->is_floating_point()),
+             name, " must be [N,H_v,K,V]");
+    }
+    // false: a Python error is set
+    template <typename Args> bool fill(Args &a, Held &held) const {
+        a.B = B, a.T = T, a.H_q = H_q, a.H_v = H_v, a.K = K, a.V = V, a.n_seq = n_seq;
+        const Rows qr = rows(*q, held), kr = rows(*k, held), vr = rows(*v, held);
+        a.q = qr.data, a.q_row = qr.row, a.q_batch = qr.batch;
+        a.k = kr.data, a.k_row = kr.row, a.k_batch = kr.batch;
+        a.v = vr.data, a.v_row = vr.row, a.v_batch = vr.batch;
+        a.dtype = element(q->scalar_type());
+        a.scale = (float)(1.0 / std::sqrt((double)K));
+        if (scale != Py_None) a.scale = (float)PyFloat_AsDouble(scale);
+        a.segment_chunks = (int32_t)std::min<long>(PyLong_AsLong(segment_chunks), 1 << 30);
+        a.g = floats(*g, held), a.g_per_head = g->dim() == 1;
+        a.initial_state = states_of(h0, held);
+        a.cu_seqlens = indices(cu, q->device(), held);
+        return !PyErr_Occurred();
+    }
+};
+
+// la_fwd(q, k, v, g, scale, initial_state, cu_seqlens, output_final_state, output_dtype, segment_chunks)
+PyObject *la_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 10)) return nullptr;
+    Linear x = {&tensor(a[0], "q"), &tensor(a[1], "k"), &tensor(a[2], "v"), &tensor(a[3], "g"),
+                optional_tensor(a[5], "initial_state"), optional_tensor(a[6], "cu_seqlens"), a[4], a[9]};
+    x.check({});
+    const at::ScalarType type = dtype_of(a[8], at::ScalarType::Undefined, "output_dtype");
+    const int last = PyObject_IsTrue(a[7]);
+    if (last < 0) return nullptr;
+    const at::Device dev = x.q->device();
+    const c10::DeviceGuard guard(dev);
+    Held held;
+    gdr_la_fwd_args p = {};
+    if (!x.fill(p, held)) return nullptr;
+    const at::Tensor o = at::empty(x.v->sizes(), x.v->options().dtype(type));
+    at::Tensor hT, ws;
+    if (last) hT = at::empty({x.n_seq, x.H_v, x.K, x.V}, x.v->options().dtype(at::kFloat));
+    p.out_dtype = element(type), p.o = o.data_ptr(), p.final_state = last ? static_cast<float *>(hT.data_ptr()) : nullptr;
+    if (!workspace(gdr_la_fwd_workspace, "gdr_la_fwd_workspace", p, o, ws)) return nullptr;
+    if (!launch(gdr_la_fwd, "gdr_la_fwd", p, dev, {})) return nullptr;
+    return wrap_all({&o, &hT});
+    END_HANDLE_TH_ERRORS
+}
+
+// la_bwd(q, k, v, g, do, dht, scale, initial_state, cu_seqlens, grad_dtype, segment_chunks)
+PyObject *la_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 11)) return nullptr;
+    Linear x = {&tensor(a[0], "q"), &tensor(a[1], "k"), &tensor(a[2], "v"), &tensor(a[3], "g"),
+                optional_tensor(a[7], "initial_state"), optional_tensor(a[8], "cu_seqlens"), a[6], a[10]};
+    const at::Tensor *dht = optional_tensor(a[5], "dht");
+    at::Tensor dout = tensor(a[4], "do");
+    x.check({&dout, dht});
+    x.check_states(dht, "dht");
+    NEED(dout.sizes() == x.v->sizes() && dout.is_floating_point(), "do must be [B,T,H_v,V]");
+    const at::ScalarType type = dtype_of(a[9], x.q->scalar_type(), "grad_dtype");
+    const at::Device dev = x.q->device();
+    const c10::DeviceGuard guard(dev);
+    at::Tensor wide[3];  // bf16 inputs with a gradient in fp32 are taken in fp32
+    if (dout.scalar_type() != x.q->scalar_type()) {
+        if (x.q->scalar_type() == at::kBFloat16) {
+            wide[0] = x.q->to(at::kFloat), wide[1] = x.k->to(at::kFloat), wide[2] = x.v->to(at::kFloat);
+            x.q = &wide[0], x.k = &wide[1], x.v = &wide[2];
+        }
+        dout = dout.to(x.q->scalar_type());
+    }
+    Held held;
+    gdr_la_bwd_args p = {};
+    if (!x.fill(p, held)) return nullptr;
+    const at::TensorOptions grads = x.q->options().dtype(type), whole = x.q->options().dtype(at::kFloat);
+    const at::Tensor dq = at::empty(x.q->sizes(), grads), dk = at::empty(x.q->sizes(), grads), dv = at::empty(x.v->sizes(), grads),
+                     dg = at::empty(x.g->sizes(), whole);
+    at::Tensor dh0, ws;
+    if (x.h0) dh0 = at::empty(x.h0->sizes(), whole);
+    p.grad_dtype = element(type), p.dout = packed(dout, held), p.dht = states_of(dht, held);
+    p.dq = dq.data_ptr(), p.dk = dk.data_ptr(), p.dv = dv.data_ptr(), p.dg = static_cast<float *>(dg.data_ptr());
+    p.dh0 = x.h0 ? static_cast<float *>(dh0.data_ptr()) : nullptr;
+    if (!workspace(gdr_la_bwd_workspace, "gdr_la_bwd_workspace", p, dq, ws)) return nullptr;
+    if (!launch(gdr_la_bwd, "gdr_la_bwd", p, dev, {})) return nullptr;
+    return wrap_all({&dq, &dk, &dv, &dg, &dh0});
+    END_HANDLE_TH_ERRORS
+}
+
 // x [..., C] as rows of C, with the elements between them; copied where it is no such rows
 struct Matrix {
     const void *data;
@@ -436,52 +602,92 @@ Matrix matrix(const at::Tensor &x, int64_t M, int64_t C, Held &held) {
     return {x.data_ptr(), row};
 }
 
+// What both directions of the group norm check, and the arguments they share
+struct Norm {
+    const at::Tensor *x, *weight, *bias, *gate;
+    PyObject *groups, *eps, *activation, *center;
+    // false: a Python error is set
+    template <typename Args> bool fill(Args &p, const at::Tensor *dout, Held &held) const {
+        p.groups = PyLong_AsLongLong(groups), p.eps = (float)PyFloat_AsDouble(eps);
+        p.activation = (int32_t)PyLong_AsLong(activation), p.center = PyObject_IsTrue(center);
+        if (PyErr_Occurred()) return false;
+        NEED(x->dim() >= 1 && element(x->scalar_type()) >= 0, "x must be [..., C], bfloat16 or float32");
+        p.C = x->size(-1);
+        NEED(p.groups >= 1 && p.C >= 1 && p.C % p.groups == 0, "the channels of x must be a multiple of num_groups");
+        p.M = x->numel() / p.C;
+        for (const at::Tensor *t : {weight, bias})
+            NEED(!t || (t->dim() == 1 && t->size(0) == p.C && t->is_floating_point()), "weight and bias must be [C]");
+        NEED(!gate || (gate->sizes() == x->sizes() && element(gate->scalar_type()) >= 0),
+             "gate must be like x, bfloat16 or float32");
+        NEED(!dout || (dout->sizes() == x->sizes() && element(dout->scalar_type()) >= 0),
+             "dout must be like x, bfloat16 or float32");
+        const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+        const at::Device dev = x->device();
+        NEED(dev.is_cuda(), "inputs must be on the GPU");
+        for (const at::Tensor *t : {x, weight, bias, gate, dout}) {
+            if (!t) continue;
+            NEED(t->device() == dev, "all tensors must be on one GPU");
+            NEED(!forward || !t->unsafeGetTensorImpl()->autograd_meta() || !t->_fw_grad(0).defined(),
+                 "group_norm has no tangent in forward mode");
+        }
+        const c10::DeviceGuard guard(dev);
+        const Matrix xm = matrix(*x, p.M, p.C, held), zm = gate ? matrix(*gate, p.M, p.C, held) : Matrix{nullptr, 0};
+        p.x = xm.data, p.x_row = xm.row, p.gate = zm.data, p.gate_row = zm.row;
+        p.x_dtype = element(x->scalar_type()), p.gate_dtype = gate ? element(gate->scalar_type()) : p.x_dtype;
+        p.weight = weight ? floats(*weight, held) : nullptr, p.bias = bias ? floats(*bias, held) : nullptr;
+        return true;
+    }
+};
+
 // norm(x, groups, weight, bias, gate, eps, activation, center, output_dtype)
 PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (!count(n, 9)) return nullptr;
-    const at::Tensor &x = tensor(a[0], "x"), *weight = optional_tensor(a[2], "weight"), *bias = optional_tensor(a[3], "bias"),
-                     *gate = optional_tensor(a[4], "gate");
-    gdr_norm_fwd_args p = {};
-    p.groups = PyLong_AsLongLong(a[1]);
-    if (p.groups == -1 && PyErr_Occurred()) return nullptr;
-    p.eps = (float)PyFloat_AsDouble(a[5]);
-    if (PyErr_Occurred()) return nullptr;
-    p.activation = (int32_t)PyLong_AsLong(a[6]);
-    p.center = PyObject_IsTrue(a[7]);
-    if (PyErr_Occurred()) return nullptr;
-    NEED(x.dim() >= 1 && element(x.scalar_type()) >= 0, "x must be [..., C], bfloat16 or float32");
-    p.C = x.size(-1);
-    NEED(p.groups >= 1 && p.C >= 1 && p.C % p.groups == 0, "the channels of x must be a multiple of num_groups");
-    p.M = x.numel() / p.C;
-    for (const at::Tensor *t : {weight, bias})
-        NEED(!t || (t->dim() == 1 && t->size(0) == p.C && t->is_floating_point()), "weight and bias must be [C]");
-    NEED(!gate || (gate->sizes() == x.sizes() && element(gate->scalar_type()) >= 0),
-         "gate must be like x, bfloat16 or float32");
-    const at::ScalarType type = a[8] == Py_None               ? (gate ? gate : &x)->scalar_type()
-                                : THPDtype_Check(a[8]) ? reinterpret_cast<THPDtype *>(a[8])->scalar_type
-                                                       : at::ScalarType::Undefined;
-    NEED(element(type) >= 0, "output_dtype must be bfloat16 or float32");
-    const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
-    const at::Device dev = x.device();
-    NEED(dev.is_cuda(), "inputs must be on the GPU");
-    for (const at::Tensor *t : {&x, weight, bias, gate}) {
-        if (!t) continue;
-        NEED(t->device() == dev, "all tensors must be on one GPU");
-        NEED(!forward || !t->unsafeGetTensorImpl()->autograd_meta() || !t->_fw_grad(0).defined(),
-             "group_norm has no tangent in forward mode");
-    }
-    const c10::DeviceGuard guard(dev);
-    at::Tensor out = at::empty(x.sizes(), x.options().dtype(type));
+    const Norm x = {&tensor(a[0], "x"), optional_tensor(a[2], "weight"), optional_tensor(a[3], "bias"),
+                    optional_tensor(a[4], "gate"), a[1], a[5], a[6], a[7]};
     Held held;
-    const Matrix xm = matrix(x, p.M, p.C, held), zm = gate ? matrix(*gate, p.M, p.C, held) : Matrix{nullptr, 0};
-    p.x = xm.data, p.x_row = xm.row, p.gate = zm.data, p.gate_row = zm.row;
-    p.x_dtype = element(x.scalar_type()), p.out_dtype = element(type);
-    p.gate_dtype = gate ? element(gate->scalar_type()) : p.x_dtype;
-    p.weight = weight ? floats(*weight, held) : nullptr, p.bias = bias ? floats(*bias, held) : nullptr;
-    p.out = out.data_ptr();
+    gdr_norm_fwd_args p = {};
+    const at::ScalarType type = dtype_of(a[8], (x.gate ? x.gate : x.x)->scalar_type(), a[8] == Py_None ? "x and gate" : "output_dtype");
+    if (!x.fill(p, nullptr, held)) return nullptr;
+    const at::Device dev = x.x->device();
+    const c10::DeviceGuard guard(dev);
+    const at::Tensor out = at::empty(x.x->sizes(), x.x->options().dtype(type));
+    p.out_dtype = element(type), p.out = out.data_ptr();
     if (!launch(gdr_group_norm, "gdr_group_norm", p, dev, {})) return nullptr;
     return THPVariable_Wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// norm_bwd(x, groups, dout, weight, bias, gate, eps, activation, center, weight_grads)
+PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 10)) return nullptr;
+    const Norm x = {&tensor(a[0], "x"), optional_tensor(a[3], "weight"), optional_tensor(a[4], "bias"),
+                    optional_tensor(a[5], "gate"), a[1], a[6], a[7], a[8]};
+    const at::Tensor &dout = tensor(a[2], "dout");
+    const int sums = PyObject_IsTrue(a[9]);
+    if (sums < 0) return nullptr;
+    Held held;
+    gdr_norm_bwd_args p = {};
+    if (!x.fill(p, &dout, held)) return nullptr;
+    const at::Device dev = x.x->device();
+    const c10::DeviceGuard guard(dev);
+    const at::TensorOptions whole = x.x->options().dtype(at::kFloat);
+    const at::Tensor dx = at::empty(x.x->sizes(), x.x->options());
+    at::Tensor dz, dw, db, ws;
+    if (x.gate) dz = at::empty(x.x->sizes(), x.gate->options());
+    if (x.weight && sums) dw = at::empty({p.C}, whole);
+    if (x.bias && sums) db = at::empty({p.C}, whole);
+    p.out_dtype = element(dout.scalar_type());
+    p.dout = dout.is_contiguous() ? dout.data_ptr() : held.keep(dout.contiguous()).data_ptr();
+    p.dx = dx.data_ptr(), p.dgate = dz.defined() ? dz.data_ptr() : nullptr;
+    p.dweight = dw.defined() ? static_cast<float *>(dw.data_ptr()) : nullptr;
+    p.dbias = db.defined() ? static_cast<float *>(db.data_ptr()) : nullptr;
+    if ((dw.defined() || db.defined()) &&
+        !workspace(gdr_group_norm_bwd_workspace, "gdr_group_norm_bwd_workspace", p, dx, ws))
+        return nullptr;
+    if (!launch(gdr_group_norm_bwd, "gdr_group_norm_bwd", p, dev, {})) return nullptr;
+    return wrap_all({&dx, &dw, &db, &dz});
     END_HANDLE_TH_ERRORS
 }
 
@@ -504,10 +710,13 @@ PyMethodDef methods[] = {{"connect", (PyCFunction)(void (*)(void))connect, METH_
                          {"la_step", (PyCFunction)(void (*)(void))la_step, METH_FASTCALL, nullptr},
                          {"tree", (PyCFunction)(void (*)(void))tree, METH_FASTCALL, nullptr},
                          {"accept", (PyCFunction)(void (*)(void))accept, METH_FASTCALL, nullptr},
+                         {"la_fwd", (PyCFunction)(void (*)(void))la_fwd, METH_FASTCALL, nullptr},
+                         {"la_bwd", (PyCFunction)(void (*)(void))la_bwd, METH_FASTCALL, nullptr},
+                         {"norm_bwd", (PyCFunction)(void (*)(void))norm_bwd, METH_FASTCALL, nullptr},
                          {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, nullptr},
                          {"copy", (PyCFunction)(void (*)(void))copy, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdr_torch", "Checked calls of libgdr's operators on a pool of states.", -1,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdr_torch", "Checked calls of libgdr's operators.", -1,
                       methods};
 
 }  // namespace

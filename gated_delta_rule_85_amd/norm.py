@@ -12,7 +12,6 @@ import torch
 from torch.autograd import forward_ad
 
 from . import _lib
-from .api import _DT, _ptr
 from .pool import _gdr_torch
 
 _ACT = {None: _lib.ACT_NONE, "silu": _lib.ACT_SILU, "sigmoid": _lib.ACT_SIGMOID}
@@ -24,61 +23,12 @@ def _activation(name):
     return _ACT[name]
 
 
-def _matrix(x, C):
-    """x [..., C] as rows [M, C] with one distance between them (a copy where it has none)."""
-    x = x.reshape(-1, C)
-    if C > 1 and x.stride(1) != 1:
-        x = x.contiguous()
-    return x, (x.stride(0) if x.shape[0] > 1 else 0)
-
-
 def group_norm_bwd(x, num_groups, dout, weight=None, bias=None, gate=None, eps=1e-5, *, activation="silu", center=True,
                    weight_grads=True):
     """Low-level backward.  Returns ``(dx, dweight, dbias, dgate)``: dx and dgate in the dtypes
     of x and gate, dweight and dbias float32; None for what was not given (dweight and dbias
     also without ``weight_grads``).  ``dout`` may be bfloat16 or float32."""
-    act, dev, C = _activation(activation), x.device, x.shape[-1]
-    if dout.shape != x.shape or dout.dtype not in _DT:
-        raise ValueError("dout must be like x, bfloat16 or float32")
-    if gate is not None and gate.shape != x.shape:
-        raise ValueError("gate must be like x, bfloat16 or float32")
-    for t in (x, gate):
-        if t is not None and t.dtype not in _DT:
-            raise ValueError("x and gate must be bfloat16 or float32")
-    for t in (weight, bias):
-        if t is not None and (t.shape != (C,) or not t.is_floating_point()):
-            raise ValueError("weight and bias must be [C]")
-    if num_groups < 1 or C < 1 or C % num_groups:
-        raise ValueError("the channels of x must be a multiple of num_groups")
-    if not x.is_cuda:
-        raise ValueError("inputs must be on the GPU")
-    for t in (dout, weight, bias, gate):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one GPU")
-    with torch.cuda.device(dev):
-        a = _lib.NormBwdArgs()
-        xm, a.x_row = _matrix(x, C)
-        zm, a.gate_row = (None, 0) if gate is None else _matrix(gate, C)
-        dout = dout.contiguous()
-        w, b = (None if t is None else t.float().contiguous() for t in (weight, bias))
-        dx, dz = torch.empty(x.shape, dtype=x.dtype, device=dev), None
-        if gate is not None:
-            dz = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-        dw = torch.empty(C, dtype=torch.float32, device=dev) if weight is not None and weight_grads else None
-        db = torch.empty(C, dtype=torch.float32, device=dev) if bias is not None and weight_grads else None
-        a.M, a.C, a.groups = xm.shape[0], C, num_groups
-        a.x_dtype, a.out_dtype = _DT[x.dtype], _DT[dout.dtype]
-        a.gate_dtype = a.x_dtype if gate is None else _DT[gate.dtype]
-        a.activation, a.center, a.eps = act, int(center), float(eps)
-        a.x, a.weight, a.bias, a.gate, a.dout = _ptr(xm), _ptr(w), _ptr(b), _ptr(zm), _ptr(dout)
-        a.dx, a.dgate, a.dweight, a.dbias = _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db)
-        ws = None
-        if dw is not None or db is not None:
-            nbytes = _lib.group_norm_bwd_workspace(a)
-            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
-        _lib.group_norm_bwd(a, torch.cuda.current_stream(dev).cuda_stream)
-    return dx, dw, db, dz
+    return _gdr_torch.norm_bwd(x, num_groups, dout, weight, bias, gate, eps, _activation(activation), center, weight_grads)
 
 
 class _GroupNorm(torch.autograd.Function):

@@ -5,7 +5,11 @@ most; an fp32 one, and a bf16 one before its rounding, is off by a few fp32 roun
 of the exponential, 2^-20 of the values it is made of.  dx is a difference of terms of the size of
 rstd dn, and each of its errors is relative to that; n is rstd times a difference of values of
 the size of x, so that its own error is 2^-23 rstd |x|, which enters dx as a factor of rstd dn
-three times (n, the mean of dn n, and the values dn of an activation of n).
+three times (n, the mean of dn n, and the values dn of an activation of n).  dweight and dbias are
+sums over the tokens of terms t, each off by 2^-20 |t| at most, so that a sum is off by 2^-20 of the
+sum of |t|.  The sum itself may be any part of that, since the terms' signs differ: sqrt(M) |dbias|
+is of the size of sum |t| only on the average over many channels.  With a single channel a sum of
+0.033 of 300 terms of size one was off by 1.2e-6: 4e-5 of the sum, 2^-28 of the terms.
 """
 import math
 
@@ -57,11 +61,20 @@ def exact(a, G, act, center, dout=None, eps=1e-5):
     dn = (dy * w).reshape(M, G, -1)
     nn = n.reshape(M, G, -1)
     dx = rstd * (dn - nn * (dn * nn).mean(-1, keepdim=True) - (dn.mean(-1, keepdim=True) if center else 0))
-    return out, dx.reshape(M, C), (dy * n).sum(0), dy.sum(0), dout * y * slope if gated else None, \
+    return out, dx.reshape(M, C), Sum(dy * n), Sum(dy), dout * y * slope if gated else None, \
         (rstd * dn.abs().amax(-1, keepdim=True).expand(dn.shape) * (1 + size * rstd)).norm().item()
 
 
+class Sum:
+    """A sum over the tokens, and the norm of the sums of its terms' sizes."""
+
+    def __init__(self, terms):
+        self.value, self.scale = terms.sum(0), terms.abs().sum(0).norm().item()
+
+
 def check(got, want, dtype, what, scale=0.0):
+    if isinstance(want, Sum):
+        want, scale = want.value, want.scale
     assert got.dtype == dtype, what
     d, n = (got.double().reshape(want.shape) - want).norm().item(), want.norm().item()
     tol = ROUNDED[dtype] * n + COMPUTED * max(n, scale)
@@ -85,10 +98,9 @@ def test_forward_and_backward(gdr, D, act, center):
             check(got, y, out, "out")
             g = gdr.group_norm_bwd(a["x"], G, dout, a["weight"], a["bias"], a["gate"], activation=act, center=center)
             check(g[0], dx, x, "dx", scale)
-            # sums over the tokens of terms whose signs differ
-            check(g[1], dw, F32, "dweight", math.sqrt(M) * dw.norm().item())
+            check(g[1], dw, F32, "dweight")
             if a["bias"] is not None:
-                check(g[2], db, F32, "dbias", math.sqrt(M) * db.norm().item())
+                check(g[2], db, F32, "dbias")
             if gate is not None:
                 check(g[3], dz, gate, "dgate")
 
@@ -137,7 +149,7 @@ def test_rows_of_wider_tensors(gdr, D):
         g = gdr.group_norm_bwd(x, G, dout, w, gate=gate)
         _, dx, dw, _, dz, scale = exact(a, G, "silu", True, dout)
         check(g[0], dx, BF, "dx", scale)
-        check(g[1], dw, F32, "dweight", 6 * dw.norm().item())
+        check(g[1], dw, F32, "dweight")
 
 
 def test_autograd_and_differences(gdr):
