@@ -16,6 +16,7 @@ struct LaSeqs {
     int64_t g_tok;      // floats between the gates of two tokens (0: one gate per head)
     int64_t T;
     int n_seq, Hv, seg_chunks;
+    int n_seg;          // segments of every sequence (without cu)
 };
 
 // tokens [bos, eos) of sequence j among [0, B T); offsets are clamped to [0, T], an end before
@@ -29,29 +30,47 @@ __device__ __forceinline__ void la_bounds(const LaSeqs &s, int j, int64_t &bos, 
         eos = bos + s.T;
     }
 }
-// place of a sequence's first segment: a sequence of n tokens takes n / seg_tokens + 1 places at
-// most, and the sequences' places do not meet
-__host__ __device__ __forceinline__ int la_first(int64_t bos, int j, int64_t seg_tokens) {
-    return (int)(bos / seg_tokens) + j;
+// place of a sequence's first segment.  Packed: a sequence of n tokens takes n / seg_tokens + 1 places
+// at most, and the sequences' places do not meet
+__device__ __forceinline__ int la_first(const LaSeqs &s, int64_t bos, int j, int64_t seg_tokens) {
+    return s.cu ? (int)(bos / seg_tokens) + j : j * s.n_seg;
 }
-__host__ __device__ __forceinline__ int64_t la_slots(int64_t tokens, int64_t n_seq, int64_t seg_tokens) {
-    return tokens / seg_tokens + n_seq;
+inline int64_t la_segments(int64_t T, int64_t seg_tokens) { return T > seg_tokens ? (T + seg_tokens - 1) / seg_tokens : 1; }
+inline int64_t la_slots(bool packed, int64_t T, int64_t n_seq, int64_t seg_tokens) {
+    return packed ? T / seg_tokens + n_seq : n_seq * la_segments(T, seg_tokens);
 }
-// sequence and segment of a place (false: none)
+// sequence and segment of a place (false: none); of whole waves.  64 sequences are looked at in a step
 __device__ __forceinline__ bool la_place(const LaSeqs &s, int place, int &j, int &m) {
     const int64_t seg_tokens = (int64_t)s.seg_chunks * CH;
-    int lo = 0, hi = s.n_seq - 1;  // the last sequence whose first place is not past it
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        int64_t bos, eos;
-        la_bounds(s, mid, bos, eos);
-        if (la_first(bos, mid, seg_tokens) <= place) lo = mid; else hi = mid - 1;
+    if (!s.cu) {
+        j = place / s.n_seg, m = place - j * s.n_seg;
+        return true;
     }
+    int lo = 0;  // the last sequence whose first place is not past it
     int64_t bos, eos;
+    for (int n = s.n_seq; n > 1;) {
+        const int step = (n + 63) >> 6, at = lane_id() * step;
+        bool before = false;
+        if (at < n) {
+            la_bounds(s, lo + at, bos, eos);
+            before = la_first(s, bos, lo + at, seg_tokens) <= place;
+        }
+        const int skip = max((int)__popcll(__ballot(before)) - 1, 0) * step;
+        lo += skip, n = min(step, n - skip);
+    }
     la_bounds(s, lo, bos, eos);
     j = lo;
-    m = place - la_first(bos, lo, seg_tokens);
+    m = place - la_first(s, bos, lo, seg_tokens);
     return m >= 0 && (m == 0 || m * seg_tokens < eos - bos);
+}
+
+// Work of a workgroup: `share` neighbours, which read the same q and k, on one XCD's L2, and the XCDs by
+// turns, since some places of packed sequences hold no segment: 32768 tokens of 8 heads in 33 places of 8
+// workgroups, the last place empty, took 219 us with neighbouring places on an XCD (33 workgroups for
+// the 32 compute units of seven XCDs), and 139 without it
+__device__ __forceinline__ int la_work(int id, int total, int share) {
+    const int k = id >> 3, turn = k / share;
+    return (turn + 1) * share * 8 > total ? id : (turn * 8 + (id & 7)) * share + k % share;
 }
 
 // One scan: o_t = out_scale S_t^T q_t with S_t = e^g S + in_scale k_t v_t^T over every sequence
@@ -84,6 +103,7 @@ struct LaParams {
     LaJob job[3];
     int n_jobs, n_cb;     // jobs and blocks of 64 columns in the grid
     int split;            // workgroups take a segment each, from the border states
+    int share;            // neighbours in the grid that read the same q and k (launch)
     int64_t tokens;       // B T
 };
 
@@ -106,8 +126,8 @@ struct LaGates {
     float *dg;               // [tokens][Hv], or per-head partial sums [places][Hv] (s.g_tok 0)
 };
 
-// out: type of the jobs' o; dots: whether they sum dots
-hipError_t launch_la_scan(Dt dt, Dt out, int KD, bool dots, const LaParams &p, int items, hipStream_t s);
+// out: type of the jobs' o; last: the type that it is rounded to in the end; dots: whether they sum dots
+hipError_t launch_la_scan(Dt dt, Dt out, Dt last, int KD, bool dots, const LaParams &p, int items, hipStream_t s);
 // end states of segments only, into the border after (rev: before) each, with their decays
 hipError_t launch_la_states(Dt dt, int KD, const LaParams &p, int items, hipStream_t s);
 hipError_t launch_la_carry(const LaCarry &p, hipStream_t s);

@@ -21,21 +21,35 @@ bool wide(int32_t dtype, int64_t units) { return dtype == GDR_BF16 && units >= U
 
 // Chunks per segment, or 0: no split.  N chunks a sequence, `units` sequences and heads of `blocks` times
 // 64 columns, `scans` scans and `states` scans without output.  In the time of a chunk of 128 columns on every
-// compute unit (4.4 us): a chunk of 64 columns takes 0.6, one without output 0.5 of a workgroup that
-// shares its compute unit; a workgroup's start 1 to 3, the launches and the carry between the two
-// 3 and what the segments' states take.  Prefill of one sequence of 4096 tokens (32 heads of 128 columns):
-// 177 us unsplit, 144 / 109 / 107 with segments of 32 / 8 / 4; of 1024 tokens 50 unsplit, 58 with 4
-int64_t split_chunks(int32_t dtype, int64_t N, int64_t units, int64_t blocks, int64_t scans, int64_t states) {
+// compute unit (4.4 us): a chunk of 64 columns takes 0.6 (backwards 0.7), one without output 0.5 of a
+// workgroup that shares its compute unit; a workgroup's start 1 to 3, the launches and the carry
+// between the two 3 and what the segments' states take.  Prefill of one sequence of 4096 tokens (32
+// heads of 128 columns) takes 77 us split, 162 unsplit; backwards, 4 x 2048 tokens of 32 heads 406 us
+// with segments of 16 and 468 unsplit.
+// Of packed sequences the lengths are not known here: the time of one with all the tokens counts as much
+// as that of half of them with twice the mean length.
+int64_t split_chunks(int32_t dtype, int64_t N, int64_t n_seq, bool packed, int64_t heads, int64_t blocks, int64_t scans,
+                     int64_t states) {
+    if (N < 2) return 0;
+    const double half = scans > 1 ? 0.7 : 0.6;
     auto scan = [&](int64_t u, int64_t L) {
-        return blocks == 2 && wide(dtype, u) ? (double)cdiv(u, UNITS) * (L + 1) : 0.6 * (double)cdiv(u * blocks, UNITS) * (L + 1);
+        return blocks == 2 && wide(dtype, u) ? (double)cdiv(u, UNITS) * (L + 1) : half * (double)cdiv(u * blocks, UNITS) * (L + 1);
     };
-    double best = scans * scan(units, N);
+    auto time = [&](int64_t units, int64_t n, int64_t l) {  // n chunks each, segments of l
+        const int64_t S = cdiv(n, l);
+        if (S < 2) return scans * scan(units, n);
+        return scans * scan(S * units, l) + 0.5 * (double)cdiv(states * (S - 1) * units * blocks, 2 * UNITS) * (l + 3) + 3 + S / 16.0;
+    };
+    auto all = [&](int64_t l) {
+        return packed ? time(heads, N, l) + time(cdiv(n_seq, 2) * heads, cdiv(2 * N, n_seq + 1), l) : time(n_seq * heads, N, l);
+    };
+    const int64_t units = packed ? heads : n_seq * heads;
+    double best = all(N);
     int64_t L = 0;
     for (int64_t S = 2; S <= N && (S - 1) * units < 4 * UNITS; ++S) {
         const int64_t l = cdiv(N, S);
         if (cdiv(N, l) != S) continue;  // the segments of a smaller S
-        const double t = scans * scan(S * units, l) + 0.5 * (double)cdiv(states * (S - 1) * units * blocks, 2 * UNITS) * (l + 3) +
-                         3 + S / 16.0;
+        const double t = all(l);
         if (t < best) best = t, L = l;
     }
     return L;
@@ -75,16 +89,16 @@ template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
     p.n_seq = varlen ? a->n_seq : a->B;
     p.tokens = p.n_seq > 0 ? a->B * a->T : 0;
     p.group = (int)(a->H_v / a->H_q);
-    // packed sequences may all but be one
-    const int64_t nct = cdiv(a->T, CH), units = (varlen ? 1 : std::max<int64_t>(p.n_seq, 1)) * a->H_v;
+    const int64_t nct = cdiv(a->T, CH);
     int64_t L = a->segment_chunks ? a->segment_chunks
-                                  : split_chunks(a->dtype, nct, units, std::max(a->V, backward ? a->K : 0) / 64, backward ? 3 : 1, backward ? 2 : 1);
+                                  : split_chunks(a->dtype, nct, std::max<int64_t>(p.n_seq, 1), varlen, a->H_v,
+                                                 std::max(a->V, backward ? a->K : 0) / 64, backward ? 3 : 1, backward ? 2 : 1);
     p.split = L > 0 && L < nct;
     if (backward) L = L > 0 ? std::min<int64_t>(L, BORDER_CHUNKS) : BORDER_CHUNKS;
     if (!p.split && !backward) L = std::max<int64_t>(nct, 1);
     p.seg_chunks = (int)L;
     p.seg_tokens = L * CH;
-    p.places = la_slots(p.tokens, p.n_seq, p.seg_tokens);
+    p.places = la_slots(varlen, a->T, p.n_seq, p.seg_tokens);
     // 32-bit numbers of workgroups and work-items
     if (std::max(p.places, p.n_seq) * a->H_v * 16 >= (int64_t)1 << 23) return GDR_EINVAL;
     const bool whole = wide(a->dtype, (p.split ? p.places : p.n_seq) * a->H_v);
@@ -130,8 +144,12 @@ int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
 Dt type_of(int32_t t) { return t == GDR_BF16 ? Dt::BF16 : Dt::F32; }
 
 template <typename Args> LaSeqs sequences(const Args *a, const Plan &p) {
-    return {a->cu_seqlens, a->g, a->g_per_head ? 0 : a->H_v, a->T, (int)p.n_seq, (int)a->H_v, p.seg_chunks};
+    return {a->cu_seqlens, a->g, a->g_per_head ? 0 : a->H_v, a->T, (int)p.n_seq, (int)a->H_v, p.seg_chunks,
+            (int)la_segments(a->T, p.seg_tokens)};
 }
+
+// neighbours of a grid: the v heads, blocks of columns and jobs of a q/k head
+int neighbours(const Plan &p, const LaParams &l) { return std::min(p.group * l.n_cb * l.n_jobs, 8); }
 
 // launches bind to the timing stage open on this thread (launch_k): none is
 struct NoStage {
@@ -184,14 +202,15 @@ int gdr_la_fwd(const gdr_la_fwd_args *a, hipStream_t stream) {
     const Dt dt = type_of(a->dtype);
     if (pl.split) {
         J.decays = reinterpret_cast<float *>(ws + pl.off_decays_fwd);
-        p.n_cb = (int)(a->V / 64);
+        p.n_cb = (int)(a->V / 64), p.share = neighbours(pl, p);
         if (launch_la_states(dt, (int)a->K, p, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
         const LaCarry c = {p.s, border, J.decays, (int)(a->K * a->V), 0};
         if (launch_la_carry(c, stream) != hipSuccess) return GDR_ELAUNCH;
         p.n_cb = pl.n_cb_v;
     }
+    p.share = neighbours(pl, p);
     const int items = (int)(pl.split ? pl.places : pl.n_seq);
-    return launch_la_scan(dt, type_of(a->out_dtype), (int)a->K, false, p, items, stream) == hipSuccess ? GDR_OK : GDR_ELAUNCH;
+    return launch_la_scan(dt, type_of(a->out_dtype), type_of(a->out_dtype), (int)a->K, false, p, items, stream) == hipSuccess ? GDR_OK : GDR_ELAUNCH;
 }
 
 int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
@@ -253,6 +272,7 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
             f.W = V, f.in_scale = 1.f, f.init = a->initial_state, f.border = border_fwd, f.decays = decays_fwd;
             r = dv;
             r.decays = decays_rev;
+            p.share = neighbours(pl, p);
             if (launch_la_states(dt, K, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
             LaCarry c = {s, border_fwd, decays_fwd, K * V, 0};
             if (launch_la_carry(c, stream) != hipSuccess) return GDR_ELAUNCH;
@@ -261,14 +281,14 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
         }
         LaParams p = {};
         p.s = s, p.split = pl.split, p.tokens = pl.tokens;
-        p.n_jobs = 1, p.n_cb = pl.n_cb_k;
+        p.n_jobs = 1, p.n_cb = pl.n_cb_k, p.share = neighbours(pl, p);
         p.job[0] = dq;
-        if (launch_la_scan(dt, qt, V, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        if (launch_la_scan(dt, qt, gt, V, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
         p.job[0] = dk;
-        if (launch_la_scan(dt, qt, V, false, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
-        p.n_cb = pl.n_cb_v;
+        if (launch_la_scan(dt, qt, gt, V, false, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        p.n_cb = pl.n_cb_v, p.share = neighbours(pl, p);
         p.job[0] = dv;
-        if (launch_la_scan(dt, gt, K, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
+        if (launch_la_scan(dt, gt, gt, K, true, p, items, stream) != hipSuccess) return GDR_ELAUNCH;
         if (group > 1 && pl.tokens > 0) {
             if (launch_la_heads(static_cast<float *>(dq.o), a->dq, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
             if (launch_la_heads(static_cast<float *>(dk.o), a->dk, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;

@@ -13,7 +13,7 @@ __global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
     int64_t bos, eos;
     la_bounds(p.s, j, bos, eos);
     const int64_t seg_tokens = (int64_t)p.s.seg_chunks * CH;
-    const int n_seg = (int)((eos - bos + seg_tokens - 1) / seg_tokens), place = la_first(bos, j, seg_tokens);
+    const int n_seg = (int)((eos - bos + seg_tokens - 1) / seg_tokens), place = la_first(p.s, bos, j, seg_tokens);
     if (n_seg < 3) return;
     const int64_t stride = (int64_t)p.s.Hv * p.KV;
     float *s = p.border + ((int64_t)place * p.s.Hv + hv) * p.KV + (blockIdx.x - unit * per) * 1024 + 4 * threadIdx.x;

@@ -12,15 +12,20 @@
 // chunk's work, so that one barrier a chunk orders everything: in turn c a wave stores O of chunk
 // c - 1 with its P V, makes its tiles of P of chunk c and its columns of Q h, then h', while K, Q, V
 // and the gates of chunk c + 1 are copied global -> LDS (bf16: two buffers).  NW is 8 (128 columns:
-// half of the tiles of P a column) for bf16 inputs where that leaves a workgroup for every compute unit, else 4.
+// half of the tiles of P a column) for bf16 inputs where that leaves a workgroup for every compute
+// unit, else 4.  Where the LDS has room (KS 2: bf16 in and out, no dots), 8 waves take these 64 columns
+// too, in pairs with half of the rows of S each, so that a SIMD has two waves: a wave's part of Q h
+// for its partner's rows of the chunk goes through LDS (16 KB a chunk), and P V is split by those
+// rows.  Two prompts of 8 heads of 64 columns, 2048 tokens: 73 us in place of 87; 4 x 4096 tokens of
+// 32 heads of 128: 170 in place of 183.
 //
 // rev: row r of a chunk is its r-th token from the end, and a row's gate is the next token's, so
 // that the same code scans from the last token to the first.
 //
 // Precision: q, k and v in bf16 are exact operands.  h, P and the decayed V are fp32 and enter the
 // bf16 matrix instructions in pieces of 8 bits each, x = hi + mid + lo to 2^-25 or hi + mid to
-// 2^-17.  The state always takes three.  A bf16 output takes two of h and P: its own rounding is
-// 2^-9.  An fp32 output, and the sums that gate gradients are differences of, take three.  fp32
+// 2^-17.  The state always takes three.  A bf16 output, or one that is rounded to bf16 after its sum
+// over heads, takes two of h and P: its own rounding is 2^-9.  An fp32 output, and the sums that gate gradients are differences of, take three.  fp32
 // inputs use the fp32 matrix instruction.
 #include "gdr_la.hpp"
 
@@ -131,10 +136,10 @@ template <int N, int NP> __device__ __forceinline__ void mma_pieces(f32x4 *c, co
 }
 
 // ------------------------------------------------------------ LDS layout
-template <typename In, int KD, int NP, int NW, bool OUT> struct Lay {
+template <typename In, int KD, int NP, int NW, int KS, bool OUT> struct Lay {
     static constexpr bool BF = sizeof(In) == 2;
     // buffers: as many as the two workgroups of a compute unit without output, or the one with it, have room for
-    static constexpr int ES = sizeof(In), NB = !BF ? 1 : OUT ? 2 : 3, BW = 16 * NW;
+    static constexpr int ES = sizeof(In), NB = !BF ? 1 : OUT ? 2 : 3, BW = 16 * NW / KS;
     static constexpr int KROW = KD * ES, VROW = BW * ES, PROW = CH * ES;
     static constexpr int KT = CH * KROW, VT = CH * VROW;
     static constexpr int OFF_K = 0, OFF_V = KT, OFF_Q = KT + VT, BUF = KT + VT + (OUT ? KT : 0);
@@ -144,7 +149,8 @@ template <typename In, int KD, int NP, int NW, bool OUT> struct Lay {
     static constexpr int OFF_T = OFF_S + (OUT ? 2 * NW * CH * 4 : 0);  // gate tables of two chunks (without output: of each wave)
     static constexpr int GT = (OUT ? 8 : 3) * CH;                    // floats of one
     static constexpr int OFF_G = OFF_T + (OUT ? 2 : NW) * GT * 4;    // gates of four chunks
-    static constexpr int BYTES = OFF_G + 4 * CH * 4;
+    static constexpr int OFF_X = OFF_G + 4 * CH * 4;                 // of two chunks: what a wave adds to its partner's rows
+    static constexpr int BYTES = OFF_X + (KS > 1 ? 2 * NW * 2048 : 0);
     static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
     using SK = Swz<KROW, KeyKQ>;
     using SV = Swz<VROW, typename std::conditional<VROW == 128, KeyVP, KeyKQ>::type>;
@@ -201,14 +207,15 @@ __device__ __forceinline__ float sum_rows(f32x4 x) {
 
 // ------------------------------------------------------- a workgroup's part
 // Out: void for the end states of segments alone; DOTS: LaJob's sums with e
-template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct Scan {
+template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> struct Scan {
     static constexpr bool OUT = !std::is_void<Out>::value;
-    using Y = Lay<In, KD, NP, NW, OUT>;
+    using Y = Lay<In, KD, NP, NW, KS, OUT>;
     using SK = typename Y::SK;
     using SV = typename Y::SV;
     using SP = typename Y::SP;
     using X = typename Ops<In>::X;
-    static constexpr int ES = Y::ES, BW = Y::BW, RT = KD / 16, U = KD / 32;  // tiles of 16 and of 32 rows of h
+    static constexpr int ES = Y::ES, BW = Y::BW, RT = KD / 16 / KS, U = KD / 32;  // tiles of 16 rows of h on a wave; of 32 rows of all of it
+    static_assert(KS == 1 || (KS == 2 && OUT && !DOTS), "");
 
     const LaParams &p;
     const LaJob &J;
@@ -217,6 +224,10 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
     int64_t bos;
     bool rev, starts, ends;
     int l, n16, g, w;
+    // the wave's columns 16 ct .. and rows row0 .. of h, the part-th of KS
+    __device__ __forceinline__ int ct() const { return KS == 1 ? w : w % (NW / KS); }
+    __device__ __forceinline__ int part() const { return KS == 1 ? 0 : w / (NW / KS); }
+    __device__ __forceinline__ int row0() const { return part() * (KD / KS); }
 
     __device__ __forceinline__ Scan(const LaParams &p_, int job, char *lds_) : p(p_), J(p_.job[job]), lds(lds_) {}
 
@@ -228,7 +239,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         la_bounds(p.s, j, bos, eos);
         rev = J.rev;
         len = (int)(eos - bos), nc = (len + CH - 1) / CH;
-        first_place = la_first(bos, j, (int64_t)p.s.seg_chunks * CH);
+        first_place = la_first(p.s, bos, j, (int64_t)p.s.seg_chunks * CH);
         const int n_seg = p.split ? max(1, (nc + p.s.seg_chunks - 1) / p.s.seg_chunks) : 1;
         const int c_lo = p.split ? m * p.s.seg_chunks : 0, c_hi = p.split ? min(nc, c_lo + p.s.seg_chunks) : nc;
         n_it = c_hi - c_lo, c_first = rev ? c_hi - 1 : c_lo;
@@ -245,12 +256,12 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
     __device__ __forceinline__ int64_t first_row(int64_t row, int64_t batch) const { return p.s.cu ? bos * row : (int64_t)j * batch; }
 
     // ----------------------------------------------------------------- states
-    // h[t][i]: row slot_base(t, g) + i, column 16 w + n16 of the block
+    // h[t][i]: row row0 + slot_base(t, g) + i, column 16 ct + n16 of the block
     __device__ __forceinline__ void load_state(const float *s, f32x4 (&h)[RT]) const {
-        const int col = cb * BW + 16 * w + n16;
+        const int col = cb * BW + 16 * ct() + n16;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const int r = slot_base(t, g);
+            const int r = row0() + slot_base(t, g);
             if (J.trans) {
                 h[t] = *glb(reinterpret_cast<const f32x4 *>(s + (int64_t)col * KD + r));
             } else {
@@ -260,10 +271,10 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         }
     }
     __device__ __forceinline__ void store_state(float *s, const f32x4 (&h)[RT], float f) const {
-        const int col = cb * BW + 16 * w + n16;
+        const int col = cb * BW + 16 * ct() + n16;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const int r = slot_base(t, g);
+            const int r = row0() + slot_base(t, g);
             if (J.trans) {
                 *glb(reinterpret_cast<f32x4 *>(s + (int64_t)col * KD + r)) = f * h[t];
             } else {
@@ -372,7 +383,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
     static __device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
 
     // V^T of this wave's columns and keys 32 ip ..
-    __device__ __forceinline__ X values(const char *b, int ip) const { return kt8<In, SV>(b + Y::OFF_V, 32 * ip, 16 * w, 4); }
+    __device__ __forceinline__ X values(const char *b, int ip) const { return kt8<In, SV>(b + Y::OFF_V, 32 * ip, 16 * ct(), 4); }
     // those, decayed to the chunk's end
     struct Ends {
         f32x4 e[2][2];
@@ -401,7 +412,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
 #pragma unroll
         for (int i = 0; i < N4; ++i) {
             const int t = first + i;
-            x.k[i] = kt8<In, SK>(b + Y::OFF_K, 32 * ip, 32 * (t >> 1) + 4 * (t & 1), 8);
+            x.k[i] = kt8<In, SK>(b + Y::OFF_K, 32 * ip, row0() + 32 * (t >> 1) + 4 * (t & 1), 8);
         }
         return x;
     }
@@ -477,7 +488,9 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             }
         }
     }
-    // P of N row tiles from the first on, keys 32 ip ..
+    // P of N of this wave's own row tiles from the first on, keys 32 ip ..
+    // a wave's order of the chunk's row tiles: every KS-th is its own, the one after its partner's
+    __device__ __forceinline__ int row_tile(int i) const { return KS == 1 ? i : i ^ part(); }
     template <int N> struct Weights {
         Pieces<In, NP> p[N];
     };
@@ -485,7 +498,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         Weights<N> x;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int row = 16 * (first + i) + n16, off = SP::off(row, (32 * ip + 8 * g) * ES);
+            const int row = 16 * row_tile(KS * (first + i)) + n16, off = SP::off(row, (32 * ip + 8 * g) * ES);
             if constexpr (Y::BF) {
 #pragma unroll
                 for (int k = 0; k < NP; ++k) x.p[i].p[k] = *reinterpret_cast<const bf16x8 *>(P + k * Y::PPLANE + off);
@@ -535,15 +548,15 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         // a row's place: token 16 r + n16 of the chunk, columns 4g .. of this wave's.  Offsets within a
         // whole chunk; a shorter one's rows lie that much lower where rows run backwards
         const int64_t orow = (int64_t)p.s.Hv * J.W, at = c_first * (int64_t)CH;
-        const int in_block = cb * BW + 16 * w + 4 * g;
+        const int in_block = cb * BW + 16 * ct() + 4 * g;
         Out *o0 = reinterpret_cast<Out *>(J.o) + (bos + at) * orow + (int64_t)hv * J.W + in_block;
         const int64_t o_step = (rev ? -CH : CH) * orow;
         const In *e0 = nullptr;
         float *d0 = nullptr;
         uint32_t oo[4], eo[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int tok = token_of(16 * r + n16, CH);
+        for (int r = 0; r < 4; r += KS) {
+            const int tok = token_of(16 * row_tile(r) + n16, CH);
             oo[r] = (uint32_t)tok * (uint32_t)orow;
             if constexpr (DOTS) eo[r] = (uint32_t)tok * (uint32_t)J.e_row;
         }
@@ -566,8 +579,29 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         in4 e[4];
         auto place_of_scores = [&](int buf) { return lds + Y::OFF_P + buf * Y::PT; };
         // + P V
-        auto add_first = [&](const Weights<4> &x) { mma_pieces<4>(o, v[0], x.p); };   // keys 0 .. 31 of all rows
-        auto add_rest = [&](const Weights<2> &x) { mma_pieces<2>(o + 2, v[1], x.p); };  // the others
+        constexpr int OT = 4 / KS;  // this wave's own row tiles
+        auto add_to = [&](auto first, const X &y, const auto &x) {
+            if constexpr (KS == 1) {
+                mma_pieces<OT - first>(o + first, y, x.p);
+            } else {
+                f32x4 z[OT - first];
+#pragma unroll
+                for (int i = first; i < OT; ++i) z[i - first] = o[KS * i];
+                mma_pieces<OT - first>(z, y, x.p);
+#pragma unroll
+                for (int i = first; i < OT; ++i) o[KS * i] = z[i - first];
+            }
+        };
+        auto add_first = [&](const Weights<OT> &x) { add_to(std::integral_constant<int, 0>{}, v[0], x); };  // keys 0 .. 31 of all rows
+        auto add_rest = [&](const Weights<OT / 2> &x) { add_to(std::integral_constant<int, OT / 2>{}, v[1], x); };  // the others
+        // the partner's rows, of this wave's part of Q h, to the partner, and back
+        auto exchange = [&](int buf, int wave) { return reinterpret_cast<f32x4 *>(lds + Y::OFF_X) + ((buf * NW + wave) * 2) * 64 + l; };
+        auto give = [&](int buf) {
+            if constexpr (KS > 1) exchange(buf, w)[0] = o[1], exchange(buf, w)[64] = o[3];
+        };
+        auto take = [&](int buf) {
+            if constexpr (KS > 1) o[0] += exchange(buf, w ^ (NW / 2))[0], o[2] += exchange(buf, w ^ (NW / 2))[64];
+        };
         auto finish = [&](int it, int buf) {  // chunk `it`, its dots in place buf
             const int n = rows_of(chunk_of(it));
             if constexpr (DOTS) {
@@ -583,8 +617,8 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             }
             Out *oc = o0 + (rev && n < CH ? (n - CH) * orow : 0);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (16 * r + n16 < n) *glb(reinterpret_cast<out4 *>(oc + oo[r])) = __builtin_convertvector(o[r], out4);
+            for (int r = 0; r < 4; r += KS)
+                if (16 * row_tile(r) + n16 < n) *glb(reinterpret_cast<out4 *>(oc + oo[r])) = __builtin_convertvector(o[r], out4);
             o0 += o_step;
         };
         constexpr bool TIGHT = NP == 3 || !Y::BF;  // registers for a step less of P
@@ -605,12 +639,13 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             stage();
             // the last chunk's P V (in the first turn of zeros), with the reads for the tiles of P
             const char *last = place_of_scores(buf ^ 1);
-            const Weights<4> p0 = weights<4>(last, 0, 0);
-            Weights<2> p1;
-            if (!TIGHT) p1 = weights<2>(last, 2, 1);
+            const Weights<OT> p0 = weights<OT>(last, 0, 0);
+            Weights<OT / 2> p1;
+            if (!TIGHT) p1 = weights<OT / 2>(last, OT / 2, 1);
+            if (it > 0) take(buf ^ 1);
             stage();
             if (TIGHT) {
-                p1 = weights<2>(last, 2, 1);
+                p1 = weights<OT / 2>(last, OT / 2, 1);
                 add_first(p0);
                 stage();
             }
@@ -630,7 +665,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             X q[4];
             if (Y::BF)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) q[r] = query(b, r, 0);
+                for (int r = 0; r < 4; ++r) q[r] = query(b, row_tile(r), part() * (U / KS));
             score<NT>(sc, P, rt, kt);
             stage();
             // (Q h)^T: lane (token n16 of tile r, columns 4g ..)
@@ -640,19 +675,20 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = zero4();
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U / KS; ++u) {
+                const int at = part() * (U / KS) + u;
                 X next[4];
                 if (!Y::BF)  // (registers)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) q[r] = query(b, r, u);
-                if (u + 1 < U) {
+                    for (int r = 0; r < 4; ++r) q[r] = query(b, row_tile(r), at);
+                if (u + 1 < U / KS) {
                     if (Y::BF)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) next[r] = query(b, r, u + 1);
+                    for (int r = 0; r < 4; ++r) next[r] = query(b, row_tile(r), at + 1);
                 } else {
                     v[0] = values(b, 0), v[1] = values(b, 1), ends_here = ends_of(gt), k0 = keys(b, 0, 0);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) out[r] = gt[G_OUT + 16 * r + n16];
+                    for (int r = 0; r < 4; ++r) out[r] = gt[G_OUT + 16 * row_tile(r) + n16];
                 }
                 const Pieces<In, NP> hp = pieces8<In, NP>(h[2 * u], h[2 * u + 1]);
                 mma_each<4>(o, hp, q);
@@ -663,6 +699,7 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] *= out[r];
+            give(buf);
             add_chunk(b, gt, v, ends_here, k0, h);
             if (more_rt >= 0) score<1>(score_operands<1>(b, gt, more_rt, more_kt), P, more_rt, more_kt);
             if (w == 0) {
@@ -684,8 +721,9 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
         });
         if (n_it > 0) {
             const char *last = place_of_scores((n_it - 1) & 1);
-            add_first(weights<4>(last, 0, 0));
-            add_rest(weights<2>(last, 2, 1));
+            take((n_it - 1) & 1);
+            add_first(weights<OT>(last, 0, 0));
+            add_rest(weights<OT / 2>(last, OT / 2, 1));
             finish(n_it - 1, (n_it - 1) & 1);
             if constexpr (DOTS) {
                 lds_barrier();
@@ -741,12 +779,12 @@ template <typename In, typename Out, int KD, int NP, int NW, bool DOTS> struct S
     }
 };
 
-template <typename In, typename Out, int KD, int NP, int NW, bool DOTS>
+template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS>
 __global__ __launch_bounds__(64 * NW)
     __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void gdr_la_scan_kernel(const LaParams p) {
-    using S = Scan<In, Out, KD, NP, NW, DOTS>;
+    using S = Scan<In, Out, KD, NP, NW, KS, DOTS>;
     __shared__ __attribute__((aligned(16))) char lds[S::Y::BYTES];
-    int id = xcd_remap(blockIdx.x, gridDim.x);
+    int id = la_work(blockIdx.x, gridDim.x, p.share);
     const int cb = id % p.n_cb;
     id /= p.n_cb;
     S s(p, id % p.n_jobs, lds);
@@ -758,9 +796,9 @@ __global__ __launch_bounds__(64 * NW)
 // end states of segments
 template <typename In, int KD>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void gdr_la_states_kernel(const LaParams p) {
-    using S = Scan<In, void, KD, 1, 4, false>;
+    using S = Scan<In, void, KD, 1, 4, 1, false>;
     __shared__ __attribute__((aligned(16))) char lds[S::Y::BYTES];
-    int id = xcd_remap(blockIdx.x, gridDim.x);
+    int id = la_work(blockIdx.x, gridDim.x, p.share);
     const int cb = id % p.n_cb;
     id /= p.n_cb;
     S s(p, id % p.n_jobs, lds);
@@ -775,26 +813,28 @@ hipError_t launch(int KD, const LaParams &p, int items, hipStream_t s) {
     if constexpr (sizeof(In) == 2) {  // (fp32: a wave of 8 would not have the registers)
         if (p.job[0].W == 128 * p.n_cb) {
             if (KD == 128)
-                launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
+                launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 8, 1, DOTS>, grid, dim3(512), 0, s, p);
             else
-                launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 8, DOTS>, grid, dim3(512), 0, s, p);
+                launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 8, 1, DOTS>, grid, dim3(512), 0, s, p);
             return hipGetLastError();
         }
     }
+    constexpr int KS = sizeof(In) == 2 && NP == 2 && !DOTS ? 2 : 1;  // (more pieces of P: LDS)
     if (KD == 128)
-        launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 4, DOTS>, grid, dim3(256), 0, s, p);
+        launch_k(gdr_la_scan_kernel<In, Out, 128, NP, 4 * KS, KS, DOTS>, grid, dim3(256 * KS), 0, s, p);
     else
-        launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 4, DOTS>, grid, dim3(256), 0, s, p);
+        launch_k(gdr_la_scan_kernel<In, Out, 64, NP, 4 * KS, KS, DOTS>, grid, dim3(256 * KS), 0, s, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_la_scan(Dt dt, Dt out, int KD, bool dots, const LaParams &p, int items, hipStream_t s) {
+hipError_t launch_la_scan(Dt dt, Dt out, Dt last, int KD, bool dots, const LaParams &p, int items, hipStream_t s) {
     if (dt == Dt::F32) {
         if (out == Dt::F32) return dots ? launch<float, float, 1, true>(KD, p, items, s) : launch<float, float, 1, false>(KD, p, items, s);
         return dots ? launch<float, bf16, 1, true>(KD, p, items, s) : launch<float, bf16, 1, false>(KD, p, items, s);
     }
+    if (out == Dt::F32 && last == Dt::BF16 && !dots) return launch<bf16, float, 2, false>(KD, p, items, s);
     if (out == Dt::F32) return dots ? launch<bf16, float, 3, true>(KD, p, items, s) : launch<bf16, float, 3, false>(KD, p, items, s);
     return dots ? launch<bf16, bf16, 3, true>(KD, p, items, s) : launch<bf16, bf16, 2, false>(KD, p, items, s);
 }

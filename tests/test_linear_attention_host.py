@@ -182,6 +182,19 @@ def test_chunked_validation(which, kw, code):
     assert getattr(_lib.lib, "gdr_la_" + which)(ctypes.byref(a), None) == code
 
 
+@pytest.mark.parametrize("T", [0, 1, 63, 64, 65, 128, 129, 1000, 70000])
+@pytest.mark.parametrize("n_seq", [None, 0, 1, 2, 37, 5000])
+@pytest.mark.parametrize("dtype", [_lib.BF16, _lib.F32])
+def test_chunked_split_of_any_length(T, n_seq, dtype):
+    """The split into segments, of sequences without tokens too."""
+    n = ctypes.c_size_t(0)
+    packed = {} if n_seq is None else dict(B=1, cu_seqlens=64, n_seq=n_seq)
+    for st, which in ((_lib.LaFwdArgs, "fwd"), (_lib.LaBwdArgs, "bwd")):
+        for segment in (0, 1, 7):
+            a = la_args(st, T=T, dtype=dtype, segment_chunks=segment, q_batch=0, k_batch=0, v_batch=0, **packed)
+            assert getattr(_lib.lib, "gdr_la_%s_workspace" % which)(ctypes.byref(a), ctypes.byref(n)) == 0
+
+
 def test_chunked_pointers_and_workspace():
     n = ctypes.c_size_t(0)
     call = lambda f, a: getattr(_lib.lib, f)(ctypes.byref(a), None)  # noqa: E731
