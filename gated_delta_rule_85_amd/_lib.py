@@ -90,6 +90,7 @@ class LaFwdArgs(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("q", _p), ("k", _p), ("v", _p), ("g", _p), ("initial_state", _p), ("cu_seqlens", _p),
         ("o", _p), ("final_state", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+        ("zero_rest", _i32),
     ]
 
 
@@ -105,6 +106,7 @@ class LaBwdArgs(ctypes.Structure):
         ("dout", _p), ("dht", _p),
         ("dq", _p), ("dk", _p), ("dv", _p), ("dg", _p), ("dh0", _p),
         ("workspace", _p), ("workspace_bytes", ctypes.c_size_t),
+        ("zero_rest", _i32),
     ]
 
 

@@ -126,6 +126,15 @@ struct LaGates {
     float *dg;               // [tokens][Hv], or per-head partial sums [places][Hv] (s.g_tok 0)
 };
 
+// Tensors whose rows of no sequence are cleared: [T] rows of `words` 32-bit words
+struct LaRest {
+    const int32_t *cu;
+    int64_t T;
+    int n_seq, n;
+    uint32_t *x[4];
+    int64_t words[4];
+};
+
 // out: type of the jobs' o; last: the type that it is rounded to in the end; dots: whether they sum dots
 hipError_t launch_la_scan(Dt dt, Dt out, Dt last, int KD, bool dots, const LaParams &p, int items, hipStream_t s);
 // end states of segments only, into the border after (rev: before) each, with their decays
@@ -134,6 +143,7 @@ hipError_t launch_la_carry(const LaCarry &p, hipStream_t s);
 hipError_t launch_la_gates(const LaGates &p, int items, hipStream_t s);
 // out[token][h][d] = sum over the heads of group h of x[token][H group][W] (fp32)
 hipError_t launch_la_heads(const float *x, void *out, Dt out_dt, int64_t tokens, int H, int group, int W, hipStream_t s);
+hipError_t launch_la_rest(const LaRest &p, hipStream_t s);
 // dg[h] = sum over the places of part[place][h]
 hipError_t launch_la_sum_gates(const float *part, float *dg, int64_t places, int H, hipStream_t s);
 

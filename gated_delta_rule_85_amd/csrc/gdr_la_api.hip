@@ -141,6 +141,8 @@ int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
     return GDR_OK;
 }
 
+int64_t words(int64_t elements, int32_t t) { return t == GDR_BF16 ? elements / 2 : elements; }
+
 Dt type_of(int32_t t) { return t == GDR_BF16 ? Dt::BF16 : Dt::F32; }
 
 template <typename Args> LaSeqs sequences(const Args *a, const Plan &p) {
@@ -181,11 +183,18 @@ int gdr_la_fwd(const gdr_la_fwd_args *a, hipStream_t stream) {
     Plan pl;
     const int rc = plan_fwd(a, pl);
     if (rc) return rc;
-    if (pl.n_seq == 0 || (pl.tokens == 0 && !a->final_state)) return GDR_OK;
+    const bool rest = a->zero_rest && a->cu_seqlens && a->T > 0;
+    if (rest && !a->o) return GDR_EINVAL;
+    if (!rest && (pl.n_seq == 0 || (pl.tokens == 0 && !a->final_state))) return GDR_OK;
     if (pl.tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->o)) return GDR_EINVAL;
     if (!aligned16(a->o) || !aligned16(a->final_state) || !aligned16(a->workspace)) return GDR_EINVAL;
     if (pl.total > 0 && (!a->workspace || a->workspace_bytes < pl.total)) return GDR_EWORKSPACE;
     const NoStage stage;
+    if (rest) {
+        const LaRest r = {a->cu_seqlens, a->T, (int)pl.n_seq, 1, {static_cast<uint32_t *>(a->o)}, {words(a->H_v * a->V, a->out_dtype)}};
+        if (launch_la_rest(r, stream) != hipSuccess) return GDR_ELAUNCH;
+        if (pl.n_seq == 0) return GDR_OK;
+    }
     char *ws = static_cast<char *>(a->workspace);
     float *border = pl.split ? reinterpret_cast<float *>(ws + pl.off_fwd) : nullptr;
     LaParams p = {};
@@ -217,7 +226,9 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     Plan pl;
     const int rc = plan_bwd(a, pl);
     if (rc) return rc;
-    if (pl.n_seq == 0 && !a->g_per_head) return GDR_OK;
+    const bool rest = a->zero_rest && a->cu_seqlens && a->T > 0;
+    if (rest && (!a->dq || !a->dk || !a->dv || !a->dg)) return GDR_EINVAL;
+    if (pl.n_seq == 0 && !a->g_per_head && !rest) return GDR_OK;
     if (((pl.tokens > 0 || a->g_per_head) && !a->dg) || !aligned16(a->workspace)) return GDR_EINVAL;
     if (pl.tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->dout || !a->dq || !a->dk || !a->dv)) return GDR_EINVAL;
     for (const void *x : {(const void *)a->dout, (const void *)a->dht, (const void *)a->dq, (const void *)a->dk, (const void *)a->dv,
@@ -296,6 +307,13 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
         LaGates g = {s, border_fwd, border_rev, a->dht, dots_a, dots_b, pl.n_cb_k, pl.n_cb_v, K * V, pl.tokens,
                      a->g_per_head ? at(pl.off_gates) : a->dg};
         if (launch_la_gates(g, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
+    }
+    if (rest) {  // (after the sums over the heads, which are made of every row)
+        const int64_t qk = words(a->H_q * a->K, a->grad_dtype);
+        const LaRest r = {a->cu_seqlens, a->T, (int)pl.n_seq, a->g_per_head ? 3 : 4,
+                          {static_cast<uint32_t *>(a->dq), static_cast<uint32_t *>(a->dk), static_cast<uint32_t *>(a->dv), reinterpret_cast<uint32_t *>(a->dg)},
+                          {qk, qk, words(a->H_v * a->V, a->grad_dtype), a->H_v}};
+        if (launch_la_rest(r, stream) != hipSuccess) return GDR_ELAUNCH;
     }
     if (a->g_per_head && launch_la_sum_gates(at(pl.off_gates), a->dg, pl.n_seq > 0 ? pl.places : 0, H, stream) != hipSuccess)
         return GDR_ELAUNCH;

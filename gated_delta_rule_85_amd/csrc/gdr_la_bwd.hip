@@ -168,8 +168,26 @@ __global__ __launch_bounds__(256) void gdr_la_heads_kernel(const float *x, Out *
         *reinterpret_cast<bf16x4 *>(out + i) = __builtin_convertvector(y, bf16x4);
 }
 
+// ------------------------------------------------------------------ la_rest
+// Rows before the first and behind the last of the packed sequences := 0.  (4 us where there are none.)
+__global__ __launch_bounds__(256) void gdr_la_rest_kernel(LaRest p) {
+    auto clamped = [&](int i) { return min(max((int64_t)p.cu[i], (int64_t)0), p.T); };
+    const int64_t first = p.n_seq > 0 ? clamped(0) : 0, end = p.n_seq > 0 ? max(clamped(p.n_seq), first) : 0;
+    for (int64_t i = blockIdx.x; i < first + p.T - end; i += gridDim.x) {
+        const int64_t row = i < first ? i : end + i - first;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < p.n)
+                for (int64_t at = threadIdx.x; at < p.words[k]; at += 256) p.x[k][row * p.words[k] + at] = 0u;
+    }
+}
+
 }  // namespace
 
+hipError_t launch_la_rest(const LaRest &p, hipStream_t s) {
+    launch_k(gdr_la_rest_kernel, dim3((uint32_t)(p.T < 1024 ? p.T : 1024)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
 hipError_t launch_la_carry(const LaCarry &p, hipStream_t s) {
     launch_k(gdr_la_carry_kernel, dim3((uint32_t)p.s.n_seq * p.s.Hv * (p.KV / 1024)), dim3(256), 0, s, p);
     return hipGetLastError();

@@ -509,10 +509,10 @@ struct Linear {
         a.dtype = element(q->scalar_type());
         a.scale = (float)(1.0 / std::sqrt((double)K));
         if (scale != Py_None) a.scale = (float)PyFloat_AsDouble(scale);
-        a.segment_chunks = (int32_t)std::min<long>(PyLong_AsLong(segment_chunks), 1 << 30);
+        a.segment_chunks = (int32_t)std::max(-1L, std::min(PyLong_AsLong(segment_chunks), 1L << 30));
         a.g = floats(*g, held), a.g_per_head = g->dim() == 1;
         a.initial_state = states_of(h0, held);
-        a.cu_seqlens = indices(cu, q->device(), held);
+        a.cu_seqlens = indices(cu, q->device(), held), a.zero_rest = 1;
         return !PyErr_Occurred();
     }
 };

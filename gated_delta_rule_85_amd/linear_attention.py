@@ -24,7 +24,8 @@ def chunk_linear_attention_fwd(q, k, v, g, scale=None, initial_state=None, cu_se
     heads are contiguous.  A long sequence of few heads is split into segments of
     ``segment_chunks`` chunks of 64 tokens (0: chosen for the device; the split is exact: a
     segment's part of the state is carried on by a scalar decay).  A gate of -104 or less,
-    -inf among them, empties the state.  Rows of o that belong to no sequence are undefined.
+    -inf among them, empties the state.  Rows of o that belong to no sequence are zero, and so
+    are those of its gradients.
     """
     return _gdr_torch.la_fwd(q, k, v, g, scale, initial_state, cu_seqlens, output_final_state, output_dtype, segment_chunks)
 

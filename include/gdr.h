@@ -283,6 +283,7 @@ typedef struct {
     float *final_state;         /* [N,H_v,K,V]; NULL = not wanted */
     void *workspace;
     size_t workspace_bytes;
+    int32_t zero_rest;      /* cu_seqlens: rows that belong to no sequence are written, as zero */
 } gdr_la_fwd_args;
 
 typedef struct {
@@ -306,6 +307,7 @@ typedef struct {
     float *dh0;                 /* [N,H_v,K,V] gradient of initial_state; NULL = not wanted */
     void *workspace;
     size_t workspace_bytes;
+    int32_t zero_rest;      /* cu_seqlens: rows that belong to no sequence are written, as zero */
 } gdr_la_bwd_args;
 
 /* activations of gdr_group_norm: none, z sigmoid(z), sigmoid(z) */
@@ -500,9 +502,9 @@ int gdr_la_bwd_workspace(const gdr_la_bwd_args *args, size_t *bytes);
 int gdr_la_fwd(const gdr_la_fwd_args *args, hipStream_t stream);
 
 /* Its backward on `stream`: gradients of <dout, o> + <dht, final_state>.  Every output is
-   overwritten.  Rows of dq, dk, dv and dg that belong to no sequence are left as they are, as
-   rows of o are by the forward (where v heads share a q/k head, those of dq and dk are
-   undefined).  May be captured. */
+   overwritten.  Without zero_rest, rows of dq, dk, dv and dg that belong to no sequence are left
+   as they are, as rows of o are by the forward (where v heads share a q/k head, those of dq and
+   dk are undefined).  May be captured. */
 int gdr_la_bwd(const gdr_la_bwd_args *args, hipStream_t stream);
 
 /* Group norm with its activation on `stream`.  Needs no workspace and may be captured. */

@@ -328,6 +328,50 @@ def test_rows_behind_the_last_sequence_are_left(gdr):
     check(o[:, 10:130], exact(y, scale=1.0)[0], TOL[F32], "o")
 
 
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype,Hq,Hv", [(BF, 2, 4), (BF, 2, 2), (F32, 1, 3)])
+@pytest.mark.parametrize("cu", [[0, 100, 130], [7, 90, 90, 200], [40, 40], [200], [0, 256], [255, 256]])
+def test_padded_rows_are_zero(gdr, cu, dtype, Hq, Hv, per_head):
+    """Rows of no sequence: whatever they hold, o and the gradients are zero there, and the others' are
+    those of the sequences alone."""
+    T, K, V = 256, 64, 128
+    x = inputs(1, T, Hq, Hv, K, V, dtype, gates="head" if per_head else "token")
+    first, end = (cu[0], cu[-1]) if len(cu) > 1 else (0, 0)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[first:end] = False
+    leaves = {n: x[n].clone() for n in ("q", "k", "v", "g")}
+    for n in ("q", "k", "v") if per_head else ("q", "k", "v", "g"):
+        leaves[n][:, rest] = math.nan
+    do = torch.randn(1, T, Hv, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).to(dtype)
+    pads = do.clone()
+    pads[:, rest] = math.nan
+    for t in leaves.values():
+        t.requires_grad_()
+    offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    junk = [torch.full((1 << 20,), math.nan, device="cuda") for _ in range(4)]  # what the allocator hands out next
+    torch.cuda.synchronize()
+    del junk
+    o, _ = gdr.chunk_linear_attention(**leaves, cu_seqlens=offsets, output_dtype=dtype)
+    assert (o[:, rest] == 0).all()
+    o.backward(pads)
+    assert all((leaves[n].grad[:, rest] == 0).all() for n in ("q", "k", "v"))
+    assert per_head or (leaves["g"].grad[:, rest] == 0).all()
+    if end == first:
+        assert all((t.grad == 0).all() for t in leaves.values())
+        return
+    alone = {n: (t if n == "g" and per_head else t[:, first:end]).clone().requires_grad_() for n, t in x.items()
+             if n in ("q", "k", "v", "g")}
+    want, _ = gdr.chunk_linear_attention(**alone, cu_seqlens=offsets - first, output_dtype=dtype)
+    want.backward(do[:, first:end])
+    # both are off by the tolerances of the exact result (segments may start elsewhere)
+    check(o[:, first:end], want.double(), 2 * TOL[dtype], "o")
+    along = (alone["q"] * alone["q"].grad).double().sum(-1)
+    terms = along.abs().sum(1).norm().item() if per_head else along.norm().item()
+    for n, t in alone.items():
+        got = leaves[n].grad if n == "g" and per_head else leaves[n].grad[:, first:end]
+        check(got, t.grad.double(), 2 * (TOL_GATES if n == "g" else TOL[dtype]), n, terms if n == "g" else 0.0)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("K,V", [(128, 128), (128, 64), (64, 128), (64, 64)])
 @pytest.mark.parametrize("N,T", [(1, 1), (5, 1), (33, 3), (2, 9)])

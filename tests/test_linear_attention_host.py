@@ -211,6 +211,11 @@ def test_chunked_pointers_and_workspace():
     assert call("gdr_la_fwd", long) == _lib.EWORKSPACE
     long.segment_chunks = 1 << 20
     assert _lib.lib.gdr_la_fwd_workspace(ctypes.byref(long), ctypes.byref(n)) == 0 and n.value == 0
+    # rows to clear, and nowhere to
+    none = dict(B=1, n_seq=0, cu_seqlens=64, zero_rest=1)
+    assert call("gdr_la_fwd", la_args(_lib.LaFwdArgs, o=None, **none)) == _lib.EINVAL
+    for name in ("dq", "dk", "dv", "dg"):
+        assert call("gdr_la_bwd", la_args(_lib.LaBwdArgs, **{name: None}, **none)) == _lib.EINVAL
     # nothing to do
     for kw in (dict(B=0), dict(T=0), dict(cu_seqlens=64, B=1, n_seq=0)):
         assert call("gdr_la_fwd", la_args(_lib.LaFwdArgs, **kw)) == 0
