@@ -119,10 +119,11 @@ struct LaCarry {
 struct LaGates {
     LaSeqs s;
     const float *fwd, *rev;  // states and their gradients at the borders (fwd at place 0: the last state)
-    const float *dht;        // [n_seq][Hv] or null
+    const float *dht, *h0, *dh0;  // [n_seq][Hv] or null
     const float *a, *b;      // [n_a | n_b][Hv][tokens] dots
     int n_a, n_b, KV;
     int64_t tokens;
+    double2 *at;             // [places][Hv] dg at the segments' first tokens, and its size (see the kernel)
     float *dg;               // [tokens][Hv], or per-head partial sums [places][Hv] (s.g_tok 0)
 };
 

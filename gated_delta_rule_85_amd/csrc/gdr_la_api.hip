@@ -13,7 +13,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 
 constexpr int64_t UNITS = 256;    // compute units of an MI355X, a workgroup each
-constexpr int BORDER_CHUNKS = 16; // the backward's longest segments (gate gradients start anew at each border)
+constexpr int BORDER_CHUNKS = 16; // the backward's longest segments (gate gradients start anew at each border; gdr_la_gates_kernel)
 
 // 128 columns a workgroup (bf16) where that leaves one for every compute unit (gdr_la_scan.hip): fewer
 // tiles of P a column, against all compute units busy.  `units`: sequences (or segments) and heads
@@ -81,7 +81,7 @@ struct Plan {
     int group, n_cb_k, n_cb_v;  // blocks of columns, where K or V columns are scanned
     bool split;
     int seg_chunks;
-    size_t border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, total;
+    size_t border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, off_at, total;
 };
 
 template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
@@ -137,6 +137,7 @@ int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
     p.off_dots = take(tokens * (p.n_cb_k + p.n_cb_v));
     p.off_dq = take(p.group > 1 ? tokens * a->K : 0), p.off_dk = take(p.group > 1 ? tokens * a->K : 0);
     p.off_gates = take(p.decays_bytes);
+    p.off_at = take(4 * p.decays_bytes);
     p.total = off;
     return GDR_OK;
 }
@@ -304,8 +305,8 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
             if (launch_la_heads(static_cast<float *>(dq.o), a->dq, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
             if (launch_la_heads(static_cast<float *>(dk.o), a->dk, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
         }
-        LaGates g = {s, border_fwd, border_rev, a->dht, dots_a, dots_b, pl.n_cb_k, pl.n_cb_v, K * V, pl.tokens,
-                     a->g_per_head ? at(pl.off_gates) : a->dg};
+        LaGates g = {s, border_fwd, border_rev, a->dht, a->initial_state, a->dh0, dots_a, dots_b, pl.n_cb_k, pl.n_cb_v, K * V, pl.tokens,
+                     reinterpret_cast<double2 *>(ws + pl.off_at), a->g_per_head ? at(pl.off_gates) : a->dg};
         if (launch_la_gates(g, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
     }
     if (rest) {  // (after the sums over the heads, which are made of every row)

@@ -48,11 +48,14 @@ __global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
 }
 
 // ------------------------------------------------------------------ la_gates
-// dg_t = sum over i < t <= s of what key i gives to query s: with a_s = q_s . dq_s and
-// b_i = v_i . dv_i (= k_i . dk_i), dg_t = dg at the segment's far border + sum over the segment's
-// s >= t of (a_s - b_s); at the border it is e^g <S, dS>, from the states on either side.  The
-// differences cancel from one token to the next, so the sums run in 64 bits and start anew at
-// every border.
+// dg_t = sum over i < t <= s of what key i gives to query s.  With a_s = q_s . dq_s and
+// b_i = v_i . dv_i (= k_i . dk_i), dg_t - dg_{t+1} = a_t - b_t; at a segment's first token dg is
+// e^g <S, dS>, from the states on either side (0 at a sequence's start without an initial state,
+// else <h0, dh0>), and behind its last one the next segment's, or <S, dht>, or 0.  The differences
+// cancel from one token to the next, so that they are added in 64 bits from the far end, anew in every
+// segment of 16 chunks at most; what is then missing at the near end is the sum of all errors, and
+// each token gets its share of it, by the sizes of the terms: the squares of all terms from the far end to it,
+// of all of the segment's (8 x 4096 tokens of 64 heads: 1.4e-6 off, without it 2.1e-6; segments of 8 chunks: 1.0e-6, and 3% longer).
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
     for (int i = 32; i; i >>= 1) x += __shfl_xor(x, i);
@@ -66,8 +69,43 @@ __device__ __forceinline__ double block_sum(double x, double *lds) {  // of four
     return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
-__global__ __launch_bounds__(256) void gdr_la_gates_kernel(LaGates p) {
+// scale <x, y>, and the sum of its terms' squares; on every thread
+__device__ __forceinline__ double2 product(const float *x, const float *y, int n, double scale, double *lds) {
+    float d0 = 0.f, d1 = 0.f, v0 = 0.f, v1 = 0.f;
+#pragma unroll 4
+    for (int i = 4 * (int)threadIdx.x; i < n; i += 1024) {
+        const f32x4 z = *reinterpret_cast<const f32x4 *>(x + i) * *reinterpret_cast<const f32x4 *>(y + i);
+        d0 += z[0] + z[1], d1 += z[2] + z[3];
+        v0 = fmaf(z[0], z[0], fmaf(z[1], z[1], v0)), v1 = fmaf(z[2], z[2], fmaf(z[3], z[3], v1));
+    }
+    return {scale * block_sum((double)d0 + d1, lds), scale * scale * block_sum((double)v0 + v1, lds)};
+}
+
+// at the first token of every segment
+__global__ __launch_bounds__(256) void gdr_la_borders_kernel(LaGates p) {
     __shared__ double lds[4];
+    const int place = blockIdx.x / p.s.Hv, hv = blockIdx.x - place * p.s.Hv;
+    int j, m;
+    if (!la_place(p.s, place, j, m)) return;
+    int64_t bos, eos;
+    la_bounds(p.s, j, bos, eos);
+    double2 at = {0.0, 0.0};
+    if (m > 0) {
+        const int64_t border = (int64_t)blockIdx.x * p.KV;
+        const float g = p.s.g[(bos + m * (int64_t)p.s.seg_chunks * CH) * p.s.g_tok + hv];
+        at = product(p.fwd + border, p.rev + border, p.KV, expf(g), lds);
+    } else if (p.h0) {
+        const int64_t state = ((int64_t)j * p.s.Hv + hv) * p.KV;
+        if (p.dh0)
+            at = product(p.h0 + state, p.dh0 + state, p.KV, 1.0, lds);
+        else
+            at.y = -1.0;  // not known
+    }
+    if (threadIdx.x == 0) p.at[blockIdx.x] = at;
+}
+
+__global__ __launch_bounds__(256) void gdr_la_gates_kernel(LaGates p) {
+    __shared__ double lds[4], lds2[4];
     const int place = blockIdx.x / p.s.Hv, hv = blockIdx.x - place * p.s.Hv, tid = threadIdx.x;
     int j, m;
     if (!la_place(p.s, place, j, m)) {
@@ -78,65 +116,54 @@ __global__ __launch_bounds__(256) void gdr_la_gates_kernel(LaGates p) {
     la_bounds(p.s, j, bos, eos);
     const int64_t seg_tokens = (int64_t)p.s.seg_chunks * CH, len = eos - bos;
     const int64_t lo = m * seg_tokens, hi = min(len, lo + seg_tokens);
-    // at the far border
-    const float *x = nullptr, *y = nullptr;
-    double at_border = 1.0;
-    if (hi < len) {
-        const int64_t border = ((int64_t)(place + 1) * p.s.Hv + hv) * p.KV;
-        x = p.fwd + border, y = p.rev + border;
-        const float g = p.s.g[(bos + hi) * p.s.g_tok + hv];
-        at_border = expf(g);
-    } else if (p.dht) {
-        x = p.fwd + ((int64_t)(place - m) * p.s.Hv + hv) * p.KV, y = p.dht + ((int64_t)j * p.s.Hv + hv) * p.KV;
+    const double2 near = p.at[blockIdx.x];
+    double2 far = {0.0, 0.0};
+    if (hi < len)
+        far = p.at[blockIdx.x + p.s.Hv];
+    else if (p.dht)
+        far = product(p.fwd + ((int64_t)(place - m) * p.s.Hv + hv) * p.KV, p.dht + ((int64_t)j * p.s.Hv + hv) * p.KV, p.KV, 1.0, lds);
+    // a segment's 1024 tokens at most, four per thread
+    const int64_t t0 = hi - 1024 + 4 * tid, plane = (int64_t)p.s.Hv * p.tokens;
+    double d[4], v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + i;
+        d[i] = v[i] = 0.0;
+        if (t >= lo) {
+            const int64_t at = hv * p.tokens + bos + t;
+            double a = 0.0, b = 0.0;
+            for (int c = 0; c < p.n_a; ++c) a += p.a[c * plane + at];
+            for (int c = 0; c < p.n_b; ++c) b += p.b[c * plane + at];
+            d[i] = a - b, v[i] = a * a + b * b;
+        }
     }
-    double carry = 0.0, total = 0.0;
-    if (x) {
-        float d0 = 0.f, d1 = 0.f;
-        for (int i = 4 * tid; i < p.KV; i += 1024) {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(x + i), b = *reinterpret_cast<const f32x4 *>(y + i);
-            d0 = fmaf(a[0], b[0], fmaf(a[1], b[1], d0));
-            d1 = fmaf(a[2], b[2], fmaf(a[3], b[3], d1));
-        }
-        carry = at_border * block_sum((double)d0 + d1, lds);
+#pragma unroll
+    for (int i = 2; i >= 0; --i) d[i] += d[i + 1], v[i] += v[i + 1];
+    double after = d[0], size = v[0];  // sums from this thread on, of the wave, then of the workgroup
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) {
+        const double z = __shfl_down(after, i), y = __shfl_down(size, i);
+        if (lane_id() + i < 64) after += z, size += y;
     }
-    const int64_t plane = (int64_t)p.s.Hv * p.tokens;
-    for (int64_t t1 = hi; t1 > lo; t1 -= 1024) {  // 1024 tokens at a time, four per thread
-        const int64_t t0 = t1 - 1024 + 4 * tid;
-        double d[4];
+    __syncthreads();
+    if (lane_id() == 0) lds[wave_id()] = after, lds2[wave_id()] = size;
+    __syncthreads();
+    double rest = far.x + (after - d[0]), sizes = far.y + (size - v[0]);
+    for (int i = wave_id() + 1; i < 4; ++i) rest += lds[i], sizes += lds2[i];
+    const double missing = near.x - (far.x + ((lds[0] + lds[1]) + (lds[2] + lds[3])));
+    const double all = near.y + far.y + ((lds2[0] + lds2[1]) + (lds2[2] + lds2[3]));
+    double share = missing / all;
+    if (near.y < 0.0 || !(all > 0.0) || !(fabs(share) < 1e300)) share = 0.0;
+    double total = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t t = t0 + i;
-            d[i] = 0.0;
-            if (t >= lo) {
-                const int64_t at = hv * p.tokens + bos + t;
-                for (int c = 0; c < p.n_a; ++c) d[i] += p.a[c * plane + at];
-                for (int c = 0; c < p.n_b; ++c) d[i] -= p.b[c * plane + at];
-            }
-        }
-#pragma unroll
-        for (int i = 2; i >= 0; --i) d[i] += d[i + 1];
-        double after = d[0];  // sums from this thread on, of the wave, then of the workgroup
-#pragma unroll
-        for (int i = 1; i < 64; i <<= 1) {
-            const double z = __shfl_down(after, i);
-            if (lane_id() + i < 64) after += z;
-        }
-        __syncthreads();
-        if (lane_id() == 0) lds[wave_id()] = after;
-        __syncthreads();
-        double rest = carry + (after - d[0]);
-        for (int i = wave_id() + 1; i < 4; ++i) rest += lds[i];
-        carry += lds[0] + lds[1] + lds[2] + lds[3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t t = t0 + i;
-            if (t < lo) continue;
-            const double dg = d[i] + rest;
-            if (p.s.g_tok)
-                p.dg[(bos + t) * p.s.Hv + hv] = (float)dg;
-            else
-                total += dg;
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + i;
+        if (t < lo) continue;
+        const double dg = d[i] + rest + share * (v[i] + sizes);
+        if (p.s.g_tok)
+            p.dg[(bos + t) * p.s.Hv + hv] = (float)dg;
+        else
+            total += dg;
     }
     if (p.s.g_tok == 0) {
         total = block_sum(total, lds);
@@ -193,6 +220,7 @@ hipError_t launch_la_carry(const LaCarry &p, hipStream_t s) {
     return hipGetLastError();
 }
 hipError_t launch_la_gates(const LaGates &p, int items, hipStream_t s) {
+    launch_k(gdr_la_borders_kernel, dim3((uint32_t)items * p.s.Hv), dim3(256), 0, s, p);
     launch_k(gdr_la_gates_kernel, dim3((uint32_t)items * p.s.Hv), dim3(256), 0, s, p);
     return hipGetLastError();
 }
