@@ -217,3 +217,22 @@ def test_streams_graphs_and_repeats(gdr):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(both(), kept))
+
+
+def test_offsets_past_32_bits(gdr):
+    """2.5e9 values: the last tokens' results are bit for bit those of the tokens alone."""
+    M, C, last = 300000, 8192, 100
+    x = torch.zeros(M, C, dtype=BF, device="cuda")
+    dout = torch.zeros(M, C, dtype=BF, device="cuda")
+    x[-last:] = torch.randn(last, C, device="cuda").to(BF)
+    dout[-last:] = torch.randn(last, C, device="cuda").to(BF)
+    weight, bias = torch.rand(C, device="cuda"), torch.rand(C, device="cuda")
+    args = 64, dout, weight, bias
+    y = gdr.group_norm(x, 64, weight, bias)
+    assert torch.equal(y[-last:], gdr.group_norm(x[-last:], 64, weight, bias))
+    got = gdr.group_norm_bwd(x, *args)
+    want = gdr.group_norm_bwd(x[-last:], 64, dout[-last:], weight, bias)
+    assert torch.equal(got[0][-last:], want[0]) and not got[0][:-last].any()
+    for a, b, name in zip(got[1:3], want[1:3], ("dweight", "dbias")):
+        # (the other tokens add zeros; 100 terms in another order)
+        assert (a - b).norm() <= 2 ** -24 * last * b.norm(), name

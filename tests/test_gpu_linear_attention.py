@@ -491,3 +491,53 @@ def test_streams_graphs_and_repeats(gdr):
         fresh = both()
         for k in kept:
             assert all(torch.equal(a, b) for a, b in zip(fresh, k))
+
+
+@pytest.mark.parametrize("N", [65, 300, 5000])
+def test_many_packed_sequences_split(gdr, N):
+    """The segments of more sequences than a wave has lanes, empty and long ones among them: split and
+    unsplit scans are both off by the tolerances of the exact result."""
+    gen = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 4, (N,), generator=gen)
+    for i in (0, 1, N // 2, N // 2 + 3, N - 1):
+        lens[i] = 130 + 65 * (i % 3)
+    T, H, K, V = int(lens.sum()) + 9, 2, 64, 64  # (and rows behind the last one)
+    x = inputs(1, T, 1, H, K, V, BF, lens=lens.tolist(), h0=True)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]).to(device="cuda", dtype=torch.int32)
+    do = torch.randn(1, T, H, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(BF)
+    dht = torch.randn(N, H, K, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    runs = []
+    for segment in (1, 2, 1 << 20):
+        o, hT = gdr.chunk_linear_attention_fwd(x["q"], x["k"], x["v"], x["g"], None, x["initial_state"], cu,
+                                               segment_chunks=segment)
+        grads = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, x["initial_state"], cu,
+                                               segment_chunks=segment)
+        runs.append((o, hT) + grads)
+    terms = (x["q"].double() * runs[-1][2].double()).sum(-1).norm().item()
+    for run in runs[:-1]:
+        for name, got, want in zip(("o", "hT", "dq", "dk", "dv", "dg", "dh0"), run, runs[-1]):
+            tol = TOL_GATES if name == "dg" else TOL[BF] if got.dtype == BF else TOL[F32]
+            check(got, want.double(), 2 * tol, name, terms if name == "dg" else 0.0)
+
+
+def test_offsets_past_32_bits(gdr):
+    """v, o and do of 2.5e9 elements: a sequence at the end is as it is alone."""
+    T, first, H, K, V = 300000, 299000, 64, 64, 128
+    x = inputs(1, T, 32, H, K, V, BF)
+    do = torch.randn(T - first, H * V, device="cuda").to(BF).view(1, -1, H, V)
+    whole = torch.zeros(1, T, H, V, dtype=BF, device="cuda")
+    whole[:, first:] = do
+    cu = torch.tensor([0, first, T], dtype=torch.int32, device="cuda")
+    leaves = [x[n] for n in ("q", "k", "v", "g")]
+    alone = [t[:, first:].contiguous() for t in leaves]
+    want, _ = gdr.chunk_linear_attention_fwd(*alone, output_dtype=BF)
+    got, _ = gdr.chunk_linear_attention_fwd(*leaves, cu_seqlens=cu, output_dtype=BF)
+    check(got[:, first:], want.double(), 2 * TOL[BF], "o")
+    del got
+    want = gdr.chunk_linear_attention_bwd(*alone, do)
+    got = gdr.chunk_linear_attention_bwd(*leaves, whole, cu_seqlens=cu)
+    for name, a, b in zip(("dq", "dk", "dv"), got, want):
+        check(a[:, first:], b.double(), 2 * TOL[BF], name)
+        assert (a[:, :first] == 0).all(), name  # (nothing reaches another sequence)
+    terms = (alone[0].double() * want[0].double()).sum(-1).norm().item()
+    check(got[3][:, first:], want[3].double(), 2 * TOL_GATES, "dg", terms)
