@@ -7,7 +7,7 @@
 //     dx = rstd (dn - n mean(dn n) - mean(dn)),  the last term where the norm is centred.
 // A thread keeps its channels over its tokens and their dw and db in registers; the sums of the
 // workgroups are added in a second kernel.  Bound by memory: x, gate and dout read, dx and dgate written,
-// once.  32768 x 8192 in bf16 (2.7 GB): 526 us, 5.1 TB/s, and 16 us for the sums.  The next token is
+// once.  32768 x 8192 in bf16 (2.7 GB): 526 us, 5.1 TB/s, and 8 to 16 us for the sums.  The next token is
 // not read ahead here: with the three inputs of another token a thread's registers leave room for fewer
 // waves, and it took 587 us.
 #include "gdr_norm.hpp"
