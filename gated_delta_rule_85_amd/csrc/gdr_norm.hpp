@@ -171,11 +171,13 @@ struct NormVariant {
     int vec, values, lanes;
     bool ragged;
 };
-// Pieces of 8 where the rows allow them, else single channels
+// Pieces of 8 where the rows allow them and a workgroup has a place for all that a group may touch (1025
+// of them for 8187, 8189, 8190 and 8191 channels), else single channels.  A ragged group begins up to
+// 8 - (D & -D) channels past a multiple of 8
 inline NormVariant norm_variant(int64_t D, bool aligned) {
-    if (aligned) {
-        const bool ragged = D % 8 != 0;
-        const int64_t width = ragged ? (D + 14) / 8 * 8 : D;  // pieces that it may touch
+    const bool ragged = aligned && D % 8 != 0;
+    const int64_t width = ragged ? (D + 8 - (D & -D) + 7) / 8 * 8 : D;  // of the pieces that it may touch
+    if (aligned && width <= NORM_WIDTH_MAX) {
         if (width > 512) return {8, width <= 2048 ? 8 : width <= 4096 ? 16 : 32, NORM_THREADS, ragged};
         int lanes = 1;
         while (lanes * 8 < width) lanes <<= 1;

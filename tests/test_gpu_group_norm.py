@@ -236,3 +236,25 @@ def test_offsets_past_32_bits(gdr):
     for a, b, name in zip(got[1:3], want[1:3], ("dweight", "dbias")):
         # (the other tokens add zeros; 100 terms in another order)
         assert (a - b).norm() <= 2 ** -24 * last * b.norm(), name
+
+
+@pytest.mark.parametrize("D", [517, 1030, 2050, 4100, 8185, 8187, 8189, 8190, 8191])
+def test_wide_groups_off_a_multiple_of_eight(gdr, D):
+    """Aligned rows whose groups begin anywhere: the widest have more pieces than a workgroup has places.
+    Memory that the allocator hands out next holds NaN, so that a channel that is not written shows."""
+    for G in (8, 4) if D % 2 == 0 else (8,):
+        for center, x, gate, out in ((True, BF, BF, BF), (False, F32, None, F32)):
+            a = inputs(5, G, D, x, gate, seed=D)
+            dout = torch.randn(5, G * D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(G)).to(out)
+            y, dx, dw, db, dz, scale = exact(a, G, "silu", center, dout)
+            junk = [torch.full((5 * G * D,), math.nan, device="cuda") for _ in range(4)]
+            torch.cuda.synchronize()
+            del junk
+            got = gdr.group_norm(a["x"], G, a["weight"], a["bias"], a["gate"], center=center, output_dtype=out)
+            check(got, y, out, "out")
+            g = gdr.group_norm_bwd(a["x"], G, dout, a["weight"], a["bias"], a["gate"], center=center)
+            check(g[0], dx, x, "dx", scale)
+            check(g[1], dw, F32, "dweight")
+            check(g[2], db, F32, "dbias")
+            if gate is not None:
+                check(g[3], dz, gate, "dgate")
