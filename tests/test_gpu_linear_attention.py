@@ -541,3 +541,53 @@ def test_offsets_past_32_bits(gdr):
         assert (a[:, :first] == 0).all(), name  # (nothing reaches another sequence)
     terms = (alone[0].double() * want[0].double()).sum(-1).norm().item()
     check(got[3][:, first:], want[3].double(), 2 * TOL_GATES, "dg", terms)
+
+
+def _resets(T, n, closed, seed):
+    """Gates of T tokens of which n close at the start of every 16 and two more anywhere."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    g = torch.nn.functional.logsigmoid(2 * torch.randn(1, T, 2, device="cuda", generator=gen) + 3)
+    g[:, torch.arange(T, device="cuda") % 16 < n] = closed
+    g[:, torch.randint(T, (2,), device="cuda", generator=gen)] = closed
+    return g
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("closed", [-math.inf, -104.0, -60.0, -5.0])
+@pytest.mark.parametrize("n", [0, 1, 4, 8])
+def test_decays_between_tokens(gdr, n, closed, dtype):
+    """Keys and values of a single one read the decay from every token to every later one out of o, and
+    to the end out of the state.  Its error is relative to the gates between the two, whatever came
+    before them: their sum S is made of at most twelve roundings, each 2^-24 of S at most, and what is
+    made of it goes through fewer than sixteen more."""
+    T = 128
+    one = torch.eye(T, device="cuda").to(dtype).view(1, T, 1, T)
+    g = _resets(T, n, closed, seed=n)
+    total = g[0].double().clamp(min=-1000).cumsum(0)
+    o, hT = gdr.chunk_linear_attention_fwd(torch.ones_like(one), one, one.expand(1, T, 2, T), g, 1.0)
+    between = total[:, None] - total[None]  # [t, i, head]
+    got = o[0].transpose(1, 2).double()
+    past = torch.ones(T, T, dtype=torch.bool, device="cuda").tril()[:, :, None]
+    for got, between in ((got.where(past, 0), between.where(past, -math.inf)),
+                         (hT[0].diagonal(dim1=1, dim2=2).T.double(), between[-1])):
+        off = (got - between.exp()).abs()
+        tol = 2.0 ** -24 * (16 + 16 * between.abs().nan_to_num(posinf=0)) * between.exp() + 2.0 ** -120
+        assert (off <= tol).all(), "%.3g times the tolerance" % (off / tol).max()
+    assert not o[0].transpose(1, 2).where(past, 0).isnan().any() and not (o[0].transpose(1, 2) * ~past).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 4, 8])
+def test_gradients_behind_resets(gdr, n, dtype):
+    """Gates that empty the state do not make what follows them less precise."""
+    x = inputs(1, 300, 1, 2, 64, 128, dtype, h0=True)
+    x["g"] = _resets(300, n, -math.inf, seed=n)
+    do = torch.randn(x["v"].shape, device="cuda").to(dtype)
+    dht = torch.randn(x["initial_state"].shape, device="cuda")
+    o, hT, *want = exact(dict(x, g=x["g"].clamp(min=-1000)), do, dht)
+    got, last = gdr.chunk_linear_attention_fwd(**x)
+    check(got, o, TOL[F32], "o")
+    check(last, hT, TOL[F32], "final_state")
+    grads = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, x["initial_state"], grad_dtype=F32)
+    for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "dh0"), grads, want, [TOL[F32]] * 3 + [TOL_GATES, TOL[F32]]):
+        check(a, b, tol, name, want[5] if name == "dg" else 0.0)
