@@ -11,7 +11,7 @@ namespace gdr {
 // (1 <= b < its segments) lies before token 64 seg_chunks b.  What is kept per segment or border
 // of all sequences is indexed by la_first() + its number; there are la_slots() such places.
 struct LaSeqs {
-    const int32_t *cu;  // [n_seq + 1] or null
+    const int32_t *cu;  // [n_seq + 1] or null; of more than LA_WAVE_SEQS sequences, launch_la_offsets' table
     const float *g;
     int64_t g_tok;      // floats between the gates of two tokens (0: one gate per head)
     int64_t T;
@@ -19,21 +19,41 @@ struct LaSeqs {
     int n_seg;          // segments of every sequence (without cu)
 };
 
-// tokens [bos, eos) of sequence j among [0, B T); offsets are clamped to [0, T], an end before
-// its start to the start
+// Offsets are taken within [0, T] and as no less than any before them, so that sequences never share a
+// row.  Up to 64 sequences' are held by a wave, one a lane; those of more are made into a table first.
+constexpr int LA_WAVE_SEQS = 64;
+
+// running maximum over the 64 lanes, of values of 0 or more
+__device__ __forceinline__ int la_running_max(int x) {
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8: within 16 lanes
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));  // row_bcast15, 31
+    return max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));
+}
+__device__ __forceinline__ int la_offset(const int32_t *cu, int64_t T, int i) { return min(max(cu[i], 0), (int)T); }
+// offset l of lane l (n_seq <= LA_WAVE_SEQS)
+__device__ __forceinline__ int la_starts(const LaSeqs &s) { return la_running_max(la_offset(s.cu, s.T, min(lane_id(), s.n_seq))); }
+__device__ __forceinline__ void la_bounds(const LaSeqs &s, int starts, int j, int64_t &bos, int64_t &eos) {
+    bos = __builtin_amdgcn_readlane(starts, j);
+    eos = j < 63 ? __builtin_amdgcn_readlane(starts, j + 1) : max((int)bos, la_offset(s.cu, s.T, j + 1));
+}
+// tokens [bos, eos) of sequence j among [0, B T); of whole waves, j the same on every lane
 __device__ __forceinline__ void la_bounds(const LaSeqs &s, int j, int64_t &bos, int64_t &eos) {
-    if (s.cu) {
-        bos = min(max((int64_t)s.cu[j], (int64_t)0), s.T);
-        eos = min(max((int64_t)s.cu[j + 1], bos), s.T);
-    } else {
+    if (!s.cu) {
         bos = (int64_t)j * s.T;
         eos = bos + s.T;
+    } else if (s.n_seq > LA_WAVE_SEQS) {
+        bos = s.cu[j], eos = s.cu[j + 1];
+    } else {
+        la_bounds(s, la_starts(s), __builtin_amdgcn_readfirstlane(j), bos, eos);
     }
 }
 // place of a sequence's first segment.  Packed: a sequence of n tokens takes n / seg_tokens + 1 places
 // at most, and the sequences' places do not meet
 __device__ __forceinline__ int la_first(const LaSeqs &s, int64_t bos, int j, int64_t seg_tokens) {
-    return s.cu ? (int)(bos / seg_tokens) + j : j * s.n_seg;
+    return s.cu ? (int)((uint32_t)bos / (uint32_t)seg_tokens) + j : j * s.n_seg;  // (a segment has at most 2^31 tokens)
 }
 inline int64_t la_segments(int64_t T, int64_t seg_tokens) { return T > seg_tokens ? (T + seg_tokens - 1) / seg_tokens : 1; }
 inline int64_t la_slots(bool packed, int64_t T, int64_t n_seq, int64_t seg_tokens) {
@@ -48,17 +68,20 @@ __device__ __forceinline__ bool la_place(const LaSeqs &s, int place, int &j, int
     }
     int lo = 0;  // the last sequence whose first place is not past it
     int64_t bos, eos;
-    for (int n = s.n_seq; n > 1;) {
-        const int step = (n + 63) >> 6, at = lane_id() * step;
-        bool before = false;
-        if (at < n) {
-            la_bounds(s, lo + at, bos, eos);
-            before = la_first(s, bos, lo + at, seg_tokens) <= place;
+    if (s.n_seq <= LA_WAVE_SEQS) {
+        const int starts = la_starts(s);
+        const bool before = lane_id() < s.n_seq && la_first(s, starts, lane_id(), seg_tokens) <= place;
+        lo = max((int)__popcll(__ballot(before)) - 1, 0);
+        la_bounds(s, starts, lo, bos, eos);
+    } else {
+        for (int n = s.n_seq; n > 1;) {
+            const int step = (n + 63) >> 6, at = lane_id() * step;
+            const bool before = at < n && la_first(s, s.cu[lo + at], lo + at, seg_tokens) <= place;
+            const int skip = max((int)__popcll(__ballot(before)) - 1, 0) * step;
+            lo += skip, n = min(step, n - skip);
         }
-        const int skip = max((int)__popcll(__ballot(before)) - 1, 0) * step;
-        lo += skip, n = min(step, n - skip);
+        la_bounds(s, lo, bos, eos);
     }
-    la_bounds(s, lo, bos, eos);
     j = lo;
     m = place - la_first(s, bos, lo, seg_tokens);
     return m >= 0 && (m == 0 || m * seg_tokens < eos - bos);
@@ -129,9 +152,8 @@ struct LaGates {
 
 // Tensors whose rows of no sequence are cleared: [T] rows of `words` 32-bit words
 struct LaRest {
-    const int32_t *cu;
-    int64_t T;
-    int n_seq, n;
+    LaSeqs s;
+    int n;
     uint32_t *x[4];
     int64_t words[4];
 };
@@ -145,6 +167,8 @@ hipError_t launch_la_gates(const LaGates &p, int items, hipStream_t s);
 // out[token][h][d] = sum over the heads of group h of x[token][H group][W] (fp32)
 hipError_t launch_la_heads(const float *x, void *out, Dt out_dt, int64_t tokens, int H, int group, int W, hipStream_t s);
 hipError_t launch_la_rest(const LaRest &p, hipStream_t s);
+// to[i] (n of them) = the largest of cu[0] .. cu[i], within [0, T]
+hipError_t launch_la_offsets(const int32_t *cu, int32_t *to, int64_t n, int64_t T, hipStream_t s);
 // dg[h] = sum over the places of part[place][h]
 hipError_t launch_la_sum_gates(const float *part, float *dg, int64_t places, int H, hipStream_t s);
 

@@ -81,7 +81,7 @@ struct Plan {
     int group, n_cb_k, n_cb_v;  // blocks of columns, where K or V columns are scanned
     bool split;
     int seg_chunks;
-    size_t border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, off_at, total;
+    size_t offsets_bytes, off_offsets, border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, off_at, total;
 };
 
 template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
@@ -105,6 +105,7 @@ template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
     p.n_cb_k = a->K == 128 && !whole ? 2 : 1, p.n_cb_v = a->V == 128 && !whole ? 2 : 1;
     p.border_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v * a->K * a->V));
     p.decays_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v));
+    p.offsets_bytes = varlen && p.n_seq > LA_WAVE_SEQS ? up(sizeof(int32_t) * (size_t)(p.n_seq + 1)) : 0;
     return GDR_OK;
 }
 
@@ -115,7 +116,8 @@ int plan_fwd(const gdr_la_fwd_args *a, Plan &p) {
     if (rc) return rc;
     p.off_fwd = 0;
     p.off_decays_fwd = p.border_bytes;
-    p.total = p.split ? p.border_bytes + p.decays_bytes : 0;
+    p.off_offsets = p.split ? p.border_bytes + p.decays_bytes : 0;
+    p.total = p.off_offsets + p.offsets_bytes;
     return GDR_OK;
 }
 
@@ -138,6 +140,7 @@ int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
     p.off_dq = take(p.group > 1 ? tokens * a->K : 0), p.off_dk = take(p.group > 1 ? tokens * a->K : 0);
     p.off_gates = take(p.decays_bytes);
     p.off_at = take(4 * p.decays_bytes);
+    p.off_offsets = take(p.offsets_bytes);
     p.total = off;
     return GDR_OK;
 }
@@ -147,8 +150,14 @@ int64_t words(int64_t elements, int32_t t) { return t == GDR_BF16 ? elements / 2
 Dt type_of(int32_t t) { return t == GDR_BF16 ? Dt::BF16 : Dt::F32; }
 
 template <typename Args> LaSeqs sequences(const Args *a, const Plan &p) {
-    return {a->cu_seqlens, a->g, a->g_per_head ? 0 : a->H_v, a->T, (int)p.n_seq, (int)a->H_v, p.seg_chunks,
+    const int32_t *cu = p.offsets_bytes ? reinterpret_cast<const int32_t *>(static_cast<const char *>(a->workspace) + p.off_offsets) : a->cu_seqlens;
+    return {cu, a->g, a->g_per_head ? 0 : a->H_v, a->T, (int)p.n_seq, (int)a->H_v, p.seg_chunks,
             (int)la_segments(a->T, p.seg_tokens)};
+}
+
+// the table that `s` has for its offsets, where it has one
+template <typename Args> hipError_t make_offsets(const Args *a, const Plan &p, const LaSeqs &s, hipStream_t stream) {
+    return p.offsets_bytes ? launch_la_offsets(a->cu_seqlens, const_cast<int32_t *>(s.cu), p.n_seq + 1, a->T, stream) : hipSuccess;
 }
 
 // neighbours of a grid: the v heads, blocks of columns and jobs of a q/k head
@@ -191,15 +200,17 @@ int gdr_la_fwd(const gdr_la_fwd_args *a, hipStream_t stream) {
     if (!aligned16(a->o) || !aligned16(a->final_state) || !aligned16(a->workspace)) return GDR_EINVAL;
     if (pl.total > 0 && (!a->workspace || a->workspace_bytes < pl.total)) return GDR_EWORKSPACE;
     const NoStage stage;
+    const LaSeqs s = sequences(a, pl);
+    if (make_offsets(a, pl, s, stream) != hipSuccess) return GDR_ELAUNCH;
     if (rest) {
-        const LaRest r = {a->cu_seqlens, a->T, (int)pl.n_seq, 1, {static_cast<uint32_t *>(a->o)}, {words(a->H_v * a->V, a->out_dtype)}};
+        const LaRest r = {s, 1, {static_cast<uint32_t *>(a->o)}, {words(a->H_v * a->V, a->out_dtype)}};
         if (launch_la_rest(r, stream) != hipSuccess) return GDR_ELAUNCH;
         if (pl.n_seq == 0) return GDR_OK;
     }
     char *ws = static_cast<char *>(a->workspace);
     float *border = pl.split ? reinterpret_cast<float *>(ws + pl.off_fwd) : nullptr;
     LaParams p = {};
-    p.s = sequences(a, pl);
+    p.s = s;
     p.n_jobs = 1, p.n_cb = pl.n_cb_v, p.split = pl.split, p.tokens = pl.tokens;
     LaJob &J = p.job[0];
     J.q = a->q, J.k = a->k, J.v = a->v;
@@ -245,6 +256,7 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     float *border_fwd = at(pl.off_fwd), *border_rev = at(pl.off_rev), *decays_fwd = at(pl.off_decays_fwd), *decays_rev = at(pl.off_decays_rev);
     float *dots_a = at(pl.off_dots), *dots_b = dots_a + (int64_t)pl.n_cb_k * H * pl.tokens;
     const LaSeqs s = sequences(a, pl);
+    if (make_offsets(a, pl, s, stream) != hipSuccess) return GDR_ELAUNCH;
 
     // the backward's scans: dq forwards over S^T, dv backwards over dS, dk backwards over dS^T
     LaJob dq = {}, dv = {}, dk = {};
@@ -311,7 +323,7 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     }
     if (rest) {  // (after the sums over the heads, which are made of every row)
         const int64_t qk = words(a->H_q * a->K, a->grad_dtype);
-        const LaRest r = {a->cu_seqlens, a->T, (int)pl.n_seq, a->g_per_head ? 3 : 4,
+        const LaRest r = {s, a->g_per_head ? 3 : 4,
                           {static_cast<uint32_t *>(a->dq), static_cast<uint32_t *>(a->dk), static_cast<uint32_t *>(a->dv), reinterpret_cast<uint32_t *>(a->dg)},
                           {qk, qk, words(a->H_v * a->V, a->grad_dtype), a->H_v}};
         if (launch_la_rest(r, stream) != hipSuccess) return GDR_ELAUNCH;

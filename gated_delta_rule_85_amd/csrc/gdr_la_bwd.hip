@@ -200,9 +200,12 @@ __global__ __launch_bounds__(256) void gdr_la_heads_kernel(const float *x, Out *
 // ------------------------------------------------------------------ la_rest
 // Rows before the first and behind the last of the packed sequences := 0.  (4 us where there are none.)
 __global__ __launch_bounds__(256) void gdr_la_rest_kernel(LaRest p) {
-    auto clamped = [&](int i) { return min(max((int64_t)p.cu[i], (int64_t)0), p.T); };
-    const int64_t first = p.n_seq > 0 ? clamped(0) : 0, end = p.n_seq > 0 ? max(clamped(p.n_seq), first) : 0;
-    for (int64_t i = blockIdx.x; i < first + p.T - end; i += gridDim.x) {
+    int64_t first = 0, end = 0, at;
+    if (p.s.n_seq > 0) {
+        la_bounds(p.s, 0, first, at);
+        la_bounds(p.s, p.s.n_seq - 1, at, end);
+    }
+    for (int64_t i = blockIdx.x; i < first + p.s.T - end; i += gridDim.x) {
         const int64_t row = i < first ? i : end + i - first;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -211,10 +214,33 @@ __global__ __launch_bounds__(256) void gdr_la_rest_kernel(LaRest p) {
     }
 }
 
+// ---------------------------------------------------------------- la_offsets
+// One workgroup, 1024 offsets at a time (5 us for 5000)
+__global__ __launch_bounds__(1024) void gdr_la_offsets_kernel(const int32_t *cu, int32_t *to, int64_t n, int64_t T) {
+    __shared__ int last[2][16];  // of each wave, two turns: between two writes of one lies a barrier after its reads
+    int before = 0, turn = 0;
+    for (int64_t first = 0; first < n; first += 1024, turn ^= 1) {
+        const int64_t i = first + threadIdx.x;
+        int x = la_running_max(la_offset(cu + first, T, (int)min(n - 1 - first, (int64_t)threadIdx.x)));
+        if (lane_id() == 63) last[turn][wave_id()] = x;
+        __syncthreads();
+        x = max(x, before);
+        for (int w = 0; w < 16; ++w) {
+            before = max(before, last[turn][w]);
+            if (w < (int)wave_id()) x = max(x, before);
+        }
+        if (i < n) to[i] = x;
+    }
+}
+
 }  // namespace
 
+hipError_t launch_la_offsets(const int32_t *cu, int32_t *to, int64_t n, int64_t T, hipStream_t s) {
+    launch_k(gdr_la_offsets_kernel, dim3(1), dim3(1024), 0, s, cu, to, n, T);
+    return hipGetLastError();
+}
 hipError_t launch_la_rest(const LaRest &p, hipStream_t s) {
-    launch_k(gdr_la_rest_kernel, dim3((uint32_t)(p.T < 1024 ? p.T : 1024)), dim3(256), 0, s, p);
+    launch_k(gdr_la_rest_kernel, dim3((uint32_t)(p.s.T < 1024 ? p.s.T : 1024)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 hipError_t launch_la_carry(const LaCarry &p, hipStream_t s) {

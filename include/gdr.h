@@ -277,8 +277,9 @@ typedef struct {
     const void *q, *k, *v;
     const float *g;
     const float *initial_state; /* [N,H_v,K,V], N = B or n_seq; NULL = zeros */
-    const int32_t *cu_seqlens;  /* [n_seq+1] token offsets (B = 1), or NULL.  On the device offsets outside
-                                   [0, T] are clamped to it, an end before its start to the start */
+    const int32_t *cu_seqlens;  /* [n_seq+1] token offsets (B = 1), or NULL: read on the device, each clamped
+                                   as in gdr_fwd_args.  Rows before the first and behind the last belong
+                                   to no sequence */
     void *o;                    /* [B,T,H_v,V] out_dtype */
     float *final_state;         /* [N,H_v,K,V]; NULL = not wanted */
     void *workspace;

@@ -591,3 +591,45 @@ def test_gradients_behind_resets(gdr, n, dtype):
     grads = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, x["initial_state"], grad_dtype=F32)
     for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "dh0"), grads, want, [TOL[F32]] * 3 + [TOL_GATES, TOL[F32]]):
         check(a, b, tol, name, want[5] if name == "dg" else 0.0)
+
+
+@pytest.mark.parametrize("kind", ["past the end", "before the start", "falls", "falls within", "long", "64", "80", "1500"])
+def test_offsets_on_the_device_are_made_to_rise(gdr, kind):
+    """Offsets outside [0, T], or smaller than one before them, give what the offsets give that they are
+    taken as: no sequence shares a row with another, and rows of none are zero."""
+    T, K, V = 200, 64, 128
+    if kind in ("64", "80", "1500"):
+        T = 3000
+        offsets = torch.randint(-50, T + 50, (int(kind) + 1,), generator=torch.Generator().manual_seed(int(kind)))
+        rising = (torch.arange(len(offsets)) * T / len(offsets)).long()
+        mixed = torch.rand(len(offsets), generator=torch.Generator().manual_seed(1)) < 0.1
+        offsets = torch.where(mixed, offsets.clamp(max=T // 2), rising).tolist()
+    else:
+        offsets = {"past the end": [0, 300, 200], "before the start": [-5, 100, 10 ** 6], "falls": [50, 20, 200],
+                   "falls within": [0, 100, 50, 180, 150], "long": [7, 1500, 700, 2900, 100, 2901]}[kind]
+        T = 3000 if kind == "long" else T
+    good = list(itertools.accumulate((min(max(i, 0), T) for i in offsets), max))
+    N = len(good) - 1
+    x = inputs(1, T, 1, 2, K, V, BF)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    h0, dht = (torch.randn(N, 2, K, V, device="cuda", generator=gen) for _ in range(2))
+    do = torch.randn(1, T, 2, V, device="cuda", generator=gen).to(BF)
+    runs = []
+    for cu in (good, offsets):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        run = []
+        for segment in (0, 1, 2, 1 << 20):
+            run += gdr.chunk_linear_attention_fwd(x["q"], x["k"], x["v"], x["g"], None, h0, cu, segment_chunks=segment)
+            run += gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, h0, cu, segment_chunks=segment)
+        torch.cuda.synchronize()
+        runs.append(run)
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+    names = ["o", "hT", "dq", "dk", "dv", "dg", "dh0"]
+    for name, t in zip(itertools.cycle(names), runs[1]):
+        assert t.isfinite().all(), name
+        if name not in ("hT", "dh0"):
+            assert not t[:, :good[0]].any() and not t[:, good[-1]:].any(), name
+    # what they are taken as is right
+    want = exact(dict(x, initial_state=h0, cu_seqlens=torch.tensor(good)), do, dht)
+    for name, got, b in zip(names, runs[1], want):
+        check(got, b, TOL_GATES if name == "dg" else TOL[got.dtype], name, want[7] if name == "dg" else 0.0)
