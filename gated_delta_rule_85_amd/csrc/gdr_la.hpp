@@ -8,8 +8,9 @@
 namespace gdr {
 
 // The sequences, their gates, and their segments of seg_chunks chunks.  Border b of a sequence
-// (1 <= b < its segments) lies before token 64 seg_chunks b.  What is kept per segment or border
-// of all sequences is indexed by la_first() + its number; there are la_slots() such places.
+// (1 <= b < its segments) lies before token 64 seg_chunks b.  What is kept per segment of all
+// sequences is indexed by la_first() + its number; there are la_slots() such places.  The states at
+// the borders are indexed by la_before() + b; there are la_borders() of them.
 struct LaSeqs {
     const int32_t *cu;  // [n_seq + 1] or null; of more than LA_WAVE_SEQS sequences, launch_la_offsets' table
     const float *g;
@@ -55,9 +56,17 @@ __device__ __forceinline__ void la_bounds(const LaSeqs &s, int j, int64_t &bos, 
 __device__ __forceinline__ int la_first(const LaSeqs &s, int64_t bos, int j, int64_t seg_tokens) {
     return s.cu ? (int)((uint32_t)bos / (uint32_t)seg_tokens) + j : j * s.n_seg;  // (a segment has at most 2^31 tokens)
 }
+// place before a sequence's first border.  Packed: a sequence's borders are no more than the whole
+// multiples of seg_tokens that it reaches, (bos + n) / seg_tokens - bos / seg_tokens
+__device__ __forceinline__ int la_before(const LaSeqs &s, int64_t bos, int j, int64_t seg_tokens) {
+    return (s.cu ? (int)((uint32_t)bos / (uint32_t)seg_tokens) : j * (s.n_seg - 1)) - 1;
+}
 inline int64_t la_segments(int64_t T, int64_t seg_tokens) { return T > seg_tokens ? (T + seg_tokens - 1) / seg_tokens : 1; }
 inline int64_t la_slots(bool packed, int64_t T, int64_t n_seq, int64_t seg_tokens) {
     return packed ? T / seg_tokens + n_seq : n_seq * la_segments(T, seg_tokens);
+}
+inline int64_t la_borders(bool packed, int64_t T, int64_t n_seq, int64_t seg_tokens) {
+    return packed ? T / seg_tokens : n_seq * (la_segments(T, seg_tokens) - 1);
 }
 // sequence and segment of a place (false: none); of whole waves.  64 sequences are looked at in a step
 __device__ __forceinline__ bool la_place(const LaSeqs &s, int place, int &j, int &m) {
@@ -111,8 +120,9 @@ struct LaJob {
     void *o;              // [tokens][Hv][W]
     const float *init;    // [n_seq][Hv] states, or null: zero
     float *fin;           // [n_seq][Hv] last states (rev: times e^g of the first token), or null
-    float *border;        // [places][Hv] states at the borders, or null
-    float *border_fin;    // [places][Hv]: the last state at the sequence's first place, or null
+    float *border;        // [borders][Hv] states, or null
+    const float *with;    // [n_seq][Hv] states, or null: last[n_seq][Hv][W / 16] (scale 1), a wave's part each, becomes
+    double2 *last;        // the product of the last state with them and the sum of its terms' squares (dots; trans)
     float *decays;        // [places][Hv] the segments' whole decays (launch_la_states)
     // dots[cb][hv][token] = sum over the block's 64 columns of o and e (rows like o's), or null
     const void *e;
@@ -141,8 +151,10 @@ struct LaCarry {
 
 struct LaGates {
     LaSeqs s;
-    const float *fwd, *rev;  // states and their gradients at the borders (fwd at place 0: the last state)
-    const float *dht, *h0, *dh0;  // [n_seq][Hv] or null
+    const float *fwd, *rev;  // states and their gradients at the borders
+    const double2 *last;     // [n_seq][Hv][n_last] parts of <last state, dht> and of its terms' squares, or null
+    int n_last;
+    const float *h0, *dh0;   // [n_seq][Hv] or null
     const float *a, *b;      // [n_a | n_b][Hv][tokens] dots
     int n_a, n_b, KV;
     int64_t tokens;

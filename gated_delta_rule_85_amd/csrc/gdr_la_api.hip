@@ -81,7 +81,7 @@ struct Plan {
     int group, n_cb_k, n_cb_v;  // blocks of columns, where K or V columns are scanned
     bool split;
     int seg_chunks;
-    size_t offsets_bytes, off_offsets, border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, off_at, total;
+    size_t offsets_bytes, off_offsets, border_bytes, decays_bytes, off_fwd, off_rev, off_decays_fwd, off_decays_rev, off_dots, off_dq, off_dk, off_gates, off_at, off_last, total;
 };
 
 template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
@@ -103,7 +103,7 @@ template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
     if (std::max(p.places, p.n_seq) * a->H_v * 16 >= (int64_t)1 << 23) return GDR_EINVAL;
     const bool whole = wide(a->dtype, (p.split ? p.places : p.n_seq) * a->H_v);
     p.n_cb_k = a->K == 128 && !whole ? 2 : 1, p.n_cb_v = a->V == 128 && !whole ? 2 : 1;
-    p.border_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v * a->K * a->V));
+    p.border_bytes = up(sizeof(float) * (size_t)(la_borders(varlen, a->T, p.n_seq, p.seg_tokens) * a->H_v * a->K * a->V));
     p.decays_bytes = up(sizeof(float) * (size_t)(p.places * a->H_v));
     p.offsets_bytes = varlen && p.n_seq > LA_WAVE_SEQS ? up(sizeof(int32_t) * (size_t)(p.n_seq + 1)) : 0;
     return GDR_OK;
@@ -140,6 +140,7 @@ int plan_bwd(const gdr_la_bwd_args *a, Plan &p) {
     p.off_dq = take(p.group > 1 ? tokens * a->K : 0), p.off_dk = take(p.group > 1 ? tokens * a->K : 0);
     p.off_gates = take(p.decays_bytes);
     p.off_at = take(4 * p.decays_bytes);
+    p.off_last = take(sizeof(double2) * (size_t)(p.n_seq * a->H_v * (a->K / 16)));
     p.off_offsets = take(p.offsets_bytes);
     p.total = off;
     return GDR_OK;
@@ -265,7 +266,8 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
     dq.v = a->k, dq.v_row = a->k_row, dq.v_batch = a->k_batch, dq.v_div = group;
     dq.e = a->q, dq.e_row = a->q_row, dq.e_batch = a->q_batch, dq.e_div = group, dq.dots = dots_a;
     dq.W = K, dq.trans = 1, dq.in_scale = 1.f, dq.out_scale = a->scale;
-    dq.init = a->initial_state, dq.border = border_fwd, dq.border_fin = a->dht ? border_fwd : nullptr;
+    dq.init = a->initial_state, dq.border = border_fwd;
+    dq.with = a->dht, dq.last = reinterpret_cast<double2 *>(ws + pl.off_last);
 
     dv.q = a->k, dv.q_row = a->k_row, dv.q_batch = a->k_batch, dv.q_div = group;
     dv.k = a->q, dv.k_row = a->q_row, dv.k_batch = a->q_batch, dv.k_div = group;
@@ -317,7 +319,7 @@ int gdr_la_bwd(const gdr_la_bwd_args *a, hipStream_t stream) {
             if (launch_la_heads(static_cast<float *>(dq.o), a->dq, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
             if (launch_la_heads(static_cast<float *>(dk.o), a->dk, gt, pl.tokens, (int)a->H_q, group, K, stream) != hipSuccess) return GDR_ELAUNCH;
         }
-        LaGates g = {s, border_fwd, border_rev, a->dht, a->initial_state, a->dh0, dots_a, dots_b, pl.n_cb_k, pl.n_cb_v, K * V, pl.tokens,
+        LaGates g = {s, border_fwd, border_rev, a->dht ? dq.last : nullptr, K / 16, a->initial_state, a->dh0, dots_a, dots_b, pl.n_cb_k, pl.n_cb_v, K * V, pl.tokens,
                      reinterpret_cast<double2 *>(ws + pl.off_at), a->g_per_head ? at(pl.off_gates) : a->dg};
         if (launch_la_gates(g, (int)pl.places, stream) != hipSuccess) return GDR_ELAUNCH;
     }

@@ -15,11 +15,12 @@ __global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
     la_bounds(p.s, j, bos, eos);
     const int64_t seg_tokens = (int64_t)p.s.seg_chunks * CH;
     const int n_seg = (int)((eos - bos + seg_tokens - 1) / seg_tokens), place = la_first(p.s, bos, j, seg_tokens);
+    const int64_t first_border = la_before(p.s, bos, j, seg_tokens) + 1;
     if (n_seg < 3) return;
     const int64_t stride = (int64_t)p.s.Hv * p.KV;
-    float *s = p.border + ((int64_t)place * p.s.Hv + hv) * p.KV + (blockIdx.x - unit * per) * 1024 + 4 * threadIdx.x;
+    float *s = p.border + (first_border * p.s.Hv + hv) * p.KV + (blockIdx.x - unit * per) * 1024 + 4 * threadIdx.x;
     const float *d = p.decays + (int64_t)place * p.s.Hv + hv;
-    auto at = [&](int b) { return reinterpret_cast<f32x4 *>(s + b * stride); };
+    auto at = [&](int b) { return reinterpret_cast<f32x4 *>(s + (b - 1) * stride); };
     auto border = [&](int i) { return p.rev ? n_seg - i : i; };
     f32x4 x = *at(border(1));
     constexpr int N = 8;  // borders read at a time, a group ahead of the sums
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(256) void gdr_la_borders_kernel(LaGates p) {
     la_bounds(p.s, j, bos, eos);
     double2 at = {0.0, 0.0};
     if (m > 0) {
-        const int64_t border = (int64_t)blockIdx.x * p.KV;
+        const int64_t at_border = la_before(p.s, bos, j, (int64_t)p.s.seg_chunks * CH) + m, border = (at_border * p.s.Hv + hv) * p.KV;
         const float g = p.s.g[(bos + m * (int64_t)p.s.seg_chunks * CH) * p.s.g_tok + hv];
         at = product(p.fwd + border, p.rev + border, p.KV, expf(g), lds);
     } else if (p.h0) {
@@ -120,8 +121,11 @@ __global__ __launch_bounds__(256) void gdr_la_gates_kernel(LaGates p) {
     double2 far = {0.0, 0.0};
     if (hi < len)
         far = p.at[blockIdx.x + p.s.Hv];
-    else if (p.dht)
-        far = product(p.fwd + ((int64_t)(place - m) * p.s.Hv + hv) * p.KV, p.dht + ((int64_t)j * p.s.Hv + hv) * p.KV, p.KV, 1.0, lds);
+    else if (p.last)
+        for (int i = 0; i < p.n_last; ++i) {
+            const double2 part = p.last[((int64_t)j * p.s.Hv + hv) * p.n_last + i];
+            far.x += part.x, far.y += part.y;
+        }
     // a segment's 1024 tokens at most, four per thread
     const int64_t t0 = hi - 1024 + 4 * tid, plane = (int64_t)p.s.Hv * p.tokens;
     double d[4], v[4];

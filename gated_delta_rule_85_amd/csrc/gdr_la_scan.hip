@@ -244,7 +244,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
     const LaParams &p;
     const LaJob &J;
     char *const lds;
-    int cb, hv, j, m, len, nc, n_it, c_first, first_place;
+    int cb, hv, j, m, len, nc, n_it, c_first, first_place, before_border;
     int64_t bos;
     bool rev, starts, ends;
     int l, n16, g, w;
@@ -264,6 +264,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
         rev = J.rev;
         len = (int)(eos - bos), nc = (len + CH - 1) / CH;
         first_place = la_first(p.s, bos, j, (int64_t)p.s.seg_chunks * CH);
+        before_border = la_before(p.s, bos, j, (int64_t)p.s.seg_chunks * CH);
         const int n_seg = p.split ? max(1, (nc + p.s.seg_chunks - 1) / p.s.seg_chunks) : 1;
         const int c_lo = p.split ? m * p.s.seg_chunks : 0, c_hi = p.split ? min(nc, c_lo + p.s.seg_chunks) : nc;
         n_it = c_hi - c_lo, c_first = rev ? c_hi - 1 : c_lo;
@@ -311,7 +312,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
     __device__ __forceinline__ int64_t unit() const { return (int64_t)j * p.s.Hv + hv; }
     __device__ __forceinline__ void start_state(f32x4 (&h)[RT]) const {
         if (starts ? J.init != nullptr : OUT) {
-            load_state(starts ? J.init + unit() * KD * J.W : at_place(J.border, first_place + (rev ? m + 1 : m)), h);
+            load_state(starts ? J.init + unit() * KD * J.W : at_place(J.border, before_border + (rev ? m + 1 : m)), h);
         } else {
 #pragma unroll
             for (int t = 0; t < RT; ++t) h[t] = zero4();
@@ -323,7 +324,20 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
             if (rev && len > 0) f = fast_exp(p.s.g[bos * p.s.g_tok + hv]);
             store_state(J.fin + unit() * KD * J.W, h, f);
         }
-        if (ends && J.border_fin) store_state(at_place(J.border_fin, first_place), h, 1.f);
+        if constexpr (DOTS)
+            if (ends && J.with) {
+                const float *s = J.with + unit() * KD * J.W + (int64_t)(cb * BW + 16 * ct() + n16) * KD;
+                f32x4 d = zero4(), v = zero4();
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const f32x4 z = h[t] * *glb(reinterpret_cast<const f32x4 *>(s + row0() + slot_base(t, g)));
+                    d += z, v += z * z;
+                }
+                double2 x = {(double)((d[0] + d[1]) + (d[2] + d[3])), (double)((v[0] + v[1]) + (v[2] + v[3]))};
+#pragma unroll
+                for (int i = 32; i; i >>= 1) x.x += __shfl_xor(x.x, i), x.y += __shfl_xor(x.y, i);
+                if (l == 0) J.last[unit() * (J.W / 16) + cb * (BW / 16) + ct()] = x;
+            }
     }
 
     // ----------------------------------------------------------------- copies
@@ -752,7 +766,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
             if (--to_border == 0) {
                 to_border = p.s.seg_chunks;
                 const int after = rev ? c : c + 1;  // chunks before the border
-                if (after > 0 && after < nc) store_state(at_place(J.border, first_place + after / p.s.seg_chunks), h, 1.f);
+                if (after > 0 && after < nc) store_state(at_place(J.border, before_border + after / p.s.seg_chunks), h, 1.f);
             }
             wait_copies();
             lds_barrier();
@@ -817,7 +831,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
             }
             buf = buf + 1 == Y::NB ? 0 : buf + 1;
         }
-        store_state(at_place(J.border, first_place + (rev ? m : m + 1)), h, 1.f);
+        store_state(at_place(J.border, before_border + (rev ? m : m + 1)), h, 1.f);
         if (cb == 0 && threadIdx.x == 0) J.decays[(int64_t)(first_place + m) * p.s.Hv + hv] = whole;
     }
 };

@@ -255,3 +255,22 @@ def test_norm_validation():
     assert _lib.lib.gdr_group_norm_bwd(ctypes.byref(args(_lib.NormBwdArgs)), None) == _lib.EWORKSPACE
     assert _lib.lib.gdr_group_norm(ctypes.byref(args(_lib.NormFwdArgs, M=0)), None) == 0
     assert _lib.lib.gdr_group_norm_bwd(ctypes.byref(args(_lib.NormBwdArgs, M=0, dweight=None, dbias=None)), None) == 0
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("N,length", [(4096, 64), (512, 1024), (100, 1100), (1, 70000), (3, 1)])
+def test_workspace_holds_the_borders_alone(N, length, packed):
+    """No state is kept of a sequence that has no border: the backward's borders are 1024 tokens apart at most,
+    those of packed sequences as many as 1024 fits into all tokens."""
+    H, K, V = 64, 128, 128
+    sizes = dict(T=N * length, B=1, cu_seqlens=64, n_seq=N) if packed else dict(T=length, B=N)
+    kw = dict(sizes, H_q=H, H_v=H, K=K, V=V, q_row=H * K, k_row=H * K, v_row=H * V, segment_chunks=16, q_batch=0, k_batch=0, v_batch=0)
+    borders = N * length // 1024 if packed else N * (-(-length // 1024) - 1)
+    places = N + N * length // 1024 if packed else N * -(-length // 1024)
+    # two states a border, and per token, place and sequence no more than a few numbers a head
+    few = 4 * H * (4 * N * length + 40 * places + 32 * N) + 16 * 256
+    n = ctypes.c_size_t(0)
+    assert _lib.lib.gdr_la_bwd_workspace(ctypes.byref(la_args(_lib.LaBwdArgs, **kw)), ctypes.byref(n)) == 0
+    assert n.value <= 2 * borders * 4 * H * K * V + few
+    assert _lib.lib.gdr_la_fwd_workspace(ctypes.byref(la_args(_lib.LaFwdArgs, **kw)), ctypes.byref(n)) == 0
+    assert n.value <= borders * 4 * H * K * V + few
