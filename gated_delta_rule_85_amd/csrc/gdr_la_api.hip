@@ -93,14 +93,17 @@ template <typename Args> int plan(const Args *a, bool backward, Plan &p) {
     int64_t L = a->segment_chunks ? a->segment_chunks
                                   : split_chunks(a->dtype, nct, std::max<int64_t>(p.n_seq, 1), varlen, a->H_v,
                                                  std::max(a->V, backward ? a->K : 0) / 64, backward ? 3 : 1, backward ? 2 : 1);
+    const int64_t limit = (int64_t)1 << 22;  // (sequence or segment, v head) pairs
     p.split = L > 0 && L < nct;
     if (backward) L = L > 0 ? std::min<int64_t>(L, BORDER_CHUNKS) : BORDER_CHUNKS;
+    // (no split of its own accord into too many)
+    if (p.split && !a->segment_chunks && la_slots(varlen, a->T, p.n_seq, L * CH) * a->H_v >= limit) p.split = false;
     if (!p.split && !backward) L = std::max<int64_t>(nct, 1);
     p.seg_chunks = (int)L;
     p.seg_tokens = L * CH;
     p.places = la_slots(varlen, a->T, p.n_seq, p.seg_tokens);
-    // 32-bit numbers of workgroups and work-items
-    if (std::max(p.places, p.n_seq) * a->H_v * 16 >= (int64_t)1 << 23) return GDR_EINVAL;
+    // 32-bit numbers of work-items: 1024 at most per pair, 256 of the backward's borders where there is no split
+    if ((p.split ? p.places : p.n_seq) * a->H_v >= limit || p.places * a->H_v >= 4 * limit) return GDR_EINVAL;
     const bool whole = wide(a->dtype, (p.split ? p.places : p.n_seq) * a->H_v);
     p.n_cb_k = a->K == 128 && !whole ? 2 : 1, p.n_cb_v = a->V == 128 && !whole ? 2 : 1;
     p.border_bytes = up(sizeof(float) * (size_t)(la_borders(varlen, a->T, p.n_seq, p.seg_tokens) * a->H_v * a->K * a->V));

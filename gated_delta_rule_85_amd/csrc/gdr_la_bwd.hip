@@ -9,8 +9,8 @@ namespace {
 // border states from their segments' own: S_b += D_{b-1} S_{b-1} for b = 2 .. (rev: from the last
 // border down, S_b += D_b S_{b+1}).  A thread takes four elements of a (sequence, head) along; what it
 // reads does not wait for its sums (31 borders of 8 heads: 9.1 us in place of 12.9).
-__global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
-    const int per = p.KV / 1024, unit = blockIdx.x / per, j = unit / p.s.Hv, hv = unit - j * p.s.Hv;
+__device__ __forceinline__ void carry(const LaCarry &p, int block) {
+    const int per = p.KV / 1024, unit = block / per, j = unit / p.s.Hv, hv = unit - j * p.s.Hv;
     int64_t bos, eos;
     la_bounds(p.s, j, bos, eos);
     const int64_t seg_tokens = (int64_t)p.s.seg_chunks * CH;
@@ -18,7 +18,7 @@ __global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
     const int64_t first_border = la_before(p.s, bos, j, seg_tokens) + 1;
     if (n_seg < 3) return;
     const int64_t stride = (int64_t)p.s.Hv * p.KV;
-    float *s = p.border + (first_border * p.s.Hv + hv) * p.KV + (blockIdx.x - unit * per) * 1024 + 4 * threadIdx.x;
+    float *s = p.border + (first_border * p.s.Hv + hv) * p.KV + (block - unit * per) * 1024 + 4 * threadIdx.x;
     const float *d = p.decays + (int64_t)place * p.s.Hv + hv;
     auto at = [&](int b) { return reinterpret_cast<f32x4 *>(s + (b - 1) * stride); };
     auto border = [&](int i) { return p.rev ? n_seg - i : i; };
@@ -46,6 +46,12 @@ __global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
             *at(border(first + i)) = x;
         }
     }
+}
+// (a grid of any number of (sequence, head) pairs has a bounded number of work-items)
+constexpr int CARRY_WORKGROUPS = 1 << 20;
+__global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
+    const int blocks = p.s.n_seq * p.s.Hv * (p.KV / 1024);
+    for (int block = blockIdx.x; block < blocks; block += gridDim.x) carry(p, block);
 }
 
 // ------------------------------------------------------------------ la_gates
@@ -248,7 +254,8 @@ hipError_t launch_la_rest(const LaRest &p, hipStream_t s) {
     return hipGetLastError();
 }
 hipError_t launch_la_carry(const LaCarry &p, hipStream_t s) {
-    launch_k(gdr_la_carry_kernel, dim3((uint32_t)p.s.n_seq * p.s.Hv * (p.KV / 1024)), dim3(256), 0, s, p);
+    const int64_t blocks = (int64_t)p.s.n_seq * p.s.Hv * (p.KV / 1024);
+    launch_k(gdr_la_carry_kernel, dim3((uint32_t)(blocks < CARRY_WORKGROUPS ? blocks : CARRY_WORKGROUPS)), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 hipError_t launch_la_gates(const LaGates &p, int items, hipStream_t s) {

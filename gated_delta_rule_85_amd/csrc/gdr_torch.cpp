@@ -487,6 +487,7 @@ struct Linear {
             if (!cu->is_cuda()) check_offsets(*cu, T);
             n_seq = cu->numel() - 1;
         }
+        NEED(n_seq * H_v < (int64_t)1 << 22, "sequences times v heads must be below 2^22");
         check_states(h0, "initial_state");
         const at::Device dev = q->device();
         NEED(dev.is_cuda(), "inputs must be on the GPU");

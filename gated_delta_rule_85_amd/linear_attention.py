@@ -23,7 +23,8 @@ def chunk_linear_attention_fwd(q, k, v, g, scale=None, initial_state=None, cu_se
     q, k and v may be slices of a wider projection: they are read in place where a token's
     heads are contiguous.  A long sequence of few heads is split into segments of
     ``segment_chunks`` chunks of 64 tokens (0: chosen for the device; the split is exact: a
-    segment's part of the state is carried on by a scalar decay).  A gate of -104 or less,
+    segment's part of the state is carried on by a scalar decay).  Sequences (segments) times H_v
+    are below 2^22.  A gate of -104 or less,
     -inf among them, empties the state.  Rows of o that belong to no sequence are zero, and so
     are those of its gradients.
     """

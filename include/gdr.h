@@ -265,7 +265,9 @@ typedef struct {
    the sequence, into NaN; other sequences and other heads' states do not meet it.
    B, T and n_seq may be 0. */
 typedef struct {
-    int64_t B, T, H_q, H_v, K, V, n_seq; /* sizes as in gdr_fwd_args; B T below 2^31 - 64 */
+    /* sizes as in gdr_fwd_args; B T below 2^31 - 64, H_v below 2^16, and the sequences (where they are
+       split, segments) times H_v below 2^22 */
+    int64_t B, T, H_q, H_v, K, V, n_seq;
     /* elements between tokens' rows and between batch rows, as in gdr_pool_args */
     int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;
     int32_t dtype;          /* element type of q, k, v */
@@ -288,7 +290,7 @@ typedef struct {
 } gdr_la_fwd_args;
 
 typedef struct {
-    int64_t B, T, H_q, H_v, K, V, n_seq;
+    int64_t B, T, H_q, H_v, K, V, n_seq; /* as in gdr_la_fwd_args */
     int64_t q_row, k_row, v_row, q_batch, k_batch, v_batch;
     int32_t dtype;          /* element type of q, k, v and dout */
     int32_t grad_dtype;     /* element type of dq, dk, dv */

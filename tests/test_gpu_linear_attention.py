@@ -633,3 +633,34 @@ def test_offsets_on_the_device_are_made_to_rise(gdr, kind):
     want = exact(dict(x, initial_state=h0, cu_seqlens=torch.tensor(good)), do, dht)
     for name, got, b in zip(names, runs[1], want):
         check(got, b, TOL_GATES if name == "dg" else TOL[got.dtype], name, want[7] if name == "dg" else 0.0)
+
+
+def test_many_sequences_and_heads(gdr):
+    """640000 (sequence, head) pairs, most of them of one token: long sequences among them are bit for bit
+    what they are alone, and single tokens what their products are."""
+    N, long, H, K = 40000, 700, 16, 64
+    lens = torch.ones(N, dtype=torch.int64)
+    lens[[5, N - 2]] = long
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    T = int(cu[-1])
+    x = inputs(1, T, H, H, K, K, BF)
+    do = torch.randn(1, T, H, K, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7)).to(BF)
+    leaves = [x[n] for n in ("q", "k", "v", "g")]
+    offsets = cu.to(device="cuda", dtype=torch.int32)
+    for segment in (2, 1 << 20):
+        o, _ = gdr.chunk_linear_attention_fwd(*leaves, None, None, offsets, False, segment_chunks=segment)
+        grads = gdr.chunk_linear_attention_bwd(*leaves, do, None, None, None, offsets, segment_chunks=segment)
+        for j in (5, N - 2):
+            at = slice(int(cu[j]), int(cu[j + 1]))
+            alone = [t[:, at].contiguous() for t in leaves]
+            want = gdr.chunk_linear_attention_fwd(*alone, None, None, None, False, segment_chunks=segment)[:1]
+            want += gdr.chunk_linear_attention_bwd(*alone, do[:, at].contiguous(), segment_chunks=segment)
+            assert all(torch.equal(a[:, at], b) for a, b in zip((o,) + grads[:4], want[:5]))
+        single = torch.ones(T, dtype=torch.bool)
+        single[cu[5]:cu[6]] = single[cu[N - 2]:cu[N - 1]] = False
+        q, k, v, d = (t[0, single.cuda()].double() for t in (x["q"], x["k"], x["v"], do))
+        qk, vd = K ** -0.5 * (q * k).sum(-1, keepdim=True), K ** -0.5 * (v * d).sum(-1, keepdim=True)
+        for got, want, tol in zip((o,) + grads, (qk * v, vd * k, vd * q, qk * d), (TOL[F32], TOL[BF], TOL[BF], TOL[BF])):
+            check(got[0, single.cuda()], want, tol, "single tokens")
+        # (no state before them: nothing depends on their gates)
+        assert grads[3][0, single.cuda()].abs().max() <= TOL_GATES * (q * k).sum(-1).abs().max() * (v * d).sum(-1).abs().max()

@@ -274,3 +274,24 @@ def test_workspace_holds_the_borders_alone(N, length, packed):
     assert n.value <= 2 * borders * 4 * H * K * V + few
     assert _lib.lib.gdr_la_fwd_workspace(ctypes.byref(la_args(_lib.LaFwdArgs, **kw)), ctypes.byref(n)) == 0
     assert n.value <= borders * 4 * H * K * V + few
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_chunked_sequences_times_heads(which):
+    """Up to 2^22 (sequence, v head) pairs, and (segment, v head) pairs."""
+    st = _lib.LaFwdArgs if which == "fwd" else _lib.LaBwdArgs
+    n = ctypes.c_size_t(0)
+    for N, H, T, segment, packed, ok in ((1 << 13, 64, 1, 0, False, True), ((1 << 22) - 1, 1, 1, 0, False, True),
+                                         (1 << 22, 1, 1, 0, False, False), ((1 << 16) - 1, 64, 1 << 16, 0, True, True),
+                                         (1 << 16, 64, 1 << 16, 0, True, False), (1, 63, 1 << 22, 1, False, True),
+                                         (1, 64, 1 << 22, 1, False, False)):
+        a = la_args(st, B=1 if packed else N, T=T, H_q=H, H_v=H, K=64, V=64, q_row=H * 64, k_row=H * 64, v_row=H * 64, q_batch=0,
+                    k_batch=0, v_batch=0, segment_chunks=segment, **(dict(cu_seqlens=64, n_seq=N) if packed else {}))
+        rc = getattr(_lib.lib, "gdr_la_%s_workspace" % which)(ctypes.byref(a), ctypes.byref(n))
+        assert rc == (_lib.OK if ok else _lib.EINVAL), (N, H, T)
+
+
+def test_too_many_sequences_are_refused_by_name():
+    q = torch.zeros(1 << 16, 1, 64, 64, dtype=BF)[:, :0]
+    with pytest.raises(ValueError, match="sequences"):
+        gdr.chunk_linear_attention_fwd(q, q, q, torch.zeros(1 << 16, 0, 64))
