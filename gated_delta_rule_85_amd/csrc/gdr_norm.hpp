@@ -78,8 +78,9 @@ __device__ __forceinline__ float norm_act(int act, float z, float &slope) {
         slope = 1.f;
         return z;
     }
-    const float s = norm_sigmoid(z);
-    slope = act == ACT_SILU ? fmaf(s * z, 1.f - s, s) : s * (1.f - s);
+    const float e = fast_exp(-z), s = __builtin_amdgcn_rcpf(1.f + e);
+    // (the sigmoid's own slope by 1 - s = e s where s is near 1)
+    slope = act == ACT_SILU ? fmaf(s * z, 1.f - s, s) : s * (z > 0.f ? e * s : 1.f - s);
     return act == ACT_SILU ? z * s : s;
 }
 

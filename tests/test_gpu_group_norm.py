@@ -258,3 +258,22 @@ def test_wide_groups_off_a_multiple_of_eight(gdr, D):
             check(g[2], db, F32, "dbias")
             if gate is not None:
                 check(g[3], dz, gate, "dgate")
+
+
+@pytest.mark.parametrize("gated", [True, False])
+def test_slope_of_a_sigmoid_near_one(gdr, gated):
+    """Where the sigmoid is near 1 its slope is small, and every value of it is as precise as elsewhere: the
+    exponential's argument is rounded, 2^-24 |z|, and fewer than sixteen roundings follow."""
+    z = torch.linspace(-30, 30, 4096, device="cuda").view(4, 1024)
+    ones = torch.ones_like(z)
+    if gated:  # y = 1: dgate is the slope
+        weight, bias = torch.zeros(1024, device="cuda"), torch.ones(1024, device="cuda")
+        got = gdr.group_norm_bwd(torch.randn(4, 1024, device="cuda"), 8, ones, weight, bias, z, activation="sigmoid")[3]
+        at = z.double()
+    else:  # y = bias: dbias is the slope
+        got = torch.stack([gdr.group_norm_bwd(ones[:1], 8, ones[:1], ones[0], row, activation="sigmoid")[2] for row in z])
+        at = z.double()
+    e = torch.exp(-at.abs())
+    want = e / (1 + e) ** 2
+    off = (got.double() - want).abs() / (want * 2.0 ** -24 * (16 + 2 * at.abs()))
+    assert off.max() <= 1, "%.3g times the tolerance at %.3g" % (off.max(), at.flatten()[off.argmax()])
