@@ -49,18 +49,18 @@ template <typename T> __device__ __forceinline__ Glb<T> *glb(T *p) { return (Glb
 // Wave-wide copies of 64 x 16 (or 4) bytes global -> LDS, lane l's to 16 l (4 l) past `to`.  As
 // instructions of their own: before any read of LDS the compiler waits for every copy that it knows to
 // be in flight, whichever buffer is read, and with it for the latency of memory in every chunk.
-// wait_copies() and a barrier come before what is copied is read.
+// Nothing else here uses m0; wait_copies() and a barrier come before what is copied is read.
 __device__ __forceinline__ void copy16(const char *base, uint32_t off, const char *to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(off), "s"(base)
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void copy4(const char *base, uint32_t off, const char *to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to)), "v"(off), "s"(base)
-                 : "memory", "m0");
+                 : "memory");
 }
 // until no more than the last N instructions that touch memory are under way: they end in order, and any
 // others than copies among them make the wait longer, never shorter
