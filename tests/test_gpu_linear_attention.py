@@ -664,3 +664,23 @@ def test_many_sequences_and_heads(gdr):
             check(got[0, single.cuda()], want, tol, "single tokens")
         # (no state before them: nothing depends on their gates)
         assert grads[3][0, single.cuda()].abs().max() <= TOL_GATES * (q * k).sum(-1).abs().max() * (v * d).sum(-1).abs().max()
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("N,T,Hq,Hv,segment", [(16, 131, 16, 16, 0), (32, 70, 4, 8, 0), (1, 4100, 2, 4, 1), (3, 700, 8, 8, 1)])
+def test_full_device(gdr, N, T, Hq, Hv, segment, K, V):
+    """256 and more (sequence or segment, head) pairs: a workgroup takes 128 columns."""
+    x = inputs(N, T, Hq, Hv, K, V, BF, h0=True, seed=T)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    do = torch.randn(x["v"].shape, device="cuda", generator=gen).to(BF)
+    dht = torch.randn(x["initial_state"].shape, device="cuda", generator=gen)
+    o, hT, *want = exact(x, do, dht)
+    for out in (BF, F32):
+        got, last = gdr.chunk_linear_attention_fwd(**x, output_dtype=out, segment_chunks=segment)
+        check(got, o, TOL[out], "o")
+        check(last, hT, TOL[F32], "final_state")
+    for grad in (BF, F32):
+        grads = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, x["initial_state"],
+                                               grad_dtype=grad, segment_chunks=segment)
+        for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "dh0"), grads, want, [TOL[grad]] * 3 + [TOL_GATES, TOL[F32]]):
+            check(a, b, tol, name, want[5] if name == "dg" else 0.0)
