@@ -49,7 +49,8 @@ template <typename T> __device__ __forceinline__ Glb<T> *glb(T *p) { return (Glb
 // Wave-wide copies of 64 x 16 (or 4) bytes global -> LDS, lane l's to 16 l (4 l) past `to`.  As
 // instructions of their own: before any read of LDS the compiler waits for every copy that it knows to
 // be in flight, whichever buffer is read, and with it for the latency of memory in every chunk.
-// Nothing else here uses m0; wait_copies() and a barrier come before what is copied is read.
+// Nothing else here uses m0, which the compiler reserves: it holds no value there, and warns of a
+// clobber.  wait_copies() and a barrier come before what is copied is read.
 __device__ __forceinline__ void copy16(const char *base, uint32_t off, const char *to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
@@ -619,10 +620,10 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
         auto dots_at = [&](int buf) { return reinterpret_cast<float *>(lds + Y::OFF_S) + buf * NW * CH; };
         auto store_dots = [&](int it, int buf) {  // one wave, a row per lane
             const int c = chunk_of(it), n = rows_of(c);
-            float d = 0.f;
+            double d = 0.0;  // (gate gradients are what is left of many of these)
 #pragma unroll
-            for (int i = 0; i < NW; ++i) d += dots_at(buf)[i * CH + l];
-            if (l < n) glb(d0)[c * CH + token_of(l, n)] = d;
+            for (int i = 0; i < NW; ++i) d += (double)dots_at(buf)[i * CH + l];
+            if (l < n) glb(d0)[c * CH + token_of(l, n)] = (float)d;
         };
         // of the chunk before: its Q h, V and part of e
         f32x4 o[4] = {zero4(), zero4(), zero4(), zero4()};

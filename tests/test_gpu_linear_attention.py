@@ -684,3 +684,20 @@ def test_full_device(gdr, N, T, Hq, Hv, segment, K, V):
                                                grad_dtype=grad, segment_chunks=segment)
         for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "dh0"), grads, want, [TOL[grad]] * 3 + [TOL_GATES, TOL[F32]]):
             check(a, b, tol, name, want[5] if name == "dg" else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gate_gradients_over_long_segments(gdr, dtype):
+    """Between two borders 1024 tokens apart a gate's gradient is a sum of differences a - b of two dots, tied at
+    both ends.  A dot goes through about twelve roundings, each 2^-24 / sqrt(3) of it in the mean square, 2^-23 in
+    all; a sum of n such differences that ends where it should is off by sqrt(2) sqrt(n / 6) of that in the mean.
+    With fp32 operands the matrix instruction adds one product after the other, so that a sum of 128 goes through
+    128 roundings of its parts so far, whose mean squares are i / 128 of one of the whole: 64 of those for the
+    scores and 64 for what is made with the state, 140 in place of 12."""
+    x = inputs(2, 4096, 2, 4, 128, 128, dtype, seed=11)
+    do = torch.randn(x["v"].shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(12)).to(dtype)
+    want = exact(x, do)[2:]
+    got = gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, segment_chunks=16)
+    d = (got[3].double() - want[3]).norm().item()
+    tol = 2.0 ** -24 * math.sqrt((12 if dtype == BF else 140) / 3) * math.sqrt(2 * 1024 / 6) * want[5]
+    assert d <= tol, "%.3g of %.3g" % (d, tol)
