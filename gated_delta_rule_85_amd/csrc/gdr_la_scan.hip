@@ -153,7 +153,7 @@ template <typename In, int KD, int NP, int NW, int KS, bool OUT> struct Lay {
     static constexpr int OFF_P = NB * BUF;                           // P of two chunks
     static constexpr int OFF_S = OFF_P + (OUT ? 2 * PT : 0);         // dots of two chunks: [wave][token]
     static constexpr int OFF_T = OFF_S + (OUT ? 2 * NW * CH * 4 : 0);  // gate tables of two chunks (without output: of each wave)
-    static constexpr int GT = OUT ? 15 * CH + 4 : 3 * CH;            // floats of one
+    static constexpr int GT = (OUT ? 8 : 3) * CH;                    // floats of one
     static constexpr int OFF_G = OFF_T + (OUT ? 2 : NW) * GT * 4;    // gates of four chunks
     static constexpr int OFF_X = OFF_G + 4 * CH * 4;                 // of two chunks: what a wave adds to its partner's rows
     static constexpr int BYTES = OFF_X + (KS > 1 ? 2 * NW * 2048 : 0);
@@ -167,10 +167,10 @@ template <typename In, int KD, int NP, int NW, int KS, bool OUT> struct Lay {
 // sum of gates that lie between the two alone, never a difference of longer sums: one gate that
 // empties the state is -150 here, and a difference of sums past it would keep their rounding, 2^-17.
 // Key and row in different tiles of 16: the row's part, from the start of its tile, and the key's,
-// to the end of its tile and of d - 1 tiles more for a row tile d tiles on.  In the same tile but in
-// different fours of it the same of fours.  In the same four: summed for the pair (G_PAIR, by row and
-// key), no part of the row's (G_ZERO).
-enum { G_START = 0, G_OUT = CH, G_END = 2 * CH, G_ROW = 3 * CH, G_KEY = 4 * CH, G_ROW4 = 7 * CH, G_KEY4 = 8 * CH, G_PAIR = 11 * CH, G_ZERO = 15 * CH };
+// to the end of its tile and of d - 1 tiles more for a row tile d tiles on.  In the same tile the
+// wave adds the gates itself (between(); a prompt of 4096 tokens of 32 heads, unsplit, in 141 us, with
+// tables of such sums in 149).
+enum { G_START = 0, G_OUT = CH, G_END = 2 * CH, G_ROW = 3 * CH, G_GATE = 4 * CH, G_KEY = 5 * CH };
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // one row's gate per lane (0 past the chunk's n rows and before its sequence's first gate) -> the table;
@@ -199,23 +199,23 @@ template <bool PAIRS> __device__ __forceinline__ void gate_table(float gate, int
     t[G_END + l] = l < n ? in_scale * exp2_fast(rest + after) : 0.f;
     if (!PAIRS) return;
     t[G_ROW + l] = x;
+    t[G_GATE + l] = gate;
     t[G_KEY + l] = rest;
     t[G_KEY + CH + l] = rest + next;
     t[G_KEY + 2 * CH + l] = rest + (next + next2);
-    // a four's gates 1 .. 3: up to this lane's, and after it
-    const int at = l & 3;
-    const float q1 = dpp_mov<0x55>(gate), q2 = dpp_mov<0xAA>(gate), q3 = dpp_mov<0xFF>(gate);  // quad_perm [i, i, i, i]
-    const float to1 = at >= 1 ? q1 : 0.f, to2 = at >= 2 ? q2 : 0.f, to3 = at >= 3 ? q3 : 0.f;
-    const float to = (to1 + to2) + to3, row4 = dpp_mov<0x00>(gate) + to;
-    const float rest4 = (at < 1 ? q1 : 0.f) + (at < 2 ? q2 : 0.f) + (at < 3 ? q3 : 0.f);
-    const float four = dpp_mov<0xFF>(row4);  // all four
-    const float four1 = dpp_mov<0x104>(four), four2 = dpp_mov<0x108>(four);  // those after it, in the tile
-    t[G_ROW4 + l] = row4;
-    t[G_KEY4 + l] = rest4;
-    t[G_KEY4 + CH + l] = rest4 + four1;
-    t[G_KEY4 + 2 * CH + l] = rest4 + (four1 + four2);
-    *reinterpret_cast<f32x4 *>(t + G_PAIR + 4 * l) = f32x4{to, to2 + to3, to3, 0.f};
-    if (l == 0) t[G_ZERO] = 0.f;
+}
+
+// Sums of a tile's gates from after key 4g + i to row n16, where i is not past it: of the lane's own
+// gate, over the 16 lanes with the same g, and of those of its keys
+__device__ __forceinline__ f32x4 between(float row, const f32x4 &keys) {
+    const int after = ln16() - 4 * lg4();  // of key 4g
+    float x = after > 3 ? row : 0.f;
+    x += dpp_mov<0x111>(x);
+    x += dpp_mov<0x112>(x);
+    x += dpp_mov<0x114>(x);
+    x += dpp_mov<0x118>(x);
+    const float x2 = x + (after > 2 ? keys[3] : 0.f), x1 = x2 + (after > 1 ? keys[2] : 0.f);
+    return f32x4{x1 + (after > 0 ? keys[1] : 0.f), x1, x2, x};
 }
 
 // Sums of four values over the lanes with the same l & 15: of value [0, 2, 1, 3][l >> 4]
@@ -489,19 +489,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
         f32x4 key[N];
         float row[N];
     };
-    // where a lane finds the parts of its logarithms in a table, for one tile: made once
-    struct Logs {
-        int key, row;
-    };
-    __device__ __forceinline__ Logs logs(int rt, int kt) const {
-        const int d = rt - kt, row = 16 * rt + n16, key = 16 * kt + 4 * g, fours = (n16 >> 2) - g;
-        // (a key in a later four of the tile than the row: masked)
-        Logs x = {d ? G_KEY + (d - 1) * CH + key : fours > 0 ? G_KEY4 + (fours - 1) * CH + key : G_PAIR + 4 * row,
-                  d ? G_ROW + row : fours > 0 ? G_ROW4 + row : G_ZERO};
-        asm("" : "+v"(x.key), "+v"(x.row));  // (kept in registers: made again in every chunk, 4 x 4096 tokens took 1% longer)
-        return x;
-    }
-    template <int N> __device__ __forceinline__ Scores<N> score_operands(const char *b, const float *gt, int rt, int kt, const Logs (&at)[N]) const {
+    template <int N> __device__ __forceinline__ Scores<N> score_operands(const char *b, const float *gt, int rt, int kt) const {
         Scores<N> x;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -511,8 +499,9 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x.key[i] = *reinterpret_cast<const f32x4 *>(gt + at[i].key);
-            x.row[i] = gt[at[i].row];
+            const int d = rt - kt - i;
+            x.key[i] = *reinterpret_cast<const f32x4 *>(gt + (d ? G_KEY + (d - 1) * CH : G_GATE) + 16 * (kt + i) + 4 * g);
+            x.row[i] = gt[(d ? G_ROW : G_GATE) + 16 * rt + n16];
         }
         return x;
     }
@@ -527,9 +516,14 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
         const float scale = J.in_scale * J.out_scale;
 #pragma unroll
         for (int i = 0; i < N; ++i) {  // s[i][k]: row 16 rt + n16, key 16 (kt + i) + 4g + k
+            const bool same = rt == kt + i;
+            f32x4 log;
+            if (same)
+                log = between(x.row[i], x.key[i]);
+            else
+                log = x.row[i] + x.key[i];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                s[i][k] = rt != kt + i || 4 * g + k <= n16 ? s[i][k] * (scale * exp2_fast(x.row[i] + x.key[i][k])) : 0.f;
+            for (int k = 0; k < 4; ++k) s[i][k] = !same || 4 * g + k <= n16 ? s[i][k] * (scale * exp2_fast(log[k])) : 0.f;
             char *to = P + SP::off(16 * rt + n16, (16 * (kt + i) + 4 * g) * ES);
             if constexpr (Y::BF) {
                 bf16x4 y[NP];
@@ -675,15 +669,12 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
             o0 += o_step;
         };
         constexpr bool TIGHT = NP == 3 || !Y::BF;  // registers for a step less of P
-        // this wave's tiles of P: NT of one row tile and, for two waves, one more
+        // this wave's tiles of P: NT of one row tile and, for two waves (of eight: two without gates to add), one more
         constexpr int NT = NW == 8 ? 1 : 2;
-        const int rt = NW == 8 ? (w < 4 ? 3 : w == 5 ? 1 : w == 7 ? 0 : 2) : w < 2 ? 3 : 4 - w;
-        const int kt = NW == 8 ? (w < 4 ? w : w == 6 ? 2 : 0) : w == 1 ? 2 : 0;
-        const int more_rt = NW == 8 ? (w == 4 ? 2 : w == 5 ? 1 : -1) : w == 2 ? 2 : w == 3 ? 0 : -1;
+        const int rt = NW == 8 ? (w == 0 || w == 6 ? 1 : w == 2 || w == 4 ? 2 : w == 7 ? 0 : 3) : w < 2 ? 3 : 4 - w;
+        const int kt = NW == 8 ? (w == 1 || w == 2 ? 2 : w == 3 ? 3 : w == 6 ? 1 : 0) : w == 1 ? 2 : 0;
+        const int more_rt = NW == 8 ? (w == 4 ? 2 : w == 5 ? 3 : -1) : w == 2 ? 2 : w == 3 ? 0 : -1;
         const int more_kt = NW == 8 ? 1 : w == 2 ? 2 : 0;
-        Logs at_tiles[NT], at_more[1] = {logs(max(more_rt, 0), more_rt < 0 ? 0 : more_kt)};
-#pragma unroll
-        for (int i = 0; i < NT; ++i) at_tiles[i] = logs(rt, kt + i);
         // the waves that make the gate tables and add up the dots: on SIMDs whose waves have one tile each
         constexpr int GATES = NW == 8 ? 3 : 0, SUMS = NW == 8 ? 2 : 1;
         first_copies(from, w == GATES);
@@ -707,7 +698,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
                 add_first(p0);
                 stage();
             }
-            const Scores<NT> sc = score_operands<NT>(b, gt, rt, kt, at_tiles);
+            const Scores<NT> sc = score_operands<NT>(b, gt, rt, kt);
             if (!TIGHT) add_first(p0);
             add_rest(p1);
             if (it > 0) finish(it - 1, buf ^ 1);
@@ -759,7 +750,7 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
             for (int r = 0; r < 4; ++r) o[r] *= out[r];
             give(buf);
             add_chunk(b, gt, v, ends_here, k0, h);
-            if (more_rt >= 0) score<1>(score_operands<1>(b, gt, more_rt, more_kt, at_more), P, more_rt, more_kt);
+            if (more_rt >= 0) score<1>(score_operands<1>(b, gt, more_rt, more_kt), P, more_rt, more_kt);
             if (w == GATES) {
                 if (it + 1 < n_it) make_table(it + 1, table(buf ^ 1));
                 if (it + 2 < n_it) issue_gates(it + 2);
