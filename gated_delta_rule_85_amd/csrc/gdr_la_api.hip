@@ -24,8 +24,8 @@ bool wide(int32_t dtype, int64_t units) { return dtype == GDR_BF16 && units >= U
 // compute unit (4.4 us): a chunk of 64 columns takes 0.6 (backwards 0.7), one without output 0.5 of a
 // workgroup that shares its compute unit; a workgroup's start 1 to 3, the launches and the carry
 // between the two 3 and what the segments' states take.  Prefill of one sequence of 4096 tokens (32
-// heads of 128 columns) takes 71 us split, 150 unsplit; backwards, 4 x 2048 tokens of 32 heads 400 us
-// with segments of 16 and 442 unsplit.
+// heads of 128 columns) takes 68 us split, 141 unsplit; backwards, 4 x 2048 tokens of 32 heads 421 us
+// with segments of 16 and 473 unsplit.
 // Of packed sequences the lengths are not known here: the time of one with all the tokens counts as much
 // as that of half of them with twice the mean length.
 int64_t split_chunks(int32_t dtype, int64_t N, int64_t n_seq, bool packed, int64_t heads, int64_t blocks, int64_t scans,

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void gdr_la_carry_kernel(LaCarry p) {
 // cancel from one token to the next, so that they are added in 64 bits from the far end, anew in every
 // segment of 16 chunks at most; what is then missing at the near end is the sum of all errors, and
 // each token gets its share of it, by the sizes of the terms: the squares of all terms from the far end to it,
-// of all of the segment's (8 x 4096 tokens of 64 heads: 1.4e-6 off, without it 2.1e-6; segments of 8 chunks: 1.0e-6, and 3% longer).
+// of all of the segment's (8 x 4096 tokens of 64 heads: 9.7e-7 off, without it 1.7e-6; segments of 8 chunks: 6.8e-7, and 3% longer).
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
     for (int i = 32; i; i >>= 1) x += __shfl_xor(x, i);

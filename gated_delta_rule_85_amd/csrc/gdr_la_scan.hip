@@ -16,13 +16,13 @@
 // unit, else 4.  Where the LDS has room (KS 2: bf16 in and out, no dots), 8 waves take these 64 columns
 // too, in pairs with half of the rows of S each, so that a SIMD has two waves: a wave's part of Q h
 // for its partner's rows of the chunk goes through LDS (16 KB a chunk), and P V is split by those
-// rows.  Two prompts of 8 heads of 64 columns, 2048 tokens: 73 us in place of 87; 4 x 4096 tokens of
-// 32 heads of 128: 170 in place of 183.
+// rows.  Two prompts of 8 heads of 64 columns, 2048 tokens: 72 us in place of 89; 4 x 4096 tokens of
+// 32 heads of 128: 167 in place of 185.
 //
 // Bound by the issue of instructions and the chain of a chunk's steps, at two waves a SIMD: some wave issues in
-// 62% of the SIMDs' cycles (pairs: 76%), matrix units are busy in 37% (30%), the LDS in 34% (37%).
-// 8 x 4096 tokens of 64 heads, bf16: 555 us, 0.8 PFLOP/s of matrix instructions; the backward's scans
-// with their dots and three pieces 800 and 770 us, dk with two 590.
+// 62% of the SIMDs' cycles (pairs: 77%), matrix units are busy in 37% (30%), the LDS in 34% (37%).
+// 8 x 4096 tokens of 64 heads, bf16: 528 us, 0.8 PFLOP/s of matrix instructions; the backward's scans
+// with their dots and three pieces 740 and 725 us, dk with two 565.
 //
 // rev: row r of a chunk is its r-th token from the end, and a row's gate is the next token's, so
 // that the same code scans from the last token to the first.

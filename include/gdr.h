@@ -325,9 +325,10 @@ typedef struct {
        y = n * weight + bias,   out = y * act(gate),   or   act(y) without a gate.
 
    With one group per head it is the norm on the operators' output.  Rows of out, dout, dx and
-   dgate are contiguous; base pointers at multiples of 16 bytes and rows at multiples of 8 elements
-   are read and written in pieces of 16 bytes where the group width is a multiple of 8, others
-   channel by channel.  out may be x or gate where their types and rows are alike. */
+   dgate are contiguous.  Where all base pointers are at multiples of 16 bytes, and C and the rows'
+   distances multiples of 8, rows are read and written in pieces of 8 channels, whatever the group
+   width (8187, 8189, 8190 and 8191 excepted); else channel by channel.  out may be x or gate where
+   their types and rows are alike. */
 typedef struct {
     int64_t M, C, groups;
     int64_t x_row, gate_row; /* elements between tokens */
