@@ -701,3 +701,30 @@ def test_gate_gradients_over_long_segments(gdr, dtype):
     d = (got[3].double() - want[3]).norm().item()
     tol = 2.0 ** -24 * math.sqrt((12 if dtype == BF else 140) / 3) * math.sqrt(2 * 1024 / 6) * want[5]
     assert d <= tol, "%.3g of %.3g" % (d, tol)
+
+
+@pytest.mark.parametrize("N", [5, 80])
+def test_replays_read_the_offsets_again(gdr, N):
+    """Captured with one batch's offsets, replayed with others' in the same tensor, some of them falling."""
+    T, K, V = 2000, 64, 128
+    x = inputs(1, T, 1, 2, K, V, BF)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    do = torch.randn(1, T, 2, V, device="cuda", generator=gen).to(BF)
+    h0, dht = (torch.randn(N, 2, K, V, device="cuda", generator=gen) for _ in range(2))
+    cu = torch.linspace(0, T, N + 1).int().cuda()
+
+    def both():
+        o, hT = gdr.chunk_linear_attention_fwd(x["q"], x["k"], x["v"], x["g"], None, h0, cu, segment_chunks=3)
+        return (o, hT, *gdr.chunk_linear_attention_bwd(x["q"], x["k"], x["v"], x["g"], do, dht, None, h0, cu, segment_chunks=3))
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = both()
+    for seed in range(4):
+        new = torch.randint(-10, T + 10, (N + 1,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32)
+        cu.copy_(new if seed == 3 else new.sort()[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(both(), kept))
