@@ -671,8 +671,8 @@ template <typename In, typename Out, int KD, int NP, int NW, int KS, bool DOTS> 
         constexpr bool TIGHT = NP == 3 || !Y::BF;  // registers for a step less of P
         // this wave's tiles of P: NT of one row tile and, for two waves (of eight: two without gates to add), one more
         constexpr int NT = NW == 8 ? 1 : 2;
-        const int rt = NW == 8 ? (w == 0 || w == 6 ? 1 : w == 2 || w == 4 ? 2 : w == 7 ? 0 : 3) : w < 2 ? 3 : 4 - w;
-        const int kt = NW == 8 ? (w == 1 || w == 2 ? 2 : w == 3 ? 3 : w == 6 ? 1 : 0) : w == 1 ? 2 : 0;
+        const int rt = NW == 8 ? (w == 0 || w == 6 ? 1 : w == 2 || w == 4 ? 2 : w == 7 ? 0 : 3) : w == 1 ? 1 : w == 2 ? 2 : 3;
+        const int kt = NW == 8 ? (w == 1 || w == 2 ? 2 : w == 3 ? 3 : w == 6 ? 1 : 0) : w == 0 ? 2 : 0;
         const int more_rt = NW == 8 ? (w == 4 ? 2 : w == 5 ? 3 : -1) : w == 2 ? 2 : w == 3 ? 0 : -1;
         const int more_kt = NW == 8 ? 1 : w == 2 ? 2 : 0;
         // the waves that make the gate tables and add up the dots: on SIMDs whose waves have one tile each
