@@ -210,10 +210,13 @@ __global__ __launch_bounds__(256) void gdr_la_heads_kernel(const float *x, Out *
 // ------------------------------------------------------------------ la_rest
 // Rows before the first and behind the last of the packed sequences := 0.  (4 us where there are none.)
 __global__ __launch_bounds__(256) void gdr_la_rest_kernel(LaRest p) {
-    int64_t first = 0, end = 0, at;
-    if (p.s.n_seq > 0) {
-        la_bounds(p.s, 0, first, at);
-        la_bounds(p.s, p.s.n_seq - 1, at, end);
+    int64_t first = 0, end = 0;
+    if (p.s.n_seq > LA_WAVE_SEQS) {
+        first = p.s.cu[0], end = p.s.cu[p.s.n_seq];
+    } else if (p.s.n_seq > 0) {
+        const int starts = la_starts(p.s);
+        first = __builtin_amdgcn_readlane(starts, 0);
+        end = max(__builtin_amdgcn_readlane(starts, 63), la_offset(p.s.cu, p.s.T, p.s.n_seq));
     }
     for (int64_t i = blockIdx.x; i < first + p.s.T - end; i += gridDim.x) {
         const int64_t row = i < first ? i : end + i - first;
